@@ -50,6 +50,16 @@
  *                                   stream (default priority), each chunk
  *                                   overlapping the steps of the chunk before
  *                                   (off by default: measured no faster)
+ *       RNN_SCAN_CHUNK=n            the selective scan's time axis in chunks of
+ *                                   n steps (rounded up to whole tiles; above
+ *                                   the length: one chunk), read by
+ *                                   rnn_scan_create
+ *
+ * Beside the recurrent layers: the operators of a selective state space block
+ * (rnn_conv_*: the short causal convolution; rnn_scan_*: the selective scan;
+ * both for prompts and for single tokens) and layer normalization
+ * (rnn_norm_*), each with its gradient.  Their section below says where their
+ * conventions differ.
  */
 #ifndef ONNX_RNN_MI355X_H
 #define ONNX_RNN_MI355X_H
@@ -76,7 +86,9 @@ typedef enum {
 } rnn_status;
 
 typedef enum { RNN_CELL_RNN = 0, RNN_CELL_GRU = 1, RNN_CELL_LSTM = 2 } rnn_cell;
-typedef enum { RNN_DTYPE_F32 = 0, RNN_DTYPE_F16 = 1 } rnn_dtype;
+/* (BF16: the state space operators and layer normalization below; the
+ * recurrent layers take F32 and F16.) */
+typedef enum { RNN_DTYPE_F32 = 0, RNN_DTYPE_F16 = 1, RNN_DTYPE_BF16 = 2 } rnn_dtype;
 typedef enum { RNN_DIR_FORWARD = 0, RNN_DIR_REVERSE = 1, RNN_DIR_BIDIRECTIONAL = 2 } rnn_direction;
 
 /* The eleven ONNX activations (operator definitions):
@@ -302,8 +314,195 @@ typedef struct {
 } rnn_run_status;
 int rnn_read_run_status(const rnn_problem* problem, const void* state_scratch, void* stream, rnn_run_status* out);
 
+/* ---------------------------------------------------------------------------
+ * Operators of a selective state space block, and layer normalization.
+ *
+ * Manner: as the recurrent layers -- a description is validated into an
+ * immutable problem, scratch is the caller's, an encode call checks everything
+ * before it enqueues anything, allocates nothing, synchronises nothing, and
+ * gives bit-identical results on every run (no atomics; sums in a fixed
+ * order).  One problem may be used from many threads and streams at once, each
+ * call with scratch of its own.  A call runs on its stream's device (a NULL
+ * stream: on the current device).  Calls may be captured into a HIP graph.
+ *
+ * Types: "tensor type" is the description's dtype (f32, f16 or bf16); A, D,
+ * delta_bias, the scan's states and every gradient of a parameter are f32.
+ * Arithmetic, sums and states are f32; an output of the tensor type is rounded
+ * to nearest even once.
+ *
+ * Rows.  A sequence tensor (rnn_rows) has one row for each position: row
+ * t*batch + b in layout 0 ([S,B,n]), b*seq + t in layout 1 ([B,S,n]).  Row r
+ * begins row_stride * r elements after elem_offset, so that a slice of a wider
+ * projection is read or written in place; row_stride 0 means packed rows.
+ * Elements of a row are contiguous.  Nothing between the rows is touched.
+ *
+ * Steps.  Batch row b takes len_b steps (sequence_lens, values below 0 act as
+ * 0, above seq as seq; seq when absent); step s reads time s, or len_b - 1 - s
+ * in the reverse direction.  Past a row's length inputs are not read, and
+ * row outputs (Y, dX, ddelta, dZ, dB, dC) are zero.  A row of no steps ends in
+ * the state that it began with.  (The recurrent layers' Y_h of such a row is
+ * zero instead.)  A single token is seq = 1; a state may be updated in place:
+ * final_state may be the very buffer of initial_state.  Apart from that no
+ * output may overlap an input or another output.
+ *
+ * Limits (RNN_ERR_UNSUPPORTED): channels above 2^24, batch or seq above 2^30,
+ * a grid above 2^31 - 1 workgroups.  A tensor or a scratch above 2^52 bytes is
+ * RNN_ERR_SHAPE. */
+typedef struct {
+  void* ptr;           /* device pointer, or NULL for an absent tensor */
+  int64_t elem_offset; /* >= 0, in elements of the tensor's type */
+  int64_t row_stride;  /* elements from one row to the next, >= the row's length; 0: packed */
+} rnn_rows;
+
+/* Short causal convolution, one filter a channel (depthwise):
+ *   p_s[c] = B[c] + sum_{k < width} W[c,k] * x_{s - (width-1) + k}[c]
+ *   y_s    = p_s, or p_s * sigmoid(p_s) with silu = 1
+ * over the steps s of a row; x_{-1}, x_{-2}, ... come from initial_state, whose
+ * entry j is x_{j - (width-1)} (zeros when absent).  final_state holds the last
+ * width-1 inputs of the row in the same order. */
+typedef struct {
+  int32_t dtype;      /* rnn_dtype */
+  int32_t direction;  /* RNN_DIR_FORWARD or RNN_DIR_REVERSE */
+  int32_t layout;     /* 0 or 1 */
+  int32_t silu;       /* 0 or 1 */
+  int64_t seq;        /* S >= 0 */
+  int64_t batch;      /* B >= 0 */
+  int64_t channels;   /* C >= 1 */
+  int64_t width;      /* taps, 2 to 8 (others: RNN_ERR_UNSUPPORTED) */
+} rnn_conv_desc;
+
+typedef struct rnn_conv rnn_conv;
+
+typedef struct {
+  rnn_rows X;                /* [C] a row                            required */
+  rnn_tensor W;              /* [C, width]                           required */
+  rnn_tensor B;              /* [C]                                  optional (zeros) */
+  rnn_tensor sequence_lens;  /* [batch] int32                        optional (all seq) */
+  rnn_tensor initial_state;  /* [batch, width-1, C] tensor type      optional (zeros) */
+  rnn_rows Y;                /* [C] a row                            optional output (forward only) */
+  rnn_tensor final_state;    /* as initial_state                     optional output (forward only) */
+} rnn_conv_operands;
+
+/* Gradients of the convolution's outputs (inputs of the backward pass) and of
+ * its inputs.  p is computed again from X. */
+typedef struct {
+  rnn_rows dY;                 /* [C] a row                          required */
+  rnn_tensor d_final_state;    /* as final_state                     optional (zeros) */
+  rnn_rows dX;                 /* [C] a row                          optional output */
+  rnn_tensor dW;               /* [C, width] f32                     optional output */
+  rnn_tensor dB;               /* [C] f32                            optional output */
+  rnn_tensor d_initial_state;  /* as initial_state                   optional output; must not be d_final_state */
+} rnn_conv_gradients;
+
+int rnn_conv_create(const rnn_conv_desc* desc, rnn_conv** out);
+void rnn_conv_destroy(rnn_conv* conv);
+/* Scratch of rnn_conv_encode (always 0) and of rnn_conv_encode_backward;
+ * 256-byte aligned device memory. */
+int rnn_conv_scratch_size(const rnn_conv* conv, size_t* forward_bytes, size_t* backward_bytes);
+int rnn_conv_encode(const rnn_conv* conv, const rnn_conv_operands* operands, void* scratch, void* stream);
+int rnn_conv_encode_backward(const rnn_conv* conv, const rnn_conv_operands* operands,
+                             const rnn_conv_gradients* gradients, void* scratch, void* stream);
+
+/* Selective scan: a diagonal linear recurrence whose step size and input and
+ * output weights depend on the step,
+ *   d_s[c]   = softplus(delta_s[c] + delta_bias[c])   (delta_softplus = 1; else without softplus)
+ *   h_s[c,n] = exp(d_s[c] * A[c,n]) * h_{s-1}[c,n] + d_s[c] * x_s[c] * B_s[g,n]
+ *   y_s[c]   = sum_n C_s[g,n] * h_s[c,n] + D[c] * x_s[c]
+ *   Y_s[c]   = y_s[c], or y_s[c] * z_s[c] * sigmoid(z_s[c]) when Z is given
+ * with channel c in group g = c / (channels / groups). */
+typedef struct {
+  int32_t dtype;           /* rnn_dtype of the row tensors */
+  int32_t direction;       /* RNN_DIR_FORWARD or RNN_DIR_REVERSE */
+  int32_t layout;          /* 0 or 1 */
+  int32_t delta_softplus;  /* 0 or 1 */
+  int64_t seq;             /* S >= 0 */
+  int64_t batch;           /* B >= 0 */
+  int64_t channels;        /* C >= 1 */
+  int64_t state;           /* N, 1 to 128 (above: RNN_ERR_UNSUPPORTED) */
+  int64_t groups;          /* G >= 1, a divisor of channels */
+} rnn_scan_desc;
+
+typedef struct rnn_scan rnn_scan;
+
+typedef struct {
+  rnn_rows X;                /* [C] a row               required */
+  rnn_rows delta;            /* [C] a row               required */
+  rnn_tensor A;              /* [C, N] f32              required */
+  rnn_rows B;                /* [G*N] a row             required */
+  rnn_rows C;                /* [G*N] a row             required */
+  rnn_tensor D;              /* [C] f32                 optional (zeros) */
+  rnn_rows Z;                /* [C] a row               optional (no gate) */
+  rnn_tensor delta_bias;     /* [C] f32                 optional (zeros) */
+  rnn_tensor sequence_lens;  /* [batch] int32           optional (all seq) */
+  rnn_tensor initial_state;  /* [batch, C, N] f32       optional (zeros) */
+  rnn_rows Y;                /* [C] a row               optional output (forward only) */
+  rnn_tensor final_state;    /* [batch, C, N] f32       optional output (forward only) */
+} rnn_scan_operands;
+
+/* Gradients; states and y are computed again from the inputs.  dD needs D
+ * only in its use (it may be asked for without one), dZ needs Z. */
+typedef struct {
+  rnn_rows dY;                 /* [C] a row             required */
+  rnn_tensor d_final_state;    /* [batch, C, N] f32     optional (zeros) */
+  rnn_rows dX;                 /* [C] a row             optional outputs from here on */
+  rnn_rows ddelta;             /* [C] a row */
+  rnn_tensor dA;               /* [C, N] f32 */
+  rnn_rows dB;                 /* [G*N] a row */
+  rnn_rows dC;                 /* [G*N] a row */
+  rnn_tensor dD;               /* [C] f32 */
+  rnn_rows dZ;                 /* [C] a row */
+  rnn_tensor ddelta_bias;      /* [C] f32 */
+  rnn_tensor d_initial_state;  /* [batch, C, N] f32; must not be d_final_state */
+} rnn_scan_gradients;
+
+int rnn_scan_create(const rnn_scan_desc* desc, rnn_scan** out);
+void rnn_scan_destroy(rnn_scan* scan);
+/* Scratch of rnn_scan_encode and of rnn_scan_encode_backward (either may be
+ * 0); 256-byte aligned device memory. */
+int rnn_scan_scratch_size(const rnn_scan* scan, size_t* forward_bytes, size_t* backward_bytes);
+int rnn_scan_encode(const rnn_scan* scan, const rnn_scan_operands* operands, void* scratch, void* stream);
+int rnn_scan_encode_backward(const rnn_scan* scan, const rnn_scan_operands* operands,
+                             const rnn_scan_gradients* gradients, void* scratch, void* stream);
+
+/* Layer normalization over the last axis (the ONNX operator):
+ *   Mean = sum_i x_i / size;  InvStdDev = 1 / sqrt(sum_i (x_i - Mean)^2 / size + epsilon)
+ *   Y    = (x - Mean) * InvStdDev * Scale + B */
+typedef struct {
+  int32_t dtype;   /* rnn_dtype of X, Scale, B, Y and their row gradients */
+  float epsilon;   /* >= 0, finite */
+  int64_t rows;    /* >= 0, at most 2^30 */
+  int64_t size;    /* >= 1, at most 2^24 */
+} rnn_norm_desc;
+
+typedef struct rnn_norm rnn_norm;
+
+typedef struct {
+  rnn_rows X;             /* [size] a row           required */
+  rnn_tensor Scale;       /* [size]                 required */
+  rnn_tensor B;           /* [size]                 optional (zeros; not read by the backward pass) */
+  rnn_rows Y;             /* [size] a row           optional output (forward only) */
+  rnn_tensor Mean;        /* [rows] f32             optional output; the backward pass reads it: required there */
+  rnn_tensor InvStdDev;   /* [rows] f32             likewise */
+} rnn_norm_operands;
+
+typedef struct {
+  rnn_rows dY;        /* [size] a row               required */
+  rnn_rows dX;        /* [size] a row               optional output */
+  rnn_tensor dScale;  /* [size] f32                 optional output */
+  rnn_tensor dB;      /* [size] f32                 optional output */
+} rnn_norm_gradients;
+
+int rnn_norm_create(const rnn_norm_desc* desc, rnn_norm** out);
+void rnn_norm_destroy(rnn_norm* norm);
+/* Scratch of rnn_norm_encode (always 0) and of rnn_norm_encode_backward;
+ * 256-byte aligned device memory. */
+int rnn_norm_scratch_size(const rnn_norm* norm, size_t* forward_bytes, size_t* backward_bytes);
+int rnn_norm_encode(const rnn_norm* norm, const rnn_norm_operands* operands, void* scratch, void* stream);
+int rnn_norm_encode_backward(const rnn_norm* norm, const rnn_norm_operands* operands,
+                             const rnn_norm_gradients* gradients, void* scratch, void* stream);
+
 /* Message of the last failed call on this thread ("" if none): the cell
- * (LSTM, GRU or RNN) and the argument at fault, as the page's shape
+ * (LSTM, GRU or RNN) or operator (conv, scan or layer norm) and the argument at fault, as the page's shape
  * exception names them ("Scratch").  The string is owned by the library and
  * valid until the thread's next call. */
 const char* rnn_last_error(void);

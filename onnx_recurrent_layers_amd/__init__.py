@@ -1,4 +1,5 @@
-"""ONNX recurrent layers (RNN, GRU, LSTM) on MI355X (gfx950).
+"""ONNX recurrent layers (RNN, GRU, LSTM) on MI355X (gfx950), and the operators
+of a selective state space block with layer normalization.
 
 A thin ctypes binding over the C ABI of ``include/rnn.h`` (library
 ``librnn_mi355x.so``, built in-tree by ``onnx_recurrent_layers_amd.build``).
@@ -17,7 +18,7 @@ LIB_PATH = os.path.join(HERE, "librnn_mi355x.so")
 
 RNN_OK, RNN_ERR_ARG, RNN_ERR_SHAPE, RNN_ERR_UNSUPPORTED, RNN_ERR_HIP = range(5)
 CELLS = {"RNN": 0, "GRU": 1, "LSTM": 2}
-DTYPES = {"f32": 0, "f16": 1}
+DTYPES = {"f32": 0, "f16": 1, "bf16": 2}   # (bf16: the operators beside the recurrent layers)
 DIRECTIONS = {"forward": 0, "reverse": 1, "bidirectional": 2}
 ACTIVATIONS = {
     "Relu": 0, "Tanh": 1, "Sigmoid": 2, "Affine": 3, "LeakyRelu": 4, "ThresholdedRelu": 5,
@@ -72,6 +73,58 @@ class rnn_plan_info(ctypes.Structure):
                 ("xw_chunk_steps", ctypes.c_int32), ("xw_slots", ctypes.c_int32)]
 
 
+class rnn_rows(ctypes.Structure):
+    _fields_ = [("ptr", ctypes.c_void_p), ("elem_offset", ctypes.c_int64), ("row_stride", ctypes.c_int64)]
+
+
+class rnn_conv_desc(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("direction", ctypes.c_int32), ("layout", ctypes.c_int32),
+                ("silu", ctypes.c_int32), ("seq", ctypes.c_int64), ("batch", ctypes.c_int64),
+                ("channels", ctypes.c_int64), ("width", ctypes.c_int64)]
+
+
+class rnn_conv_operands(ctypes.Structure):
+    _fields_ = [("X", rnn_rows), ("W", rnn_tensor), ("B", rnn_tensor), ("sequence_lens", rnn_tensor),
+                ("initial_state", rnn_tensor), ("Y", rnn_rows), ("final_state", rnn_tensor)]
+
+
+class rnn_conv_gradients(ctypes.Structure):
+    _fields_ = [("dY", rnn_rows), ("d_final_state", rnn_tensor), ("dX", rnn_rows), ("dW", rnn_tensor),
+                ("dB", rnn_tensor), ("d_initial_state", rnn_tensor)]
+
+
+class rnn_scan_desc(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("direction", ctypes.c_int32), ("layout", ctypes.c_int32),
+                ("delta_softplus", ctypes.c_int32), ("seq", ctypes.c_int64), ("batch", ctypes.c_int64),
+                ("channels", ctypes.c_int64), ("state", ctypes.c_int64), ("groups", ctypes.c_int64)]
+
+
+class rnn_scan_operands(ctypes.Structure):
+    _fields_ = [("X", rnn_rows), ("delta", rnn_rows), ("A", rnn_tensor), ("B", rnn_rows), ("C", rnn_rows),
+                ("D", rnn_tensor), ("Z", rnn_rows), ("delta_bias", rnn_tensor), ("sequence_lens", rnn_tensor),
+                ("initial_state", rnn_tensor), ("Y", rnn_rows), ("final_state", rnn_tensor)]
+
+
+class rnn_scan_gradients(ctypes.Structure):
+    _fields_ = [("dY", rnn_rows), ("d_final_state", rnn_tensor), ("dX", rnn_rows), ("ddelta", rnn_rows),
+                ("dA", rnn_tensor), ("dB", rnn_rows), ("dC", rnn_rows), ("dD", rnn_tensor), ("dZ", rnn_rows),
+                ("ddelta_bias", rnn_tensor), ("d_initial_state", rnn_tensor)]
+
+
+class rnn_norm_desc(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("epsilon", ctypes.c_float), ("rows", ctypes.c_int64),
+                ("size", ctypes.c_int64)]
+
+
+class rnn_norm_operands(ctypes.Structure):
+    _fields_ = [("X", rnn_rows), ("Scale", rnn_tensor), ("B", rnn_tensor), ("Y", rnn_rows), ("Mean", rnn_tensor),
+                ("InvStdDev", rnn_tensor)]
+
+
+class rnn_norm_gradients(ctypes.Structure):
+    _fields_ = [("dY", rnn_rows), ("dX", rnn_rows), ("dScale", rnn_tensor), ("dB", rnn_tensor)]
+
+
 # rnn_products: which arithmetic units carry a stage's products
 PRODUCTS = {0: "f32 vector ALU", 1: "f32 matrix cores", 2: "f16 matrix cores", 3: "bf16x3 matrix cores"}
 
@@ -113,6 +166,18 @@ def load_library(path: str = LIB_PATH):
     lib.rnn_encode_noalloc.restype = ctypes.c_int
     lib.rnn_read_run_status.argtypes = [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, P(rnn_run_status)]
     lib.rnn_read_run_status.restype = ctypes.c_int
+    for op, desc, operands, gradients in (("conv", rnn_conv_desc, rnn_conv_operands, rnn_conv_gradients),
+                                          ("scan", rnn_scan_desc, rnn_scan_operands, rnn_scan_gradients),
+                                          ("norm", rnn_norm_desc, rnn_norm_operands, rnn_norm_gradients)):
+        def declare(name, restype, *argtypes):
+            f = getattr(lib, f"rnn_{op}_{name}")
+            f.argtypes, f.restype = list(argtypes), restype
+        declare("create", ctypes.c_int, P(desc), P(ctypes.c_void_p))
+        declare("destroy", None, ctypes.c_void_p)
+        declare("scratch_size", ctypes.c_int, ctypes.c_void_p, P(ctypes.c_size_t), P(ctypes.c_size_t))
+        declare("encode", ctypes.c_int, ctypes.c_void_p, P(operands), ctypes.c_void_p, ctypes.c_void_p)
+        declare("encode_backward", ctypes.c_int, ctypes.c_void_p, P(operands), P(gradients), ctypes.c_void_p,
+                ctypes.c_void_p)
     lib.rnn_last_error.argtypes = []
     lib.rnn_last_error.restype = ctypes.c_char_p
     _lib = lib
@@ -275,6 +340,291 @@ class Layer:
                 self.handle = None
         except Exception:
             pass
+
+
+# ---- the operators of a state space block, and layer normalization
+
+def _create(name: str, desc) -> ctypes.c_void_p:
+    h = ctypes.c_void_p()
+    _check(getattr(load_library(), name)(ctypes.byref(desc), ctypes.byref(h)))
+    return h
+
+
+def _scratch(name: str, handle):
+    forward, backward = ctypes.c_size_t(), ctypes.c_size_t()
+    _check(getattr(load_library(), name)(handle, ctypes.byref(forward), ctypes.byref(backward)))
+    return forward.value, backward.value
+
+
+def rnn_conv_create(desc: rnn_conv_desc) -> ctypes.c_void_p:
+    return _create("rnn_conv_create", desc)
+
+
+def rnn_conv_destroy(handle) -> None:
+    load_library().rnn_conv_destroy(handle)
+
+
+def rnn_conv_scratch_size(handle):
+    return _scratch("rnn_conv_scratch_size", handle)
+
+
+def rnn_conv_encode(handle, operands: rnn_conv_operands, scratch_ptr: int = 0, stream_ptr: int = 0) -> None:
+    _check(load_library().rnn_conv_encode(handle, operands, scratch_ptr or None, stream_ptr or None))
+
+
+def rnn_conv_encode_backward(handle, operands: rnn_conv_operands, gradients: rnn_conv_gradients, scratch_ptr: int = 0,
+                             stream_ptr: int = 0) -> None:
+    _check(load_library().rnn_conv_encode_backward(handle, operands, gradients, scratch_ptr or None,
+                                                   stream_ptr or None))
+
+
+def rnn_scan_create(desc: rnn_scan_desc) -> ctypes.c_void_p:
+    return _create("rnn_scan_create", desc)
+
+
+def rnn_scan_destroy(handle) -> None:
+    load_library().rnn_scan_destroy(handle)
+
+
+def rnn_scan_scratch_size(handle):
+    return _scratch("rnn_scan_scratch_size", handle)
+
+
+def rnn_scan_encode(handle, operands: rnn_scan_operands, scratch_ptr: int = 0, stream_ptr: int = 0) -> None:
+    _check(load_library().rnn_scan_encode(handle, operands, scratch_ptr or None, stream_ptr or None))
+
+
+def rnn_scan_encode_backward(handle, operands: rnn_scan_operands, gradients: rnn_scan_gradients, scratch_ptr: int = 0,
+                             stream_ptr: int = 0) -> None:
+    _check(load_library().rnn_scan_encode_backward(handle, operands, gradients, scratch_ptr or None,
+                                                   stream_ptr or None))
+
+
+def rnn_norm_create(desc: rnn_norm_desc) -> ctypes.c_void_p:
+    return _create("rnn_norm_create", desc)
+
+
+def rnn_norm_destroy(handle) -> None:
+    load_library().rnn_norm_destroy(handle)
+
+
+def rnn_norm_scratch_size(handle):
+    return _scratch("rnn_norm_scratch_size", handle)
+
+
+def rnn_norm_encode(handle, operands: rnn_norm_operands, scratch_ptr: int = 0, stream_ptr: int = 0) -> None:
+    _check(load_library().rnn_norm_encode(handle, operands, scratch_ptr or None, stream_ptr or None))
+
+
+def rnn_norm_encode_backward(handle, operands: rnn_norm_operands, gradients: rnn_norm_gradients, scratch_ptr: int = 0,
+                             stream_ptr: int = 0) -> None:
+    _check(load_library().rnn_norm_encode_backward(handle, operands, gradients, scratch_ptr or None,
+                                                   stream_ptr or None))
+
+
+class _Operator:
+    """One created problem of the operators below plus its scratch, for repeated
+    calls.  The tensors of a call are torch tensors keyed by the C names; each
+    one's shape, type and device are checked.  Sequence tensors may be views
+    whose rows lie a constant stride apart (a slice of a wider projection); the
+    others have to be contiguous.  Calls that overlap in time need an object
+    each, since an object holds one scratch (so do graphs that replay at once)."""
+
+    op = ""             # the C functions' middle name
+    who = ""            # the name in messages
+    operand_names = ()
+    gradient_names = ()
+
+    def _open(self, desc, device, shapes):
+        import torch
+        self._handle = None
+        lib = load_library()
+        self._destroy = getattr(lib, f"rnn_{self.op}_destroy")
+        self._encode = getattr(lib, f"rnn_{self.op}_encode")
+        self._encode_backward = getattr(lib, f"rnn_{self.op}_encode_backward")
+        self._handle = _create(f"rnn_{self.op}_create", desc)
+        self.forward_bytes, self.backward_bytes = _scratch(f"rnn_{self.op}_scratch_size", self._handle)
+        self.device = torch.device(device)
+        if self.device.index is None:
+            self.device = torch.device(self.device.type, torch.cuda.current_device())
+        self._index = self.device.index
+        # name -> (shape, torch type, row tensor)
+        self._specs = shapes(torch, {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}[self.dtype])
+        self._forward_scratch = self._backward_scratch = None
+        if self.forward_bytes:
+            self._forward_scratch = torch.empty(self.forward_bytes, dtype=torch.uint8, device=self.device)
+
+    def _bad(self, code, text):
+        return RnnError(code, f"{self.who}: {text}")
+
+    def _fill(self, struct, names, tensors):
+        specs = self._specs
+        for name in names:
+            t = tensors.get(name)
+            if t is None:
+                continue
+            shape, dtype, row = specs[name]
+            if t.shape != shape:
+                raise self._bad(RNN_ERR_SHAPE, f"{name}: shape {tuple(t.shape)}, expected {shape}")
+            if t.dtype is not dtype:
+                raise self._bad(RNN_ERR_ARG, f"{name}: type {t.dtype}, expected {dtype}")
+            if t.get_device() != self._index:
+                raise self._bad(RNN_ERR_ARG, f"{name}: on {t.device}, expected {self.device}")
+            field = getattr(struct, name)
+            if not t.is_contiguous() and t.numel():
+                if not row:
+                    raise self._bad(RNN_ERR_ARG, f"{name}: has to be contiguous")
+                field.row_stride = self._row_stride(name, t)
+            field.ptr = t.data_ptr()
+        return struct
+
+    def _row_stride(self, name, t):
+        """Elements from one row to the next, where all leading dimensions go by one stride."""
+        size, stride = t.shape, t.stride()
+        if size[-1] > 1 and stride[-1] != 1:
+            raise self._bad(RNN_ERR_ARG, f"{name}: the elements of a row have to be contiguous")
+        step = None
+        for n, d in zip(reversed(size[:-1]), reversed(stride[:-1])):
+            if n == 1:
+                continue
+            if step is None:
+                step, rows = d, n
+            elif d != step * rows:
+                raise self._bad(RNN_ERR_ARG, f"{name}: its rows have to lie a constant stride apart, got {stride}")
+            else:
+                rows *= n
+        if step is not None and step < size[-1]:
+            raise self._bad(RNN_ERR_ARG, f"{name}: its rows overlap, stride {step}")
+        return 0 if step is None else step
+
+    def _call(self, encode, structs, scratch, stream):
+        import torch
+        st = stream if stream is not None else torch.cuda.current_stream(self.device)
+        if scratch is not None and st.cuda_stream and not torch.cuda.is_current_stream_capturing():
+            scratch.record_stream(st)   # (not reused, once this object is gone, before the call has run)
+        ptr = scratch.data_ptr() if scratch is not None else None
+        if torch.cuda.current_device() == self._index:
+            _check(encode(self._handle, *structs, ptr, st.cuda_stream or None))
+        else:
+            with torch.cuda.device(self.device):
+                _check(encode(self._handle, *structs, ptr, st.cuda_stream or None))
+
+    def _known(self, tensors):
+        for name in tensors:
+            if name not in self._specs:
+                raise self._bad(RNN_ERR_ARG, f"{name}: unknown tensor")
+
+    def encode(self, tensors: dict, stream=None) -> None:
+        """Enqueue the operator on `stream` (default: the current one)."""
+        self._known(tensors)
+        ops = self._fill(self._operands(), self.operand_names, tensors)
+        self._call(self._encode, (ops,), self._forward_scratch, stream)
+
+    def backward(self, tensors: dict, stream=None) -> None:
+        """Enqueue the gradient.  `tensors` holds the forward pass's inputs too.
+        The first call allocates its scratch, so it cannot be the captured one."""
+        import torch
+        self._known(tensors)
+        ops = self._fill(self._operands(), self.input_names, tensors)
+        grads = self._fill(self._gradients(), self.gradient_names, tensors)
+        if self._backward_scratch is None and self.backward_bytes:
+            if torch.cuda.is_current_stream_capturing():
+                raise self._bad(RNN_ERR_ARG, "scratch: call backward once before a graph captures it")
+            self._backward_scratch = torch.empty(self.backward_bytes, dtype=torch.uint8, device=self.device)
+        self._call(self._encode_backward, (ops, grads), self._backward_scratch, stream)
+
+    def __del__(self):
+        try:
+            if getattr(self, "_handle", None):
+                self._destroy(self._handle)
+                self._handle = None
+        except Exception:
+            pass
+
+
+class CausalConv(_Operator):
+    """Short causal convolution (``rnn_conv_*``): one filter of ``width`` taps a
+    channel over time, with SiLU or without, for prompts and (``seq = 1``, state
+    carried) single tokens, and its gradient."""
+
+    op, who = "conv", "conv"
+    _operands, _gradients = rnn_conv_operands, rnn_conv_gradients
+    operand_names = tuple(n for n, _ in rnn_conv_operands._fields_)
+    input_names = operand_names[:-2]
+    gradient_names = tuple(n for n, _ in rnn_conv_gradients._fields_)
+
+    def __init__(self, dtype: str, seq: int, batch: int, channels: int, width: int = 4, silu: bool = True,
+                 direction: str = "forward", layout: int = 1, device: str = "cuda"):
+        self.dtype = dtype
+        desc = rnn_conv_desc(DTYPES[dtype], DIRECTIONS[direction], int(layout), int(silu), int(seq), int(batch),
+                             int(channels), int(width))
+
+        def shapes(torch, dt):
+            row = ((seq, batch, channels) if layout == 0 else (batch, seq, channels), dt, True)
+            state = ((batch, width - 1, channels), dt, False)
+            f32 = torch.float32
+            return {"X": row, "W": ((channels, width), dt, False), "B": ((channels,), dt, False),
+                    "sequence_lens": ((batch,), torch.int32, False), "initial_state": state, "Y": row,
+                    "final_state": state, "dY": row, "d_final_state": state, "dX": row,
+                    "dW": ((channels, width), f32, False), "dB": ((channels,), f32, False), "d_initial_state": state}
+
+        self._open(desc, device, shapes)
+
+
+class SelectiveScan(_Operator):
+    """Selective scan (``rnn_scan_*``): the state space recurrence with a step
+    size and input and output weights of each step, skip and gate, for prompts
+    and (``seq = 1``, state carried) single tokens, and its gradient.  A, D,
+    delta_bias, the states and the gradients of parameters are f32."""
+
+    op, who = "scan", "scan"
+    _operands, _gradients = rnn_scan_operands, rnn_scan_gradients
+    operand_names = tuple(n for n, _ in rnn_scan_operands._fields_)
+    input_names = operand_names[:-2]
+    gradient_names = tuple(n for n, _ in rnn_scan_gradients._fields_)
+
+    def __init__(self, dtype: str, seq: int, batch: int, channels: int, state: int, groups: int = 1,
+                 delta_softplus: bool = True, direction: str = "forward", layout: int = 1, device: str = "cuda"):
+        self.dtype = dtype
+        desc = rnn_scan_desc(DTYPES[dtype], DIRECTIONS[direction], int(layout), int(delta_softplus), int(seq),
+                             int(batch), int(channels), int(state), int(groups))
+
+        def shapes(torch, dt):
+            lead = (seq, batch) if layout == 0 else (batch, seq)
+            f32 = torch.float32
+            row, bc = (lead + (channels,), dt, True), (lead + (groups * state,), dt, True)
+            chan, h = ((channels,), f32, False), ((batch, channels, state), f32, False)
+            a = ((channels, state), f32, False)
+            return {"X": row, "delta": row, "A": a, "B": bc, "C": bc, "D": chan, "Z": row, "delta_bias": chan,
+                    "sequence_lens": ((batch,), torch.int32, False), "initial_state": h, "Y": row, "final_state": h,
+                    "dY": row, "d_final_state": h, "dX": row, "ddelta": row, "dA": a, "dB": bc, "dC": bc, "dD": chan,
+                    "dZ": row, "ddelta_bias": chan, "d_initial_state": h}
+
+        self._open(desc, device, shapes)
+
+
+class LayerNorm(_Operator):
+    """Layer normalization (``rnn_norm_*``, the ONNX operator over the last
+    axis) with its gradient.  X is [rows, size]; Mean and InvStdDev are f32,
+    and the backward pass reads them."""
+
+    op, who = "norm", "layer norm"
+    _operands, _gradients = rnn_norm_operands, rnn_norm_gradients
+    operand_names = tuple(n for n, _ in rnn_norm_operands._fields_)
+    input_names = ("X", "Scale", "Mean", "InvStdDev")
+    gradient_names = tuple(n for n, _ in rnn_norm_gradients._fields_)
+
+    def __init__(self, dtype: str, rows: int, size: int, epsilon: float = 1e-5, device: str = "cuda"):
+        self.dtype = dtype
+        desc = rnn_norm_desc(DTYPES[dtype], float(epsilon), int(rows), int(size))
+
+        def shapes(torch, dt):
+            row, stat = ((rows, size), dt, True), ((rows,), torch.float32, False)
+            col, grad = ((size,), dt, False), ((size,), torch.float32, False)
+            return {"X": row, "Scale": col, "B": col, "Y": row, "Mean": stat, "InvStdDev": stat, "dY": row, "dX": row,
+                    "dScale": grad, "dB": grad}
+
+        self._open(desc, device, shapes)
 
 
 def output_shapes(spec) -> dict:

@@ -456,6 +456,14 @@ int encode_layer(const rnn_problem* problem, const rnn_operands* ops, void* xw_s
 
 int set_error(int code, int cell, const char* msg) { return fail(code, cell, "%s", msg); }
 
+// (RNN_OK clears the message; the state space operators and layer
+// normalization, seq_api.cpp, report through this)
+int set_error_of(int code, const char* who, const char* text) {
+  if (code == RNN_OK) g_error.clear();
+  else g_error = std::string(who) + ": " + text;
+  return code;
+}
+
 }  // namespace rnnhip
 
 extern "C" int rnn_encode(const rnn_problem* problem, const rnn_operands* ops, void* xw_scratch,

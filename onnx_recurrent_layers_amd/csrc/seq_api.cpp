@@ -1,0 +1,694 @@
+// seq_api.cpp -- the C ABI of the state space operators (short causal
+// convolution, selective scan) and of layer normalization: validation,
+// scratch sizing, choice of launch shapes.  Every check runs in 64-bit checked
+// arithmetic before anything is enqueued; messages name operator and argument.
+#include <algorithm>
+#include <cmath>
+#include <cstdarg>
+#include <cstdio>
+#include <cstdlib>
+#include <new>
+
+#include "seq_ops.h"
+
+using namespace rnnhip;
+
+struct rnn_conv {
+  rnn_conv_desc d;
+  int es;
+  size_t backward_bytes;
+  int tile, tile_b;     // steps a thread walks, forward and backward
+  int64_t parts;        // partial weight gradients at most (element-wise channels: as many)
+};
+
+struct rnn_scan {
+  rnn_scan_desc d;
+  int es, ns, np;
+  int cpg, cbg;
+  int chunk_f, nchunk_f, chunk_b, nchunk_b;
+  int nseg;
+  size_t forward_bytes, backward_bytes;
+};
+
+struct rnn_norm {
+  rnn_norm_desc d;
+  int es;
+  int parts;
+  size_t backward_bytes;
+};
+
+namespace {
+
+constexpr int64_t kMaxBytes = int64_t(1) << 52;
+constexpr int64_t kMaxThreads = (int64_t(1) << 32) - 1;   // of one launch
+
+int fail(int code, const char* who, const char* fmt, ...) {
+  char buf[512];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(buf, sizeof buf, fmt, ap);
+  va_end(ap);
+  return set_error_of(code, who, buf);
+}
+
+// a*b*c*... in bytes, or -1 when it overflows the largest tensor accepted.
+int64_t bytes_of(std::initializer_list<int64_t> f) {
+  int64_t n = 1;
+  for (int64_t x : f) {
+    if (x < 0) return -1;
+    if (x == 0) return 0;
+  }
+  for (int64_t x : f) {
+    if (n > kMaxBytes / x) return -1;
+    n *= x;
+  }
+  return n;
+}
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int elem_size(int dtype) { return dtype == RNN_DTYPE_F32 ? 4 : 2; }
+
+// Scratch regions, 256-byte aligned.
+struct Regions {
+  size_t off = 0;
+  bool ok = true;
+  size_t take(std::initializer_list<int64_t> f) {
+    const int64_t n = bytes_of(f);
+    const size_t at = off;
+    if (n < 0 || off > size_t(kMaxBytes)) ok = false;
+    else off = (off + size_t(n) + 255) & ~size_t(255);
+    return at;
+  }
+};
+
+// The stream's device for the time of a call.
+class OnDevice {
+ public:
+  explicit OnDevice(hipStream_t s) {
+    if (!s || s == hipStreamPerThread) return;
+    hipDevice_t d = 0;
+    int cur = 0;
+    if (hipStreamGetDevice(s, &d) != hipSuccess || hipGetDevice(&cur) != hipSuccess || cur == int(d)) return;
+    if (hipSetDevice(int(d)) == hipSuccess) back_ = cur;
+  }
+  ~OnDevice() {
+    if (back_ >= 0) (void)hipSetDevice(back_);
+  }
+
+ private:
+  int back_ = -1;
+};
+
+// The tensors of one call: resolved one by one, the first failure kept.
+class Tensors {
+ public:
+  explicit Tensors(const char* who) : who_(who) {}
+  int status = RNN_OK;
+
+  char* tensor(const rnn_tensor& t, int es, const char* name, bool required, bool output = false) {
+    return resolve(t.ptr, t.elem_offset, es, name, required, output);
+  }
+  Rows rows(const rnn_rows& t, int es, int64_t length, int64_t count, const char* name, bool required, bool output = false) {
+    Rows r{nullptr, length};
+    if (status != RNN_OK) return r;
+    if (t.ptr) {
+      if (t.row_stride != 0 && t.row_stride < length) {
+        status = fail(RNN_ERR_SHAPE, who_, "%s: row_stride %lld below the row's length %lld", name, (long long)t.row_stride,
+                      (long long)length);
+        return r;
+      }
+      if (t.row_stride) r.rs = t.row_stride;
+      if (bytes_of({std::max<int64_t>(count, 1), r.rs, es}) < 0) {
+        status = fail(RNN_ERR_SHAPE, who_, "%s: size overflows", name);
+        return r;
+      }
+    }
+    r.p = resolve(t.ptr, t.elem_offset, es, name, required, output);
+    return r;
+  }
+  // An output may share its first element with no other tensor of the call;
+  // `pair` names the two that may be one buffer.
+  void apart(const char* pair_a = nullptr, const char* pair_b = nullptr) {
+    for (int i = 0; i < n_ && status == RNN_OK; ++i)
+      for (int j = 0; j < i && status == RNN_OK; ++j)
+        if (seen_[i].p == seen_[j].p && (seen_[i].output || seen_[j].output) &&
+            !(seen_[i].name == pair_b && seen_[j].name == pair_a))
+          status = fail(RNN_ERR_ARG, who_, "%s: the same memory as %s", seen_[i].name, seen_[j].name);
+  }
+
+ private:
+  struct Seen {
+    const char* p;
+    const char* name;
+    bool output;
+  };
+  const char* who_;
+  Seen seen_[32];
+  int n_ = 0;
+
+  char* resolve(void* ptr, int64_t offset, int es, const char* name, bool required, bool output) {
+    if (status != RNN_OK) return nullptr;
+    if (!ptr) {
+      if (required) status = fail(RNN_ERR_ARG, who_, "%s: NULL", name);
+      return nullptr;
+    }
+    if (offset < 0) {
+      status = fail(RNN_ERR_ARG, who_, "%s: negative element offset", name);
+      return nullptr;
+    }
+    if (offset > kMaxBytes / es) {
+      status = fail(RNN_ERR_SHAPE, who_, "%s: element offset overflows", name);
+      return nullptr;
+    }
+    char* p = static_cast<char*>(ptr) + offset * es;
+    if (reinterpret_cast<uintptr_t>(p) % uintptr_t(es)) {
+      status = fail(RNN_ERR_ARG, who_, "%s: address not aligned to its %d-byte element", name, es);
+      return nullptr;
+    }
+    if (n_ < 32) seen_[n_++] = Seen{p, name, output};
+    return p;
+  }
+};
+
+bool aligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+bool aligned(const Rows& r, size_t n, int es) { return aligned(r.p, n) && (size_t(r.rs) * size_t(es)) % n == 0; }
+
+int check_scratch(const char* who, void* scratch, size_t need) {
+  if (!need) return RNN_OK;
+  if (!scratch) return fail(RNN_ERR_ARG, who, "scratch: NULL (needs %zu bytes)", need);
+  if (!aligned(scratch, 256)) return fail(RNN_ERR_ARG, who, "scratch: not 256-byte aligned");
+  return RNN_OK;
+}
+
+int check_seq(const char* who, int dtype, int direction, int layout, int64_t seq, int64_t batch, int64_t channels) {
+  if (dtype < RNN_DTYPE_F32 || dtype > RNN_DTYPE_BF16) return fail(RNN_ERR_ARG, who, "dtype: unknown value %d", dtype);
+  if (direction == RNN_DIR_BIDIRECTIONAL)
+    return fail(RNN_ERR_ARG, who, "direction: forward or reverse (two problems for both)");
+  if (direction != RNN_DIR_FORWARD && direction != RNN_DIR_REVERSE)
+    return fail(RNN_ERR_ARG, who, "direction: unknown value %d", direction);
+  if (layout != 0 && layout != 1) return fail(RNN_ERR_ARG, who, "layout: must be 0 or 1, got %d", layout);
+  if (seq < 0) return fail(RNN_ERR_SHAPE, who, "seq: negative (%lld)", (long long)seq);
+  if (batch < 0) return fail(RNN_ERR_SHAPE, who, "batch: negative (%lld)", (long long)batch);
+  if (channels < 1) return fail(RNN_ERR_SHAPE, who, "channels: must be at least 1 (%lld)", (long long)channels);
+  if (channels > (int64_t(1) << 24)) return fail(RNN_ERR_UNSUPPORTED, who, "channels: above 16777216");
+  if (batch > (int64_t(1) << 30)) return fail(RNN_ERR_UNSUPPORTED, who, "batch: above 2^30");
+  if (seq > (int64_t(1) << 30)) return fail(RNN_ERR_UNSUPPORTED, who, "seq: above 2^30");
+  return RNN_OK;
+}
+
+const char kConv[] = "conv", kScan[] = "scan", kNorm[] = "layer norm";
+
+// Names that may be one buffer (compared by address).
+const char kInitial[] = "initial_state", kFinal[] = "final_state";
+
+}  // namespace
+
+// ---------------------------------------------------------------- convolution
+
+extern "C" int rnn_conv_create(const rnn_conv_desc* desc, rnn_conv** out) {
+  set_error_of(RNN_OK, nullptr, nullptr);
+  if (out) *out = nullptr;
+  if (!desc) return fail(RNN_ERR_ARG, kConv, "desc: NULL");
+  if (!out) return fail(RNN_ERR_ARG, kConv, "out: NULL");
+  const rnn_conv_desc& d = *desc;
+  if (int rc = check_seq(kConv, d.dtype, d.direction, d.layout, d.seq, d.batch, d.channels)) return rc;
+  if (d.silu != 0 && d.silu != 1) return fail(RNN_ERR_ARG, kConv, "silu: must be 0 or 1");
+  if (d.width < 1) return fail(RNN_ERR_SHAPE, kConv, "width: must be at least 1 (%lld)", (long long)d.width);
+  if (d.width < 2 || d.width > 8) return fail(RNN_ERR_UNSUPPORTED, kConv, "width: 2 to 8, got %lld", (long long)d.width);
+  const int es = elem_size(d.dtype);
+  if (bytes_of({d.seq, d.batch, d.channels, es}) < 0) return fail(RNN_ERR_SHAPE, kConv, "X: size overflows");
+  if (bytes_of({d.batch, d.width, d.channels, es}) < 0) return fail(RNN_ERR_SHAPE, kConv, "initial_state: size overflows");
+  // Steps a thread walks: long walks read the K-1 steps before them less
+  // often, short ones give the chip more threads.
+  auto tile = [&](int64_t least, int v, int64_t threads) {
+    int64_t t = 64;
+    while (t > least && d.batch * ceil_div(d.seq, t) * ceil_div(d.channels, v) < threads) t /= 2;
+    return int(t);
+  };
+  const int tf = tile(8, 16 / es, 262144), tb = tile(16, 4, 131072);
+  // the most workgroups a launch may need (element-wise channels; a workgroup
+  // spans 8 channels at least)
+  const int64_t grid_f = d.batch * std::max<int64_t>(ceil_div(d.seq, tf), 1) * ceil_div(d.channels, 8);
+  const int64_t ntb = std::max<int64_t>(ceil_div(ceil_div(d.seq, tb), 4), 1);
+  const int64_t grid_b = d.batch * ntb * ceil_div(d.channels, 64);
+  if (grid_f > kMaxThreads / 256 || grid_b > kMaxThreads / 256)
+    return fail(RNN_ERR_UNSUPPORTED, kConv, "seq x batch x channels: too large for one launch");
+  Regions r;
+  r.take({d.batch, ntb, d.width + 1, d.channels, 4});
+  if (!r.ok) return fail(RNN_ERR_SHAPE, kConv, "scratch: size overflows");
+  rnn_conv* c = new (std::nothrow) rnn_conv();
+  if (!c) return fail(RNN_ERR_ARG, kConv, "out of host memory");
+  c->d = d;
+  c->es = es;
+  c->tile = tf;
+  c->tile_b = tb;
+  c->parts = d.batch * ntb;
+  c->backward_bytes = r.off;
+  *out = c;
+  return RNN_OK;
+}
+
+extern "C" void rnn_conv_destroy(rnn_conv* conv) { delete conv; }
+
+extern "C" int rnn_conv_scratch_size(const rnn_conv* conv, size_t* forward_bytes, size_t* backward_bytes) {
+  set_error_of(RNN_OK, nullptr, nullptr);
+  if (!conv) return fail(RNN_ERR_ARG, kConv, "conv: NULL");
+  if (forward_bytes) *forward_bytes = 0;
+  if (backward_bytes) *backward_bytes = conv->backward_bytes;
+  return RNN_OK;
+}
+
+namespace {
+
+SeqGeom geometry(int64_t seq, int64_t batch, int layout, int direction, const char* lens) {
+  SeqGeom g;
+  g.S = int(seq);
+  g.B = int(batch);
+  g.layout = layout;
+  g.reverse = direction == RNN_DIR_REVERSE;
+  g.lens = reinterpret_cast<const int32_t*>(lens);
+  return g;
+}
+
+// The operands both directions read.
+void conv_inputs(const rnn_conv& c, const rnn_conv_operands& o, Tensors& t, ConvArgs& a) {
+  const rnn_conv_desc& d = c.d;
+  const int64_t rows = d.seq * d.batch;
+  a.X = t.rows(o.X, c.es, d.channels, rows, "X", rows > 0);
+  a.W = t.tensor(o.W, c.es, "W", true);
+  a.bias = t.tensor(o.B, c.es, "B", false);
+  a.geo = geometry(d.seq, d.batch, d.layout, d.direction, t.tensor(o.sequence_lens, 4, "sequence_lens", false));
+  a.init = t.tensor(o.initial_state, c.es, kInitial, false);
+  a.C = int(d.channels);
+  a.K = int(d.width);
+  a.silu = d.silu;
+}
+
+}  // namespace
+
+extern "C" int rnn_conv_encode(const rnn_conv* conv, const rnn_conv_operands* operands, void* scratch, void* stream) {
+  (void)scratch;
+  set_error_of(RNN_OK, nullptr, nullptr);
+  if (!conv) return fail(RNN_ERR_ARG, kConv, "conv: NULL");
+  if (!operands) return fail(RNN_ERR_ARG, kConv, "operands: NULL");
+  const rnn_conv& c = *conv;
+  const rnn_conv_desc& d = c.d;
+  Tensors t(kConv);
+  ConvArgs a{};
+  conv_inputs(c, *operands, t, a);
+  a.Y = t.rows(operands->Y, c.es, d.channels, d.seq * d.batch, "Y", false, true);
+  a.fin = t.tensor(operands->final_state, c.es, kFinal, false, true);
+  t.apart(kInitial, kFinal);
+  if (t.status != RNN_OK) return t.status;
+  if (d.batch == 0 || (!a.Y.p && !a.fin)) return RNN_OK;
+  const int v = 16 / c.es;
+  const bool vec = d.channels % v == 0 && aligned(a.X, 16, c.es) && aligned(a.Y, 16, c.es) && aligned(a.W, 16) &&
+                   aligned(a.bias, 16) && aligned(a.init, 16) && aligned(a.fin, 16);
+  const int64_t n = vec ? d.channels / v : d.channels;   // threads along the channels
+  a.tile = c.tile;
+  a.tx = 8;
+  while (a.tx < 256 && a.tx < n) a.tx *= 2;
+  a.ncb = int(ceil_div(n, a.tx));
+  a.ntb = int(std::max<int64_t>(ceil_div(ceil_div(d.seq, a.tile), 256 / a.tx), 1));
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  OnDevice on(s);
+  if (hipError_t e = launch_conv(a, d.dtype, vec ? v : 1, s); e != hipSuccess)
+    return fail(RNN_ERR_HIP, kConv, "launch: %s", hipGetErrorString(e));
+  return RNN_OK;
+}
+
+extern "C" int rnn_conv_encode_backward(const rnn_conv* conv, const rnn_conv_operands* operands,
+                                        const rnn_conv_gradients* gradients, void* scratch, void* stream) {
+  set_error_of(RNN_OK, nullptr, nullptr);
+  if (!conv) return fail(RNN_ERR_ARG, kConv, "conv: NULL");
+  if (!operands) return fail(RNN_ERR_ARG, kConv, "operands: NULL");
+  if (!gradients) return fail(RNN_ERR_ARG, kConv, "gradients: NULL");
+  const rnn_conv& c = *conv;
+  const rnn_conv_desc& d = c.d;
+  const rnn_conv_gradients& g = *gradients;
+  Tensors t(kConv);
+  ConvArgs a{};
+  const int64_t rows = d.seq * d.batch;
+  conv_inputs(c, *operands, t, a);
+  a.dY = t.rows(g.dY, c.es, d.channels, rows, "dY", rows > 0);
+  a.dfin = t.tensor(g.d_final_state, c.es, "d_final_state", false);
+  a.dX = t.rows(g.dX, c.es, d.channels, rows, "dX", false, true);
+  float* dW = reinterpret_cast<float*>(t.tensor(g.dW, 4, "dW", false, true));
+  float* dB = reinterpret_cast<float*>(t.tensor(g.dB, 4, "dB", false, true));
+  a.dinit = t.tensor(g.d_initial_state, c.es, "d_initial_state", false, true);
+  t.apart();
+  if (t.status != RNN_OK) return t.status;
+  if (!a.dX.p && !dW && !dB && !a.dinit) return RNN_OK;
+  const size_t need = dW || dB ? c.backward_bytes : 0;
+  if (int rc = check_scratch(kConv, scratch, need)) return rc;
+  a.part = dW || dB ? static_cast<float*>(scratch) : nullptr;
+  const size_t al = size_t(4) * c.es;   // four channels a thread
+  const bool vec = d.channels % 4 == 0 && aligned(a.X, al, c.es) && aligned(a.dY, al, c.es) && aligned(a.dX, al, c.es) &&
+                   aligned(a.W, al) && aligned(a.bias, al) && aligned(a.init, al) && aligned(a.dfin, al) &&
+                   aligned(a.dinit, al);
+  a.tile = c.tile_b;
+  a.tx = 64;
+  a.ncb = int(ceil_div(d.channels, vec ? 256 : 64));
+  a.ntb = int(std::max<int64_t>(ceil_div(ceil_div(d.seq, a.tile), 4), 1));
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  OnDevice on(s);
+  if (hipError_t e = launch_conv_backward(a, d.dtype, vec ? 4 : 1, s); e != hipSuccess)
+    return fail(RNN_ERR_HIP, kConv, "launch: %s", hipGetErrorString(e));
+  if (dW || dB) {
+    ColSumArgs cs{a.part, int(c.parts), (d.width + 1) * d.channels, dW, dB, int(d.channels), int(d.width)};
+    if (hipError_t e = launch_colsum(cs, s); e != hipSuccess)
+      return fail(RNN_ERR_HIP, kConv, "sums launch: %s", hipGetErrorString(e));
+  }
+  return RNN_OK;
+}
+
+// ----------------------------------------------------------------------- scan
+
+namespace {
+
+// Steps of a chunk of the time axis.  `blocks`: the workgroups that the rows
+// and channels give by themselves; `want`: those that fill the chip; more
+// chunks than 64 would make their join at a chunk's start long.
+int chunk_steps(int64_t seq, int64_t blocks, int64_t want, int tile, int64_t least) {
+  if (const char* e = std::getenv("RNN_SCAN_CHUNK")) {
+    const int64_t n = std::atoll(e);
+    if (n > 0) return int(std::min<int64_t>(ceil_div(n, tile) * tile, std::max<int64_t>(ceil_div(seq, tile), 1) * tile));
+  }
+  int64_t n = 1;
+  while (n < 64 && blocks * n < want && seq / (2 * n) >= least) n *= 2;
+  return int(std::max<int64_t>(ceil_div(ceil_div(seq, n), tile), 1) * tile);
+}
+
+}  // namespace
+
+extern "C" int rnn_scan_create(const rnn_scan_desc* desc, rnn_scan** out) {
+  set_error_of(RNN_OK, nullptr, nullptr);
+  if (out) *out = nullptr;
+  if (!desc) return fail(RNN_ERR_ARG, kScan, "desc: NULL");
+  if (!out) return fail(RNN_ERR_ARG, kScan, "out: NULL");
+  const rnn_scan_desc& d = *desc;
+  if (int rc = check_seq(kScan, d.dtype, d.direction, d.layout, d.seq, d.batch, d.channels)) return rc;
+  if (d.delta_softplus != 0 && d.delta_softplus != 1) return fail(RNN_ERR_ARG, kScan, "delta_softplus: must be 0 or 1");
+  if (d.state < 1) return fail(RNN_ERR_SHAPE, kScan, "state: must be at least 1 (%lld)", (long long)d.state);
+  if (d.state > kScanMaxState) return fail(RNN_ERR_UNSUPPORTED, kScan, "state: above %d", kScanMaxState);
+  if (d.groups < 1 || d.groups > d.channels || d.channels % d.groups)
+    return fail(RNN_ERR_SHAPE, kScan, "groups: must divide channels (%lld of %lld)", (long long)d.groups, (long long)d.channels);
+  rnn_scan p{};
+  p.d = d;
+  p.es = elem_size(d.dtype);
+  p.ns = scan_lane_states(d.state);
+  p.np = 4 * p.ns;
+  p.cpg = int(d.channels / d.groups);
+  p.cbg = int(ceil_div(p.cpg, 64));
+  if (bytes_of({d.seq, d.batch, d.channels, p.es}) < 0) return fail(RNN_ERR_SHAPE, kScan, "X: size overflows");
+  if (bytes_of({d.seq, d.batch, d.groups, d.state, p.es}) < 0) return fail(RNN_ERR_SHAPE, kScan, "B: size overflows");
+  if (bytes_of({d.batch, d.channels, p.np, 4}) < 0) return fail(RNN_ERR_SHAPE, kScan, "initial_state: size overflows");
+  const int64_t nb = d.groups * p.cbg;   // workgroups along the channels
+  const int64_t blocks = std::max<int64_t>(d.batch, 1) * nb;
+  const int tile = scan_tile(p.ns), seg = scan_segment(p.ns);
+  p.chunk_f = chunk_steps(d.seq, blocks, blocks < 256 ? 512 : 0, tile, 64);
+  p.chunk_b = chunk_steps(d.seq, blocks, 512, tile, 64);
+  p.nchunk_f = int(std::max<int64_t>(ceil_div(d.seq, p.chunk_f), 1));
+  p.nchunk_b = int(std::max<int64_t>(ceil_div(d.seq, p.chunk_b), 1));
+  p.nseg = int(std::max<int64_t>(ceil_div(d.seq, seg), 1));
+  const int64_t most = kMaxThreads / 256;
+  const int64_t sums = ceil_div(d.seq * d.batch * 2, 256) * d.groups * d.state + d.channels * (p.np + 2);
+  if (blocks > most / std::max(p.nchunk_f, p.nchunk_b) || sums > most)
+    return fail(RNN_ERR_UNSUPPORTED, kScan, "seq x batch x channels: too large for one launch");
+  Regions f, b;
+  if (p.nchunk_f > 1) {
+    f.take({d.batch, p.nchunk_f, d.channels, p.np, 4});
+    f.take({d.batch, p.nchunk_f, d.channels, 4});
+    f.take({d.batch, d.channels, p.np, 4});
+  }
+  b.take({d.batch, p.nseg, d.channels, p.np, 4});
+  b.take({d.batch, p.nseg, d.channels, 4});
+  b.take({nb, d.batch, d.seq, 2, p.np, 4});
+  b.take({d.batch, p.nchunk_b, d.channels, p.np, 4});
+  b.take({d.batch, p.nchunk_b, 2, d.channels, 4});
+  if (p.nchunk_b > 1) {
+    b.take({d.batch, p.nchunk_b, d.channels, p.np, 4});
+    b.take({d.batch, p.nchunk_b, d.channels, p.np, 4});
+    b.take({d.batch, p.nchunk_b, d.channels, 4});
+  }
+  if (!f.ok || !b.ok) return fail(RNN_ERR_SHAPE, kScan, "scratch: size overflows");
+  p.forward_bytes = f.off;
+  p.backward_bytes = b.off;
+  rnn_scan* q = new (std::nothrow) rnn_scan(p);
+  if (!q) return fail(RNN_ERR_ARG, kScan, "out of host memory");
+  *out = q;
+  return RNN_OK;
+}
+
+extern "C" void rnn_scan_destroy(rnn_scan* scan) { delete scan; }
+
+extern "C" int rnn_scan_scratch_size(const rnn_scan* scan, size_t* forward_bytes, size_t* backward_bytes) {
+  set_error_of(RNN_OK, nullptr, nullptr);
+  if (!scan) return fail(RNN_ERR_ARG, kScan, "scan: NULL");
+  if (forward_bytes) *forward_bytes = scan->forward_bytes;
+  if (backward_bytes) *backward_bytes = scan->backward_bytes;
+  return RNN_OK;
+}
+
+namespace {
+
+void scan_inputs(const rnn_scan& p, const rnn_scan_operands& o, Tensors& t, ScanArgs& a) {
+  const rnn_scan_desc& d = p.d;
+  const int64_t rows = d.seq * d.batch, gn = d.groups * d.state;
+  const bool any = rows > 0;
+  a.X = t.rows(o.X, p.es, d.channels, rows, "X", any);
+  a.delta = t.rows(o.delta, p.es, d.channels, rows, "delta", any);
+  a.A = reinterpret_cast<const float*>(t.tensor(o.A, 4, "A", true));
+  a.Bm = t.rows(o.B, p.es, gn, rows, "B", any);
+  a.Cm = t.rows(o.C, p.es, gn, rows, "C", any);
+  a.D = reinterpret_cast<const float*>(t.tensor(o.D, 4, "D", false));
+  a.Z = t.rows(o.Z, p.es, d.channels, rows, "Z", false);
+  a.have_z = a.Z.p != nullptr;
+  a.dbias = reinterpret_cast<const float*>(t.tensor(o.delta_bias, 4, "delta_bias", false));
+  a.geo = geometry(d.seq, d.batch, d.layout, d.direction, t.tensor(o.sequence_lens, 4, "sequence_lens", false));
+  a.init = reinterpret_cast<const float*>(t.tensor(o.initial_state, 4, kInitial, false));
+  a.C = int(d.channels);
+  a.N = int(d.state);
+  a.G = int(d.groups);
+  a.softplus = d.delta_softplus;
+  a.cpg = p.cpg;
+  a.cbg = p.cbg;
+  a.np = p.np;
+  a.nseg = p.nseg;
+}
+
+bool vec_state(const rnn_scan& p, std::initializer_list<const float*> ts) {
+  if (p.d.state != p.np) return false;
+  const size_t n = std::min<size_t>(16, size_t(p.ns) * 4);
+  for (const float* t : ts)
+    if (!aligned(t, n)) return false;
+  return true;
+}
+
+}  // namespace
+
+extern "C" int rnn_scan_encode(const rnn_scan* scan, const rnn_scan_operands* operands, void* scratch, void* stream) {
+  set_error_of(RNN_OK, nullptr, nullptr);
+  if (!scan) return fail(RNN_ERR_ARG, kScan, "scan: NULL");
+  if (!operands) return fail(RNN_ERR_ARG, kScan, "operands: NULL");
+  const rnn_scan& p = *scan;
+  const rnn_scan_desc& d = p.d;
+  Tensors t(kScan);
+  ScanArgs a{};
+  scan_inputs(p, *operands, t, a);
+  a.Y = t.rows(operands->Y, p.es, d.channels, d.seq * d.batch, "Y", false, true);
+  a.fin = reinterpret_cast<float*>(t.tensor(operands->final_state, 4, kFinal, false, true));
+  t.apart(kInitial, kFinal);
+  if (t.status != RNN_OK) return t.status;
+  if (d.batch == 0 || (!a.Y.p && !a.fin)) return RNN_OK;
+  if (int rc = check_scratch(kScan, scratch, p.forward_bytes)) return rc;
+  a.chunk = p.chunk_f;
+  a.nchunk = p.nchunk_f;
+  a.vec_state = vec_state(p, {a.A, a.init, a.fin});
+  if (a.nchunk > 1) {
+    char* base = static_cast<char*>(scratch);
+    Regions f;
+    a.loc = reinterpret_cast<float*>(base + f.take({d.batch, a.nchunk, d.channels, p.np, 4}));
+    a.sum = reinterpret_cast<float*>(base + f.take({d.batch, a.nchunk, d.channels, 4}));
+    a.first = reinterpret_cast<float*>(base + f.take({d.batch, d.channels, p.np, 4}));
+  }
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  OnDevice on(s);
+  if (a.nchunk > 1)
+    if (hipError_t e = launch_scan_local(a, d.dtype, s); e != hipSuccess)
+      return fail(RNN_ERR_HIP, kScan, "chunk launch: %s", hipGetErrorString(e));
+  if (hipError_t e = launch_scan(a, d.dtype, s); e != hipSuccess)
+    return fail(RNN_ERR_HIP, kScan, "launch: %s", hipGetErrorString(e));
+  return RNN_OK;
+}
+
+extern "C" int rnn_scan_encode_backward(const rnn_scan* scan, const rnn_scan_operands* operands,
+                                        const rnn_scan_gradients* gradients, void* scratch, void* stream) {
+  set_error_of(RNN_OK, nullptr, nullptr);
+  if (!scan) return fail(RNN_ERR_ARG, kScan, "scan: NULL");
+  if (!operands) return fail(RNN_ERR_ARG, kScan, "operands: NULL");
+  if (!gradients) return fail(RNN_ERR_ARG, kScan, "gradients: NULL");
+  const rnn_scan& p = *scan;
+  const rnn_scan_desc& d = p.d;
+  const rnn_scan_gradients& g = *gradients;
+  const int64_t rows = d.seq * d.batch, gn = d.groups * d.state;
+  Tensors t(kScan);
+  ScanArgs a{};
+  scan_inputs(p, *operands, t, a);
+  a.dY = t.rows(g.dY, p.es, d.channels, rows, "dY", rows > 0);
+  a.dfin = reinterpret_cast<const float*>(t.tensor(g.d_final_state, 4, "d_final_state", false));
+  a.dX = t.rows(g.dX, p.es, d.channels, rows, "dX", false, true);
+  a.ddelta = t.rows(g.ddelta, p.es, d.channels, rows, "ddelta", false, true);
+  a.dA = reinterpret_cast<float*>(t.tensor(g.dA, 4, "dA", false, true));
+  a.dB = t.rows(g.dB, p.es, gn, rows, "dB", false, true);
+  a.dC = t.rows(g.dC, p.es, gn, rows, "dC", false, true);
+  a.dD = reinterpret_cast<float*>(t.tensor(g.dD, 4, "dD", false, true));
+  a.dZ = t.rows(g.dZ, p.es, d.channels, rows, "dZ", false, true);
+  a.ddbias = reinterpret_cast<float*>(t.tensor(g.ddelta_bias, 4, "ddelta_bias", false, true));
+  a.dinit = reinterpret_cast<float*>(t.tensor(g.d_initial_state, 4, "d_initial_state", false, true));
+  t.apart();
+  if (t.status != RNN_OK) return t.status;
+  if (a.dZ.p && !a.have_z) return fail(RNN_ERR_ARG, kScan, "dZ: there is no Z");
+  if (!a.dX.p && !a.ddelta.p && !a.dA && !a.dB.p && !a.dC.p && !a.dD && !a.dZ.p && !a.ddbias && !a.dinit) return RNN_OK;
+  if (int rc = check_scratch(kScan, scratch, p.backward_bytes)) return rc;
+  a.chunk = p.chunk_b;
+  a.nchunk = p.nchunk_b;
+  a.vec_state = vec_state(p, {a.A, a.init, a.dfin, a.dinit});
+  char* base = static_cast<char*>(scratch);
+  Regions b;
+  auto at = [&](std::initializer_list<int64_t> f) { return reinterpret_cast<float*>(base + b.take(f)); };
+  a.ckpt = at({d.batch, p.nseg, d.channels, p.np, 4});
+  a.cum = at({d.batch, p.nseg, d.channels, 4});
+  a.pbc = at({d.groups * p.cbg, d.batch, d.seq, 2, p.np, 4});
+  a.pA = at({d.batch, a.nchunk, d.channels, p.np, 4});
+  a.pD = at({d.batch, a.nchunk, 2, d.channels, 4});
+  if (a.nchunk > 1) {
+    a.loc = at({d.batch, a.nchunk, d.channels, p.np, 4});
+    a.gloc = at({d.batch, a.nchunk, d.channels, p.np, 4});
+    a.sum = at({d.batch, a.nchunk, d.channels, 4});
+  }
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  OnDevice on(s);
+  if (hipError_t e = launch_scan_backward(a, d.dtype, s); e != hipSuccess)
+    return fail(RNN_ERR_HIP, kScan, "backward launch: %s", hipGetErrorString(e));
+  return RNN_OK;
+}
+
+// --------------------------------------------------------- layer normalization
+
+extern "C" int rnn_norm_create(const rnn_norm_desc* desc, rnn_norm** out) {
+  set_error_of(RNN_OK, nullptr, nullptr);
+  if (out) *out = nullptr;
+  if (!desc) return fail(RNN_ERR_ARG, kNorm, "desc: NULL");
+  if (!out) return fail(RNN_ERR_ARG, kNorm, "out: NULL");
+  const rnn_norm_desc& d = *desc;
+  if (d.dtype < RNN_DTYPE_F32 || d.dtype > RNN_DTYPE_BF16) return fail(RNN_ERR_ARG, kNorm, "dtype: unknown value %d", d.dtype);
+  if (!(d.epsilon >= 0.f) || std::isinf(d.epsilon)) return fail(RNN_ERR_ARG, kNorm, "epsilon: must be finite and not negative");
+  if (d.rows < 0) return fail(RNN_ERR_SHAPE, kNorm, "rows: negative (%lld)", (long long)d.rows);
+  if (d.size < 1) return fail(RNN_ERR_SHAPE, kNorm, "size: must be at least 1 (%lld)", (long long)d.size);
+  if (d.size > (int64_t(1) << 24)) return fail(RNN_ERR_UNSUPPORTED, kNorm, "size: above 16777216");
+  if (d.rows > (int64_t(1) << 30)) return fail(RNN_ERR_UNSUPPORTED, kNorm, "rows: above 2^30");
+  const int es = elem_size(d.dtype);
+  if (bytes_of({d.rows, d.size, es}) < 0) return fail(RNN_ERR_SHAPE, kNorm, "X: size overflows");
+  // a launch holds rows x the threads of a row (16 to 256; 64 for at most
+  // 1024 values of 16 bits, 256 above)
+  if (d.rows > kMaxThreads / 256 - 256) return fail(RNN_ERR_UNSUPPORTED, kNorm, "rows: too many for one launch");
+  rnn_norm* n = new (std::nothrow) rnn_norm();
+  if (!n) return fail(RNN_ERR_ARG, kNorm, "out of host memory");
+  n->d = d;
+  n->es = es;
+  // partial sums of dScale and dB: two workgroups a compute unit, but four
+  // rows at least for each
+  n->parts = int(std::max<int64_t>(1, std::min<int64_t>(512, ceil_div(d.rows, 4))));
+  Regions r;
+  r.take({n->parts, 2, d.size, 4});
+  n->backward_bytes = r.off;
+  *out = n;
+  return RNN_OK;
+}
+
+extern "C" void rnn_norm_destroy(rnn_norm* norm) { delete norm; }
+
+extern "C" int rnn_norm_scratch_size(const rnn_norm* norm, size_t* forward_bytes, size_t* backward_bytes) {
+  set_error_of(RNN_OK, nullptr, nullptr);
+  if (!norm) return fail(RNN_ERR_ARG, kNorm, "norm: NULL");
+  if (forward_bytes) *forward_bytes = 0;
+  if (backward_bytes) *backward_bytes = norm->backward_bytes;
+  return RNN_OK;
+}
+
+extern "C" int rnn_norm_encode(const rnn_norm* norm, const rnn_norm_operands* operands, void* scratch, void* stream) {
+  (void)scratch;
+  set_error_of(RNN_OK, nullptr, nullptr);
+  if (!norm) return fail(RNN_ERR_ARG, kNorm, "norm: NULL");
+  if (!operands) return fail(RNN_ERR_ARG, kNorm, "operands: NULL");
+  const rnn_norm& p = *norm;
+  const rnn_norm_desc& d = p.d;
+  const rnn_norm_operands& o = *operands;
+  Tensors t(kNorm);
+  NormArgs a{};
+  a.X = t.rows(o.X, p.es, d.size, d.rows, "X", d.rows > 0);
+  a.scale = t.tensor(o.Scale, p.es, "Scale", true);
+  a.shift = t.tensor(o.B, p.es, "B", false);
+  a.Y = t.rows(o.Y, p.es, d.size, d.rows, "Y", false, true);
+  a.mean = reinterpret_cast<float*>(t.tensor(o.Mean, 4, "Mean", false, true));
+  a.inv = reinterpret_cast<float*>(t.tensor(o.InvStdDev, 4, "InvStdDev", false, true));
+  t.apart();
+  if (t.status != RNN_OK) return t.status;
+  if (d.rows == 0 || (!a.Y.p && !a.mean && !a.inv)) return RNN_OK;
+  a.rows = d.rows;
+  a.size = int(d.size);
+  a.eps = d.epsilon;
+  a.vec = d.size % (16 / p.es) == 0 && aligned(a.X, 16, p.es) && aligned(a.Y, 16, p.es) && aligned(a.scale, 16) &&
+          aligned(a.shift, 16);
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  OnDevice on(s);
+  if (hipError_t e = launch_norm(a, d.dtype, s); e != hipSuccess)
+    return fail(RNN_ERR_HIP, kNorm, "launch: %s", hipGetErrorString(e));
+  return RNN_OK;
+}
+
+extern "C" int rnn_norm_encode_backward(const rnn_norm* norm, const rnn_norm_operands* operands,
+                                        const rnn_norm_gradients* gradients, void* scratch, void* stream) {
+  set_error_of(RNN_OK, nullptr, nullptr);
+  if (!norm) return fail(RNN_ERR_ARG, kNorm, "norm: NULL");
+  if (!operands) return fail(RNN_ERR_ARG, kNorm, "operands: NULL");
+  if (!gradients) return fail(RNN_ERR_ARG, kNorm, "gradients: NULL");
+  const rnn_norm& p = *norm;
+  const rnn_norm_desc& d = p.d;
+  const rnn_norm_operands& o = *operands;
+  const rnn_norm_gradients& g = *gradients;
+  Tensors t(kNorm);
+  NormArgs a{};
+  const bool any = d.rows > 0;
+  a.X = t.rows(o.X, p.es, d.size, d.rows, "X", any);
+  a.scale = t.tensor(o.Scale, p.es, "Scale", true);
+  a.mean = reinterpret_cast<float*>(t.tensor(o.Mean, 4, "Mean", any));
+  a.inv = reinterpret_cast<float*>(t.tensor(o.InvStdDev, 4, "InvStdDev", any));
+  a.dY = t.rows(g.dY, p.es, d.size, d.rows, "dY", any);
+  a.dX = t.rows(g.dX, p.es, d.size, d.rows, "dX", false, true);
+  float* dScale = reinterpret_cast<float*>(t.tensor(g.dScale, 4, "dScale", false, true));
+  float* dB = reinterpret_cast<float*>(t.tensor(g.dB, 4, "dB", false, true));
+  t.apart();
+  if (t.status != RNN_OK) return t.status;
+  if (!a.dX.p && !dScale && !dB) return RNN_OK;
+  const bool sums = dScale || dB;
+  if (int rc = check_scratch(kNorm, scratch, sums ? p.backward_bytes : 0)) return rc;
+  a.rows = d.rows;
+  a.size = int(d.size);
+  a.eps = d.epsilon;
+  a.parts = p.parts;
+  a.part = sums ? static_cast<float*>(scratch) : nullptr;
+  a.vec = d.size % (16 / p.es) == 0 && aligned(a.X, 16, p.es) && aligned(a.dY, 16, p.es) && aligned(a.dX, 16, p.es) &&
+          aligned(a.scale, 16);
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  OnDevice on(s);
+  if (hipError_t e = launch_norm_backward(a, d.dtype, s); e != hipSuccess)
+    return fail(RNN_ERR_HIP, kNorm, "launch: %s", hipGetErrorString(e));
+  if (sums) {
+    ColSumArgs cs{a.part, a.parts, 2 * d.size, dScale, dB, int(d.size), 1};
+    if (hipError_t e = launch_colsum(cs, s); e != hipSuccess)
+      return fail(RNN_ERR_HIP, kNorm, "sums launch: %s", hipGetErrorString(e));
+  }
+  return RNN_OK;
+}
