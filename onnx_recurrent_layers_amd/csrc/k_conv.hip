@@ -183,19 +183,30 @@ __global__ __launch_bounds__(256) void conv_backward_kernel(ConvArgs a) {
     const T* xp = X + (r.base + s0 * r.step) * a.X.rs;
     const T* gp = dY + (r.base + s0 * r.step) * a.dY.rs;
     const int64_t xd = r.step * a.X.rs, gd = r.step * a.dY.rs;
-    for (int s = s0; s - K + 1 < e1; s += 4, xp += 4 * xd, gp += 4 * gd) {
-      Pack<T, V> in[4], gin[4];
-      if (s < L) {
+    // four steps' rows, and the next four's under way; past the row's end its
+    // last step's (not used)
+    Pack<T, V> nin[4], ngin[4];
+    auto fetch = [&](int s) {
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int at = min(u, L - 1 - s);
-          in[u] = *reinterpret_cast<const Pack<T, V>*>(xp + at * xd);
-          gin[u] = *reinterpret_cast<const Pack<T, V>*>(gp + at * gd);
-        }
-      } else {
-#pragma unroll
-        for (int u = 0; u < 4; ++u) in[u] = gin[u] = Pack<T, V>{};
+      for (int u = 0; u < 4; ++u) {
+        const int64_t at = min(u, L - 1 - s);
+        nin[u] = *reinterpret_cast<const Pack<T, V>*>(xp + at * xd);
+        ngin[u] = *reinterpret_cast<const Pack<T, V>*>(gp + at * gd);
       }
+    };
+#pragma unroll
+    for (int u = 0; u < 4; ++u) nin[u] = ngin[u] = Pack<T, V>{};
+    if (s0 < L) fetch(s0);
+    for (int s = s0; s - K + 1 < e1; s += 4) {
+      Pack<T, V> in[4], gin[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        in[u] = nin[u];
+        gin[u] = ngin[u];
+      }
+      xp += 4 * xd;
+      gp += 4 * gd;
+      if (s + 4 < L && s + 4 - K + 1 < e1) fetch(s + 4);
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         const int st = s + u;

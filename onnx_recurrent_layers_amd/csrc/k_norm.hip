@@ -161,29 +161,40 @@ __global__ __launch_bounds__(256) void norm_backward_kernel(NormArgs a) {
       if (c < a.size) get<T, V>(scale + c, sc[m]);
     }
   }
-  for (int64_t r0 = int64_t(blockIdx.x) * RB; r0 < a.rows; r0 += int64_t(a.parts) * RB) {
+  // the next rows' values are under way while these are summed
+  const int64_t by = int64_t(a.parts) * RB;
+  Pack<T, V> px[R], pg[R];
+  float pm = 0.f, pi = 0.f;
+  auto fetch = [&](int64_t row) {
+    const int64_t at = row < a.rows ? row : a.rows - 1;
+    const T* X = reinterpret_cast<const T*>(a.X.p) + at * a.X.rs;
+    const T* G = reinterpret_cast<const T*>(a.dY.p) + at * a.dY.rs;
+#pragma unroll
+    for (int m = 0; m < R; ++m) {
+      const int c = min((m * W + t) * V, a.size - V);
+      px[m] = *reinterpret_cast<const Pack<T, V>*>(X + c);
+      pg[m] = *reinterpret_cast<const Pack<T, V>*>(G + c);
+    }
+    pm = a.mean[at];
+    pi = a.inv[at];
+  };
+  if (M > 0 && int64_t(blockIdx.x) * RB < a.rows) fetch(int64_t(blockIdx.x) * RB + slot);
+  for (int64_t r0 = int64_t(blockIdx.x) * RB; r0 < a.rows; r0 += by) {
     const int64_t row = r0 + slot;
     const bool in = row < a.rows;
     const int64_t at = in ? row : a.rows - 1;
-    const T* X = reinterpret_cast<const T*>(a.X.p) + at * a.X.rs;
-    const T* G = reinterpret_cast<const T*>(a.dY.p) + at * a.dY.rs;
     T* D = reinterpret_cast<T*>(a.dX.p) + at * a.dX.rs;
-    const float mean = a.mean[at], inv = a.inv[at];
     float v[2] = {0.f, 0.f};
     if constexpr (M > 0) {
       float xh[M][V], g[M][V];
+      const float mean = pm, inv = pi;
 #pragma unroll
       for (int m = 0; m < M; ++m) {
-        const int c = (m * W + t) * V;
-        const bool is = in && c < a.size;
-        if (is) {
-          get<T, V>(X + c, xh[m]);
-          get<T, V>(G + c, g[m]);
-        }
+        const bool is = in && (m * W + t) * V < a.size;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-          xh[m][i] = is ? (xh[m][i] - mean) * inv : 0.f;
-          const float dy = is ? g[m][i] : 0.f;
+          xh[m][i] = is ? (float(px[m].v[i]) - mean) * inv : 0.f;
+          const float dy = is ? float(pg[m].v[i]) : 0.f;
           ds[m][i] = __builtin_fmaf(dy, xh[m][i], ds[m][i]);
           db[m][i] += dy;
           g[m][i] = dy * sc[m][i];
@@ -191,6 +202,7 @@ __global__ __launch_bounds__(256) void norm_backward_kernel(NormArgs a) {
           v[1] = __builtin_fmaf(g[m][i], xh[m][i], v[1]);
         }
       }
+      if (r0 + by < a.rows) fetch(row + by);   // uniform
       if (a.dX.p) {
         row_sums<W, 2>(v, lds);
         const float m0 = v[0] * per, m1 = v[1] * per;
@@ -206,6 +218,9 @@ __global__ __launch_bounds__(256) void norm_backward_kernel(NormArgs a) {
         }
       }
     } else if (a.dX.p) {
+      const T* X = reinterpret_cast<const T*>(a.X.p) + at * a.X.rs;
+      const T* G = reinterpret_cast<const T*>(a.dY.p) + at * a.dY.rs;
+      const float mean = a.mean[at], inv = a.inv[at];
       for (int c = t * V; c < a.size; c += W * V) {
         float x[V], g[V], s[V];
         get<T, V>(X + c, x);

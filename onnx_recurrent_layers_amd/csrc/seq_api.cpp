@@ -21,11 +21,18 @@ struct rnn_conv {
   int64_t parts;        // partial weight gradients at most (element-wise channels: as many)
 };
 
+// How one direction of a scan lies on the chip.
+struct ScanPlan {
+  int nw, np;           // waves of a workgroup, states padded to their shares
+  int chunk, nchunk;    // steps of a chunk of the time axis, chunks
+};
+
 struct rnn_scan {
   rnn_scan_desc d;
-  int es, ns, np;
+  int es;
   int cpg, cbg;
-  int chunk_f, nchunk_f, chunk_b, nchunk_b;
+  bool tokens;          // forward by the kernel for a few steps
+  ScanPlan f, b;
   int nseg;
   size_t forward_bytes, backward_bytes;
 };
@@ -366,17 +373,50 @@ extern "C" int rnn_conv_encode_backward(const rnn_conv* conv, const rnn_conv_ope
 
 namespace {
 
-// Steps of a chunk of the time axis.  `blocks`: the workgroups that the rows
-// and channels give by themselves; `want`: those that fill the chip; more
-// chunks than 64 would make their join at a chunk's start long.
-int chunk_steps(int64_t seq, int64_t blocks, int64_t want, int tile, int64_t least) {
+// The split of the states and the chunks of the time axis.  `blocks`: the
+// workgroups that the rows and channels give by themselves; `want`: those that
+// chunks are to make of them.  A chunk has 32 steps or more (a workgroup starts
+// and joins in about the time of a tile of 16), and there are 64 at most.
+ScanPlan scan_plan(const rnn_scan_desc& d, bool backward, int64_t blocks, int64_t want) {
+  ScanPlan p{};
+  const int64_t n = std::min<int64_t>(std::max<int64_t>(ceil_div(want, blocks), 1), 64);
+  p.chunk = int(std::max<int64_t>(ceil_div(std::max<int64_t>(ceil_div(d.seq, n), n > 1 ? 32 : 1), kScanTile), 1) * kScanTile);
   if (const char* e = std::getenv("RNN_SCAN_CHUNK")) {
-    const int64_t n = std::atoll(e);
-    if (n > 0) return int(std::min<int64_t>(ceil_div(n, tile) * tile, std::max<int64_t>(ceil_div(seq, tile), 1) * tile));
+    const int64_t c = std::atoll(e), whole = std::max<int64_t>(ceil_div(d.seq, kScanTile), 1) * kScanTile;
+    if (c > 0) p.chunk = int(c >= whole ? whole : ceil_div(c, kScanTile) * kScanTile);
   }
-  int64_t n = 1;
-  while (n < 64 && blocks * n < want && seq / (2 * n) >= least) n *= 2;
-  return int(std::max<int64_t>(ceil_div(ceil_div(seq, n), tile), 1) * tile);
+  p.nchunk = int(std::max<int64_t>(ceil_div(d.seq, p.chunk), 1));
+  scan_split(d.state, backward, &p.nw, &p.np);
+  return p;
+}
+
+// The scratch regions of the two directions, in the order that they are taken.
+struct ScanScratch {
+  size_t sink, loc, sum, first, ckpt, cum, pbc, pA, pD, gloc;
+};
+bool scan_scratch(const rnn_scan& p, bool backward, ScanScratch* at, size_t* total) {
+  const rnn_scan_desc& d = p.d;
+  const ScanPlan& q = backward ? p.b : p.f;
+  Regions r;
+  *at = ScanScratch{};
+  if (backward || !p.tokens) {
+    at->sink = r.take({d.channels, 4});
+    if (q.nchunk > 1) {
+      at->loc = r.take({d.batch, q.nchunk, q.np, d.channels, 4});
+      at->sum = r.take({d.batch, q.nchunk, d.channels, 4});
+      if (!backward) at->first = r.take({d.batch, q.np, d.channels, 4});
+      else at->gloc = r.take({d.batch, q.nchunk, q.np, d.channels, 4});
+    }
+  }
+  if (backward) {
+    at->ckpt = r.take({d.batch, p.nseg, q.np, d.channels, 4});
+    at->cum = r.take({d.batch, p.nseg, d.channels, 4});
+    at->pbc = r.take({d.groups, p.cbg, d.batch, d.seq, 2, q.np, 4});
+    at->pA = r.take({d.batch, q.nchunk, q.np, d.channels, 4});
+    at->pD = r.take({d.batch, q.nchunk, 2, d.channels, 4});
+  }
+  *total = r.off;
+  return r.ok;
 }
 
 }  // namespace
@@ -396,44 +436,28 @@ extern "C" int rnn_scan_create(const rnn_scan_desc* desc, rnn_scan** out) {
   rnn_scan p{};
   p.d = d;
   p.es = elem_size(d.dtype);
-  p.ns = scan_lane_states(d.state);
-  p.np = 4 * p.ns;
   p.cpg = int(d.channels / d.groups);
   p.cbg = int(ceil_div(p.cpg, 64));
   if (bytes_of({d.seq, d.batch, d.channels, p.es}) < 0) return fail(RNN_ERR_SHAPE, kScan, "X: size overflows");
   if (bytes_of({d.seq, d.batch, d.groups, d.state, p.es}) < 0) return fail(RNN_ERR_SHAPE, kScan, "B: size overflows");
-  if (bytes_of({d.batch, d.channels, p.np, 4}) < 0) return fail(RNN_ERR_SHAPE, kScan, "initial_state: size overflows");
-  const int64_t nb = d.groups * p.cbg;   // workgroups along the channels
-  const int64_t blocks = std::max<int64_t>(d.batch, 1) * nb;
-  const int tile = scan_tile(p.ns), seg = scan_segment(p.ns);
-  p.chunk_f = chunk_steps(d.seq, blocks, blocks < 256 ? 512 : 0, tile, 64);
-  p.chunk_b = chunk_steps(d.seq, blocks, 512, tile, 64);
-  p.nchunk_f = int(std::max<int64_t>(ceil_div(d.seq, p.chunk_f), 1));
-  p.nchunk_b = int(std::max<int64_t>(ceil_div(d.seq, p.chunk_b), 1));
-  p.nseg = int(std::max<int64_t>(ceil_div(d.seq, seg), 1));
-  const int64_t most = kMaxThreads / 256;
-  const int64_t sums = ceil_div(d.seq * d.batch * 2, 256) * d.groups * d.state + d.channels * (p.np + 2);
-  if (blocks > most / std::max(p.nchunk_f, p.nchunk_b) || sums > most)
+  if (bytes_of({d.batch, d.channels, d.state, 4}) < 0) return fail(RNN_ERR_SHAPE, kScan, "initial_state: size overflows");
+  const int64_t blocks = std::max<int64_t>(d.batch, 1) * d.groups * p.cbg;
+  p.tokens = d.seq <= kScanTokens;
+  // Forward, chunks cost the recurrence twice: below 160 workgroups only.  (16
+  // states, 2048 channels, 1024 steps: 4 rows, 128 workgroups, in four chunks
+  // 85 us, in one 113; 8 rows, 256 workgroups, in one 118.)  Backward, states
+  // are computed ahead in any case.  (8 x 512 x 1024, 128 workgroups: two chunks
+  // 125 us, four 133, one 215.)
+  p.f = scan_plan(d, false, blocks, blocks <= 160 ? 512 : 0);
+  p.b = scan_plan(d, true, blocks, 256);
+  p.nseg = int(std::max<int64_t>(ceil_div(d.seq, scan_segment(p.b.np / p.b.nw)), 1));
+  const int64_t most = kMaxThreads / 512;
+  const int64_t sums = ceil_div(d.seq * d.batch * 2, 256) * d.groups * d.state + d.channels * (p.b.np + 2);
+  if (blocks > most / std::max(p.f.nchunk, p.b.nchunk) || sums > most)
     return fail(RNN_ERR_UNSUPPORTED, kScan, "seq x batch x channels: too large for one launch");
-  Regions f, b;
-  if (p.nchunk_f > 1) {
-    f.take({d.batch, p.nchunk_f, d.channels, p.np, 4});
-    f.take({d.batch, p.nchunk_f, d.channels, 4});
-    f.take({d.batch, d.channels, p.np, 4});
-  }
-  b.take({d.batch, p.nseg, d.channels, p.np, 4});
-  b.take({d.batch, p.nseg, d.channels, 4});
-  b.take({nb, d.batch, d.seq, 2, p.np, 4});
-  b.take({d.batch, p.nchunk_b, d.channels, p.np, 4});
-  b.take({d.batch, p.nchunk_b, 2, d.channels, 4});
-  if (p.nchunk_b > 1) {
-    b.take({d.batch, p.nchunk_b, d.channels, p.np, 4});
-    b.take({d.batch, p.nchunk_b, d.channels, p.np, 4});
-    b.take({d.batch, p.nchunk_b, d.channels, 4});
-  }
-  if (!f.ok || !b.ok) return fail(RNN_ERR_SHAPE, kScan, "scratch: size overflows");
-  p.forward_bytes = f.off;
-  p.backward_bytes = b.off;
+  ScanScratch at;
+  if (!scan_scratch(p, false, &at, &p.forward_bytes) || !scan_scratch(p, true, &at, &p.backward_bytes))
+    return fail(RNN_ERR_SHAPE, kScan, "scratch: size overflows");
   rnn_scan* q = new (std::nothrow) rnn_scan(p);
   if (!q) return fail(RNN_ERR_ARG, kScan, "out of host memory");
   *out = q;
@@ -473,16 +497,45 @@ void scan_inputs(const rnn_scan& p, const rnn_scan_operands& o, Tensors& t, Scan
   a.softplus = d.delta_softplus;
   a.cpg = p.cpg;
   a.cbg = p.cbg;
-  a.np = p.np;
-  a.nseg = p.nseg;
 }
 
-bool vec_state(const rnn_scan& p, std::initializer_list<const float*> ts) {
-  if (p.d.state != p.np) return false;
-  const size_t n = std::min<size_t>(16, size_t(p.ns) * 4);
-  for (const float* t : ts)
-    if (!aligned(t, n)) return false;
-  return true;
+// The launch of an element type.
+template <typename F>
+hipError_t of_type(int dtype, F f32, F f16, F bf16, const ScanArgs& a, hipStream_t s) {
+  return dtype == RNN_DTYPE_F32 ? f32(a, s) : dtype == RNN_DTYPE_F16 ? f16(a, s) : bf16(a, s);
+}
+
+// Whether every group's channels and all rows come in aligned packs of four.
+bool vec_rows(const rnn_scan& p, std::initializer_list<Rows> ts) {
+  const size_t n = size_t(4) * p.es;
+  bool ok = p.cpg % 4 == 0;
+  for (const Rows& t : ts) ok = ok && aligned(t, n, p.es);
+  return ok;
+}
+
+// One direction's plan and scratch.
+void scan_lay(const rnn_scan& p, bool backward, void* scratch, ScanArgs& a) {
+  const ScanPlan& q = backward ? p.b : p.f;
+  a.chunk = q.chunk;
+  a.nchunk = q.nchunk;
+  a.nw = q.nw;
+  a.np = q.np;
+  a.nseg = p.nseg;
+  a.vec_rows = vec_rows(p, {a.X, a.delta, a.Z, a.Y, a.dY, a.dX, a.ddelta, a.dZ});
+  ScanScratch at;
+  size_t total;
+  scan_scratch(p, backward, &at, &total);
+  auto f = [&](size_t off) { return reinterpret_cast<float*>(static_cast<char*>(scratch) + off); };
+  a.sink = static_cast<char*>(scratch) + at.sink;
+  a.loc = f(at.loc);
+  a.sum = f(at.sum);
+  a.first = f(at.first);
+  a.gloc = f(at.gloc);
+  a.ckpt = f(at.ckpt);
+  a.cum = f(at.cum);
+  a.pbc = f(at.pbc);
+  a.pA = f(at.pA);
+  a.pD = f(at.pD);
 }
 
 }  // namespace
@@ -502,22 +555,27 @@ extern "C" int rnn_scan_encode(const rnn_scan* scan, const rnn_scan_operands* op
   if (t.status != RNN_OK) return t.status;
   if (d.batch == 0 || (!a.Y.p && !a.fin)) return RNN_OK;
   if (int rc = check_scratch(kScan, scratch, p.forward_bytes)) return rc;
-  a.chunk = p.chunk_f;
-  a.nchunk = p.nchunk_f;
-  a.vec_state = vec_state(p, {a.A, a.init, a.fin});
-  if (a.nchunk > 1) {
-    char* base = static_cast<char*>(scratch);
-    Regions f;
-    a.loc = reinterpret_cast<float*>(base + f.take({d.batch, a.nchunk, d.channels, p.np, 4}));
-    a.sum = reinterpret_cast<float*>(base + f.take({d.batch, a.nchunk, d.channels, 4}));
-    a.first = reinterpret_cast<float*>(base + f.take({d.batch, d.channels, p.np, 4}));
-  }
   hipStream_t s = static_cast<hipStream_t>(stream);
   OnDevice on(s);
+  if (p.tokens) {
+    // states whole 16-byte pieces of four lanes
+    const int64_t n = d.state;
+    const size_t al = size_t(std::min<int64_t>(16, n));
+    const size_t bc = size_t(std::min<int64_t>(n / 4, 4) * p.es);   // (a lane's piece of B and of C)
+    a.vec_state = (n == 4 || n == 8 || n == 16 || n == 32 || n == 64 || n == 128) && aligned(a.A, al) && aligned(a.init, al) &&
+                  aligned(a.fin, al) && aligned(a.Bm, bc, p.es) && aligned(a.Cm, bc, p.es);
+    if (hipError_t e = launch_scan_tokens(a, d.dtype, s); e != hipSuccess)
+      return fail(RNN_ERR_HIP, kScan, "launch: %s", hipGetErrorString(e));
+    return RNN_OK;
+  }
+  scan_lay(p, false, scratch, a);
+  if (!a.Y.p) a.Y = Rows{reinterpret_cast<char*>(a.sink), 0};   // (outputs that are not wanted)
+  // more workgroups than compute units and rows of unequal length
+  a.balance = a.geo.lens && a.nchunk == 1 && d.batch > 1 && d.batch <= 256 && d.batch * d.groups * p.cbg > 256;
   if (a.nchunk > 1)
-    if (hipError_t e = launch_scan_local(a, d.dtype, s); e != hipSuccess)
+    if (hipError_t e = of_type(d.dtype, launch_scan_local_f32, launch_scan_local_f16, launch_scan_local_bf16, a, s); e != hipSuccess)
       return fail(RNN_ERR_HIP, kScan, "chunk launch: %s", hipGetErrorString(e));
-  if (hipError_t e = launch_scan(a, d.dtype, s); e != hipSuccess)
+  if (hipError_t e = of_type(d.dtype, launch_scan_f32, launch_scan_f16, launch_scan_bf16, a, s); e != hipSuccess)
     return fail(RNN_ERR_HIP, kScan, "launch: %s", hipGetErrorString(e));
   return RNN_OK;
 }
@@ -551,25 +609,10 @@ extern "C" int rnn_scan_encode_backward(const rnn_scan* scan, const rnn_scan_ope
   if (a.dZ.p && !a.have_z) return fail(RNN_ERR_ARG, kScan, "dZ: there is no Z");
   if (!a.dX.p && !a.ddelta.p && !a.dA && !a.dB.p && !a.dC.p && !a.dD && !a.dZ.p && !a.ddbias && !a.dinit) return RNN_OK;
   if (int rc = check_scratch(kScan, scratch, p.backward_bytes)) return rc;
-  a.chunk = p.chunk_b;
-  a.nchunk = p.nchunk_b;
-  a.vec_state = vec_state(p, {a.A, a.init, a.dfin, a.dinit});
-  char* base = static_cast<char*>(scratch);
-  Regions b;
-  auto at = [&](std::initializer_list<int64_t> f) { return reinterpret_cast<float*>(base + b.take(f)); };
-  a.ckpt = at({d.batch, p.nseg, d.channels, p.np, 4});
-  a.cum = at({d.batch, p.nseg, d.channels, 4});
-  a.pbc = at({d.groups * p.cbg, d.batch, d.seq, 2, p.np, 4});
-  a.pA = at({d.batch, a.nchunk, d.channels, p.np, 4});
-  a.pD = at({d.batch, a.nchunk, 2, d.channels, 4});
-  if (a.nchunk > 1) {
-    a.loc = at({d.batch, a.nchunk, d.channels, p.np, 4});
-    a.gloc = at({d.batch, a.nchunk, d.channels, p.np, 4});
-    a.sum = at({d.batch, a.nchunk, d.channels, 4});
-  }
+  scan_lay(p, true, scratch, a);
   hipStream_t s = static_cast<hipStream_t>(stream);
   OnDevice on(s);
-  if (hipError_t e = launch_scan_backward(a, d.dtype, s); e != hipSuccess)
+  if (hipError_t e = of_type(d.dtype, launch_scan_backward_f32, launch_scan_backward_f16, launch_scan_backward_bf16, a, s); e != hipSuccess)
     return fail(RNN_ERR_HIP, kScan, "backward launch: %s", hipGetErrorString(e));
   return RNN_OK;
 }

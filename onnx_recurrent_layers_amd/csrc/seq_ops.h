@@ -41,28 +41,31 @@ struct ScanArgs {
   int32_t C, N, G, softplus;
   int32_t cpg, cbg;          // channels of a group, workgroups along them
   int32_t chunk, nchunk;     // steps of a chunk of the time axis, chunks
-  int32_t vec_state;         // state rows may be moved 16 bytes at a time
+  int32_t vec_state;         // states may be moved 16 bytes at a time (tokens)
+  int32_t vec_rows;          // groups and rows of channels are whole aligned packs of four
   int32_t have_z;
+  int32_t balance;           // rows in an order of their lengths (one chunk, at most 256 rows)
   Rows X, delta, Bm, Cm, Z, Y;
   const float *A, *D, *dbias, *init;
   float* fin;
-  // scratch, f32; NP = N padded to four lanes' shares, [c][NP] channel-major
-  float* loc;     // [B][nchunk][C][NP]: a chunk's end state from a zero (first chunk: the initial) state
+  // scratch, f32; NP = N padded to nw waves' shares
+  int32_t nw, np;            // waves of a workgroup, NP
+  float* loc;     // [B][nchunk][NP][C]: a chunk's end state from a zero (first chunk: the initial) state
   float* sum;     // [B][nchunk][C]: a chunk's sum of step sizes
-  float* first;   // [B][C][NP]: the initial state, kept apart for an update in place
+  float* first;   // [B][NP][C]: the initial state, kept apart for an update in place
+  char* sink;     // [C] of the tensor type: what is stored for no step (any workgroup, never read)
   // backward
   Rows dY, dX, ddelta, dB, dC, dZ;
   const float* dfin;
   float* dinit;
   float *dA, *dD, *ddbias;
-  float* ckpt;    // [B][nseg][C][NP]: the chunk-local state before each segment
+  float* ckpt;    // [B][nseg][NP][C]: the chunk-local state before each segment
   float* cum;     // [B][nseg][C]: the sum of step sizes from the chunk's start to the segment's
-  float* gloc;    // [B][nchunk][C][NP]: a chunk's gradient at its start, from a zero one at its end
-  float* pbc;     // [G*cbg][B][S][2][NP]: dB and dC of a workgroup's channels
-  float* pA;      // [B*nchunk][C][NP]
+  float* gloc;    // [B][nchunk][NP][C]: a chunk's gradient at its start, from a zero one at its end
+  float* pbc;     // [G*cbg][B][S][nw][dB: NP/nw, dC: NP/nw] of a workgroup's channels
+  float* pA;      // [B*nchunk][NP][C]
   float* pD;      // [B*nchunk][2][C]: dD, ddelta_bias
   int32_t nseg;   // segments of a row (chunks begin on segment borders)
-  int32_t np;
 };
 
 struct NormArgs {
@@ -89,23 +92,38 @@ struct ColSumArgs {
 
 constexpr int kScanMaxState = 128;
 
-// States a lane holds (four lanes share a channel), from the state size.
-inline int scan_lane_states(int64_t N) {
-  int ns = 1;
-  while (4 * ns < N) ns *= 2;
-  return ns;
+// Steps of a tile of the scan: every wave of a workgroup prepares some.
+constexpr int kScanTile = 16;
+// Steps up to which the kernel for tokens takes a sequence.
+constexpr int kScanTokens = 4;
+// Waves of a workgroup and the states that each takes (a power of two): the
+// split with the least padding.  The backward pass takes up to 16 states on
+// eight waves, two each, since its registers hold 16 steps of them.
+inline void scan_split(int64_t N, bool backward, int* nw, int* np) {
+  static const struct { int upto, nw, ns; } split[] = {{8, 4, 2}, {16, 4, 4}, {24, 6, 4}, {32, 8, 4}, {64, 8, 8}, {128, 8, 16}};
+  int i = 0;
+  while (split[i].upto < N) ++i;
+  *nw = split[i].nw;
+  *np = split[i].nw * split[i].ns;
+  if (backward && split[i].upto == 16) *nw = 8;
 }
-// Steps of a segment of the backward pass: what a lane's registers hold of
-// states and decays (64 of each where a segment may be as short as four).
-inline int scan_segment(int ns) { return ns <= 4 ? 16 : ns == 8 ? 8 : 4; }
-// Steps of a tile of B and C in shared memory.
-constexpr int scan_tile(int ns) { return ns <= 8 ? 32 : 16; }
+// Steps of a segment of the backward pass, from a wave's states: what a lane's
+// registers hold of states and decays, at most 64 of each.
+constexpr int scan_segment(int ns) { return ns <= 4 ? 16 : ns <= 8 ? 8 : 4; }
 
 hipError_t launch_conv(const ConvArgs& a, int dtype, int vec, hipStream_t s);
 hipError_t launch_conv_backward(const ConvArgs& a, int dtype, int vec, hipStream_t s);
-hipError_t launch_scan_local(const ScanArgs& a, int dtype, hipStream_t s);
-hipError_t launch_scan(const ScanArgs& a, int dtype, hipStream_t s);
-hipError_t launch_scan_backward(const ScanArgs& a, int dtype, hipStream_t s);
+hipError_t launch_scan_tokens(const ScanArgs& a, int dtype, hipStream_t s);
+// (one definition a type: k_scan_f32.hip, k_scan_f16.hip, k_scan_bf16.hip)
+hipError_t launch_scan_local_f32(const ScanArgs& a, hipStream_t s);
+hipError_t launch_scan_local_f16(const ScanArgs& a, hipStream_t s);
+hipError_t launch_scan_local_bf16(const ScanArgs& a, hipStream_t s);
+hipError_t launch_scan_f32(const ScanArgs& a, hipStream_t s);
+hipError_t launch_scan_f16(const ScanArgs& a, hipStream_t s);
+hipError_t launch_scan_bf16(const ScanArgs& a, hipStream_t s);
+hipError_t launch_scan_backward_f32(const ScanArgs& a, hipStream_t s);
+hipError_t launch_scan_backward_f16(const ScanArgs& a, hipStream_t s);
+hipError_t launch_scan_backward_bf16(const ScanArgs& a, hipStream_t s);
 hipError_t launch_norm(const NormArgs& a, int dtype, hipStream_t s);
 hipError_t launch_norm_backward(const NormArgs& a, int dtype, hipStream_t s);
 hipError_t launch_colsum(const ColSumArgs& a, hipStream_t s);
