@@ -440,8 +440,10 @@ class _Operator:
         self._handle = None
         lib = load_library()
         self._destroy = getattr(lib, f"rnn_{self.op}_destroy")
-        self._encode = getattr(lib, f"rnn_{self.op}_encode")
-        self._encode_backward = getattr(lib, f"rnn_{self.op}_encode_backward")
+        # (function objects of their own: a call's structs are filled as arrays of words)
+        self._encode, self._encode_backward = lib[f"rnn_{self.op}_encode"], lib[f"rnn_{self.op}_encode_backward"]
+        self._encode.argtypes = [ctypes.c_void_p] * 4
+        self._encode_backward.argtypes = [ctypes.c_void_p] * 5
         self._handle = _create(f"rnn_{self.op}_create", desc)
         self.forward_bytes, self.backward_bytes = _scratch(f"rnn_{self.op}_scratch_size", self._handle)
         self.device = torch.device(device)
@@ -449,7 +451,15 @@ class _Operator:
             self.device = torch.device(self.device.type, torch.cuda.current_device())
         self._index = self.device.index
         # name -> (shape, torch type, row tensor)
-        self._specs = shapes(torch, {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}[self.dtype])
+        specs = shapes(torch, {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}[self.dtype])
+        self._specs = specs
+
+        def layout(struct, names):   # struct's words, and of each of `names` (first word, shape, type, row tensor)
+            return ctypes.c_uint64 * (ctypes.sizeof(struct) // 8), [(n, getattr(struct, n).offset // 8, *specs[n]) for n in names]
+
+        self._forward = layout(self._operands, self.operand_names)
+        self._inputs = layout(self._operands, self.input_names)
+        self._grads = layout(self._gradients, self.gradient_names)
         self._forward_scratch = self._backward_scratch = None
         if self.forward_bytes:
             self._forward_scratch = torch.empty(self.forward_bytes, dtype=torch.uint8, device=self.device)
@@ -457,26 +467,26 @@ class _Operator:
     def _bad(self, code, text):
         return RnnError(code, f"{self.who}: {text}")
 
-    def _fill(self, struct, names, tensors):
-        specs = self._specs
-        for name in names:
+    def _fill(self, layout, tensors):
+        """One C struct of a call: a tensor is its pointer, element offset 0 and, in rows, the stride."""
+        words, fields = layout
+        w, index = words(), self._index
+        for name, at, shape, dtype, row in fields:
             t = tensors.get(name)
             if t is None:
                 continue
-            shape, dtype, row = specs[name]
             if t.shape != shape:
                 raise self._bad(RNN_ERR_SHAPE, f"{name}: shape {tuple(t.shape)}, expected {shape}")
             if t.dtype is not dtype:
                 raise self._bad(RNN_ERR_ARG, f"{name}: type {t.dtype}, expected {dtype}")
-            if t.get_device() != self._index:
+            if t.get_device() != index:
                 raise self._bad(RNN_ERR_ARG, f"{name}: on {t.device}, expected {self.device}")
-            field = getattr(struct, name)
             if not t.is_contiguous() and t.numel():
                 if not row:
                     raise self._bad(RNN_ERR_ARG, f"{name}: has to be contiguous")
-                field.row_stride = self._row_stride(name, t)
-            field.ptr = t.data_ptr()
-        return struct
+                w[at + 2] = self._row_stride(name, t)
+            w[at] = t.data_ptr()
+        return w
 
     def _row_stride(self, name, t):
         """Elements from one row to the next, where all leading dimensions go by one stride."""
@@ -510,23 +520,20 @@ class _Operator:
                 _check(encode(self._handle, *structs, ptr, st.cuda_stream or None))
 
     def _known(self, tensors):
-        for name in tensors:
-            if name not in self._specs:
-                raise self._bad(RNN_ERR_ARG, f"{name}: unknown tensor")
+        if not tensors.keys() <= self._specs.keys():
+            raise self._bad(RNN_ERR_ARG, f"{min(tensors.keys() - self._specs.keys())}: unknown tensor")
 
     def encode(self, tensors: dict, stream=None) -> None:
         """Enqueue the operator on `stream` (default: the current one)."""
         self._known(tensors)
-        ops = self._fill(self._operands(), self.operand_names, tensors)
-        self._call(self._encode, (ops,), self._forward_scratch, stream)
+        self._call(self._encode, (self._fill(self._forward, tensors),), self._forward_scratch, stream)
 
     def backward(self, tensors: dict, stream=None) -> None:
         """Enqueue the gradient.  `tensors` holds the forward pass's inputs too.
         The first call allocates its scratch, so it cannot be the captured one."""
         import torch
         self._known(tensors)
-        ops = self._fill(self._operands(), self.input_names, tensors)
-        grads = self._fill(self._gradients(), self.gradient_names, tensors)
+        ops, grads = self._fill(self._inputs, tensors), self._fill(self._grads, tensors)
         if self._backward_scratch is None and self.backward_bytes:
             if torch.cuda.is_current_stream_capturing():
                 raise self._bad(RNN_ERR_ARG, "scratch: call backward once before a graph captures it")

@@ -375,12 +375,16 @@ namespace {
 
 // The split of the states and the chunks of the time axis.  `blocks`: the
 // workgroups that the rows and channels give by themselves; `want`: those that
-// chunks are to make of them.  A chunk has 32 steps or more (a workgroup starts
-// and joins in about the time of a tile of 16), and there are 64 at most.
+// chunks are to make of them.  A chunk has `least` steps or more, since a
+// workgroup starts and joins in about the time of a tile or two of 16 steps
+// (3 rows of 257 steps by 1002 channels, 24 states, forward: chunks of 64 36 us,
+// of 32 48; 5 rows of 80 by 250, 10 states, backward: of 32 28 us, of 64 38),
+// and there are 64 at most.
 ScanPlan scan_plan(const rnn_scan_desc& d, bool backward, int64_t blocks, int64_t want) {
+  const int64_t least = backward ? 32 : 64;
   ScanPlan p{};
   const int64_t n = std::min<int64_t>(std::max<int64_t>(ceil_div(want, blocks), 1), 64);
-  p.chunk = int(std::max<int64_t>(ceil_div(std::max<int64_t>(ceil_div(d.seq, n), n > 1 ? 32 : 1), kScanTile), 1) * kScanTile);
+  p.chunk = int(std::max<int64_t>(ceil_div(std::max<int64_t>(ceil_div(d.seq, n), n > 1 ? least : 1), kScanTile), 1) * kScanTile);
   if (const char* e = std::getenv("RNN_SCAN_CHUNK")) {
     const int64_t c = std::atoll(e), whole = std::max<int64_t>(ceil_div(d.seq, kScanTile), 1) * kScanTile;
     if (c > 0) p.chunk = int(c >= whole ? whole : ceil_div(c, kScanTile) * kScanTile);

@@ -140,6 +140,8 @@ def test_operands_refused(op):
         # scratch
         refused(lambda: backward(h, filled(op, "operands"), filled(op, "gradients")), ARG, start, "scratch: NULL")
         refused(lambda: backward(h, filled(op, "operands"), filled(op, "gradients"), FAKE + 64), ARG, start, "scratch: not 256-byte aligned")
+        if op == "scan":
+            refused(lambda: encode(h, filled(op, "operands")), ARG, start, "scratch: NULL")
     finally:
         destroy(h)
 
@@ -190,14 +192,17 @@ def test_scratch_sizes(monkeypatch):
     rl.rnn_norm_destroy(h)
     monkeypatch.setenv("RNN_SCAN_CHUNK", "32")
     h = rl.rnn_scan_create(scan_desc(seq=100, batch=2, channels=10, state=5, groups=2))
-    # 4 chunks, states padded to 8, segments of 16 steps, 2 channel blocks
+    # a row for what is not stored; 4 chunks, states padded to 8, segments of 16 steps, 2 channel blocks
+    loc, total = up(2 * 4 * 8 * 10 * 4), up(2 * 4 * 10 * 4)
     assert rl.rnn_scan_scratch_size(h) == (
-        up(2 * 4 * 10 * 8 * 4) + up(2 * 4 * 10 * 4) + up(2 * 10 * 8 * 4),
-        up(2 * 7 * 10 * 8 * 4) + up(2 * 7 * 10 * 4) + up(2 * 2 * 100 * 2 * 8 * 4) + up(2 * 4 * 10 * 8 * 4) + up(2 * 4 * 2 * 10 * 4)
-        + 2 * up(2 * 4 * 10 * 8 * 4) + up(2 * 4 * 10 * 4))
+        up(10 * 4) + loc + total + up(2 * 8 * 10 * 4),
+        up(10 * 4) + 2 * loc + total + up(2 * 7 * 8 * 10 * 4) + up(2 * 7 * 10 * 4) + up(2 * 2 * 100 * 2 * 8 * 4) + loc + up(2 * 4 * 2 * 10 * 4))
     rl.rnn_scan_destroy(h)
     monkeypatch.setenv("RNN_SCAN_CHUNK", "1000")
     h = rl.rnn_scan_create(scan_desc(seq=100, batch=2, channels=10, state=5, groups=2))
+    assert rl.rnn_scan_scratch_size(h)[0] == up(10 * 4)
+    rl.rnn_scan_destroy(h)
+    h = rl.rnn_scan_create(scan_desc(seq=1))      # tokens
     assert rl.rnn_scan_scratch_size(h)[0] == 0
     rl.rnn_scan_destroy(h)
 
@@ -211,26 +216,27 @@ def test_recurrent_layers_refuse_bf16():
 
 @pytest.fixture
 def scan():
-    op = rl.SelectiveScan(dtype="f32", seq=5, batch=3, channels=6, state=4, device="cuda:0")
-    op._index = -1     # CPU tensors stand for the device's: nothing is launched
+    op = rl.SelectiveScan(dtype="f32", seq=4, batch=3, channels=6, state=4, device="cuda:0")
+    op._index = -1     # (few steps take no scratch) CPU tensors stand for the device's: nothing is launched
     return op
 
 
 def test_binding_refuses_tensors(scan):
-    good = {"X": torch.zeros(3, 5, 6)}
+    good = {"X": torch.zeros(3, 4, 6)}
 
     def fill(**kw):
-        return lambda: scan._fill(rl.rnn_scan_operands(), scan.operand_names, good | kw)
+        return lambda: scan._fill(scan._forward, good | kw)
 
     fill()()
-    refused(fill(X=torch.zeros(5, 3, 6)), SHAPE, "scan: ", "X: shape")
-    refused(fill(X=torch.zeros(3, 5, 6, dtype=torch.float16)), ARG, "scan: ", "X: type")
-    refused(fill(X=torch.zeros(3, 5, 12)[..., ::2]), ARG, "scan: ", "X: the elements of a row")
-    refused(fill(X=torch.zeros(5, 3, 6).transpose(0, 1)), ARG, "scan: ", "constant stride")
-    refused(fill(X=torch.zeros(1, 1, 6).expand(3, 5, 6)), ARG, "scan: ", "X: its rows overlap")
+    refused(fill(X=torch.zeros(4, 3, 6)), SHAPE, "scan: ", "X: shape")
+    refused(fill(X=torch.zeros(3, 4, 6, dtype=torch.float16)), ARG, "scan: ", "X: type")
+    refused(fill(X=torch.zeros(3, 4, 12)[..., ::2]), ARG, "scan: ", "X: the elements of a row")
+    refused(fill(X=torch.zeros(4, 3, 6).transpose(0, 1)), ARG, "scan: ", "constant stride")
+    refused(fill(X=torch.zeros(1, 1, 6).expand(3, 4, 6)), ARG, "scan: ", "X: its rows overlap")
     refused(fill(A=torch.zeros(4, 6).t()), ARG, "scan: ", "A: has to be contiguous")
     refused(lambda: scan.encode({"W": torch.zeros(1)}), ARG, "scan: ", "W: unknown tensor")
-    ops = fill(X=torch.zeros(3, 5, 20)[..., 3:9])()
-    assert ops.X.row_stride == 20
+    x = torch.zeros(3, 4, 20)[..., 3:9]
+    ops = rl.rnn_scan_operands.from_buffer(fill(X=x)())
+    assert (ops.X.ptr, ops.X.elem_offset, ops.X.row_stride) == (x.data_ptr(), 0, 20) and ops.delta.ptr is None
     scan._index = 0
     refused(fill(), ARG, "scan: ", "X: on cpu")
