@@ -162,7 +162,7 @@ __global__ __launch_bounds__(256) void norm_backward_kernel(NormArgs a) {
     }
   }
   // the next rows' values are under way while these are summed
-  const int64_t by = int64_t(a.parts) * RB;
+  const int64_t by = int64_t(gridDim.x) * RB;
   Pack<T, V> px[R], pg[R];
   float pm = 0.f, pi = 0.f;
   auto fetch = [&](int64_t row) {
@@ -354,7 +354,7 @@ struct Backward {
     if (M > 0 || a.dX.p) {
       const int64_t blocks = (a.rows + 256 / W - 1) / (256 / W);
       // (with partials wanted, every part is written, by a workgroup of no rows too)
-      const int64_t grid = a.part && M > 0 ? a.parts : blocks < a.parts ? blocks : a.parts;
+      const int64_t grid = M == 0 ? blocks : a.part || blocks > a.parts ? a.parts : blocks;
       if (hipError_t e = go(norm_backward_kernel<T, W, V, M>, grid, 256, a, s); e != hipSuccess) return e;
     }
     if (M == 0 && a.part) return go(norm_columns_kernel<T>, int64_t((a.size + 63) / 64) * a.parts, 256, a, s);

@@ -24,18 +24,13 @@ __device__ __forceinline__ void each(F&& f) {
 }
 
 // The work of workgroup `blockIdx.x` as a number in the order channel block,
-// chunk, batch row.  Workgroups go to the eight dies in turn, and a die's
-// cache is interleaved over its channels in a few hundred bytes, so that
-// neighbouring channel blocks (128 or 256 bytes of a row each) on different
-// dies would leave most channels of each cache idle (measured: 331 us against
-// ISO us for 32 rows of 1024 steps by 2048 channels).  So in each round of 256
-// workgroups, one a compute unit, a die gets neighbours.  `fold`: every second
-// round in falling order.
+// chunk, batch row: its own number, or (`fold`) every second round of 256, one
+// a compute unit, in falling order.  (Giving a die's workgroups neighbouring
+// channel blocks instead made no difference, 191.5 and 191.3 us: a block's 64
+// channels are whole cache lines that no other reads.)
 __device__ __forceinline__ int scan_order(bool fold) {
   const int blk = int(blockIdx.x), base = blk / 256 * 256, n = min(256, int(gridDim.x) - base);
-  const int die = (blk - base) % 8, j = (blk - base) / 8;
-  const int place = die * (n / 8) + min(die, n % 8) + j;
-  return base + (fold && (base & 256) ? n - 1 - place : place);
+  return fold && (base & 256) ? base + (n - 1 - (blk - base)) : blk;
 }
 
 // The batch row of rank `rank` by falling length (ties by number).  Uniform; up
@@ -233,8 +228,7 @@ struct BCWalk {
   __device__ __forceinline__ BCWalk(const ScanArgs& a, const StepRows& r, int g, int s)
       : n(task() % NP), t(task() / NP), in(n < a.N),
         b(a.Bm, r, int64_t(g) * a.N + (in ? n : 0), s, t), c(a.Cm, r, int64_t(g) * a.N + (in ? n : 0), s, t) {}
-  // the tile's steps; those past the last one there, `end` - 1, repeat it
-  // (their step size is zero)
+  // the tile's steps; for those past the last one there, `end` - 1, its values
   __device__ __forceinline__ void next(int s, int end, Values& v) {
     int64_t ob[E], oc[E];
     if (s + STEPS <= end) {
@@ -259,12 +253,15 @@ struct BCWalk {
     b.p += b.one * BY;
     c.p += c.one * BY;
   }
-  __device__ __forceinline__ void put(const Values& v, float (*to)[2 * NP]) const {
+  // the tile that begins at s; zero where there is no step or no state (times a
+  // step size of zero, an infinite B or C would make a state NaN)
+  __device__ __forceinline__ void put(const Values& v, int s, int end, float (*to)[2 * NP]) const {
     float* p = &to[t][n / NS * 2 * NS + n % NS];
 #pragma unroll
     for (int k = 0; k < E; ++k) {
-      p[k * EVERY * 2 * NP] = in ? float(v.b[k]) : 0.f;
-      p[k * EVERY * 2 * NP + NS] = in ? float(v.c[k]) : 0.f;
+      const bool is = in && s + t + k * EVERY < end;
+      p[k * EVERY * 2 * NP] = is ? float(v.b[k]) : 0.f;
+      p[k * EVERY * 2 * NP + NS] = is ? float(v.c[k]) : 0.f;
     }
   }
 };

@@ -156,7 +156,7 @@ __global__ __launch_bounds__(NW * 64) void scan_ahead_kernel(ScanArgs a) {
         dg[buf][k.t][k.q + i] = there ? g[i] : 0.f;
       }
     }
-    BC.put(nbc[j], sbc[buf]);
+    BC.put(nbc[j], s, send, sbc[buf]);
   };
   const int64_t seg0 = int64_t(b) * a.nseg;
   each<D>([&](auto J) { fetch(s0 + decltype(J)::value * TT, J); });
@@ -315,7 +315,7 @@ __global__ __launch_bounds__(NW * 64) void scan_back_kernel(ScanArgs a) {
         d[i] = there ? d[i] : 0.f;
         in[k.t][k.q + i] = make_float4(d[i], d[i] * x[i], gy[i], 0.f);
       }
-      BC.put(nbc, sbc);
+      BC.put(nbc, s, send, sbc);
 #pragma unroll
       for (int i = 0; i < NS; ++i) {
         h0[i] = p.ok ? nh[i] : 0.f;

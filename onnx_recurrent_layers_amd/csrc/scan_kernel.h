@@ -122,7 +122,7 @@ __global__ __launch_bounds__(NW * 64) void scan_kernel(ScanArgs a) {
         d[i] = there ? d[i] : 0.f;
         du[buf][k.t][k.q + i] = make_float2(d[i], there ? d[i] * px[i] : 0.f);
       }
-      BC.put(nbc[j], sbc[buf]);
+      BC.put(nbc[j], s, send, sbc[buf]);
     };
     float ox[V] = {};
     Raw<T, V, VEC> oz = {};
@@ -134,7 +134,7 @@ __global__ __launch_bounds__(NW * 64) void scan_kernel(ScanArgs a) {
         for (int i = 0; i < V; ++i) y[i] = skip[i] * ox[i];
 #pragma unroll
         for (int j = 0; j < NW; ++j) {
-                    const Pack<float, V> v = *reinterpret_cast<const Pack<float, V>*>(&part[buf][j][k.t][k.q]);
+          const Pack<float, V> v = *reinterpret_cast<const Pack<float, V>*>(&part[buf][j][k.t][k.q]);
 #pragma unroll
           for (int i = 0; i < V; ++i) y[i] += v.v[i];
         }

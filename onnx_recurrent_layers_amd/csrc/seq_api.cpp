@@ -647,6 +647,8 @@ extern "C" int rnn_norm_create(const rnn_norm_desc* desc, rnn_norm** out) {
   // partial sums of dScale and dB: two workgroups a compute unit, but four
   // rows at least for each
   n->parts = int(std::max<int64_t>(1, std::min<int64_t>(512, ceil_div(d.rows, 4))));
+  // rows too long for a workgroup's registers: workgroups of 64 columns besides
+  if (d.size > 8192) n->parts = int(std::max<int64_t>(1, std::min<int64_t>(n->parts, ceil_div(2048, ceil_div(d.size, 64)))));
   Regions r;
   r.take({n->parts, 2, d.size, 4});
   n->backward_bytes = r.off;

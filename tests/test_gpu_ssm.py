@@ -373,6 +373,31 @@ def test_scan_extreme_steps():
     assert bad[3:, 2].all() and not bad[:3].any() and bad.sum() == s - 3
 
 
+@pytest.mark.parametrize("b,c,groups", [(40, 450, 1), (257, 24, 2), (256, 66, 1), (40, 448, 7)])
+def test_scan_many_rows_of_unequal_length(b, c, groups):
+    """More workgroups than compute units: rows in the order of their lengths (up to 256 of them), ties and empty ones
+    among them."""
+    lens = [(7 * i) % 23 - 1 for i in range(b)]
+    scan_case("f32", b, 21, c, 3, groups, lens=lens, dead=float("nan"), backward=b == 40)
+
+
+@pytest.mark.parametrize("s", [3, 5, 17, 40])
+def test_scan_infinite_last_step(s):
+    """An infinite B at a row's last step makes that channel's states infinite, not NaN, wherever the step lies in a tile;
+    an infinite C touches no state."""
+    b, c, n = 2, 6, 4
+    v = scan_values("f32", b, s, c, n, 1, True)
+    lens = [s, s - 1]
+    for i in range(b):
+        v["B"][i, lens[i] - 1, 1] = float("inf")
+        v["C"][i, lens[i] - 1, 2] = float("inf")
+        v["X"][i, lens[i] - 1] = v["X"][i, lens[i] - 1].abs() + 0.1
+    t = scan_tensors(v, torch.float32, 0, s, v["init"].float().cuda(), sequence_lens=torch.tensor(lens, dtype=torch.int32).cuda())
+    rl.SelectiveScan(dtype="f32", seq=s, batch=b, channels=c, state=n).encode(t)
+    h = t["final_state"].cpu()
+    assert (h[:, :, 1] == float("inf")).all() and h[:, :, [0, 2, 3]].isfinite().all()
+
+
 # --------------------------------------------------------- layer normalization
 
 def norm_case(dtype, rows, size, shift=True, pad=0, odd=0, seed=0, far=0.0):
@@ -424,6 +449,12 @@ def norm_case(dtype, rows, size, shift=True, pad=0, odd=0, seed=0, far=0.0):
 @pytest.mark.parametrize("size", [1, 7, 64, 100, 128, 129, 256, 500, 512, 1000, 1024, 2048, 2056, 4096, 5001, 8192, 8200])
 def test_norm_sizes(dtype, size):
     norm_case(dtype, 5, size)
+
+
+@pytest.mark.parametrize("dtype,rows,size", [("bf16", 37, 16384), ("f32", 600, 9001), ("f16", 1, 70000)])
+def test_norm_long_rows(dtype, rows, size):
+    """Rows that a workgroup's registers do not hold."""
+    norm_case(dtype, rows, size)
 
 
 @pytest.mark.parametrize("rows", [0, 1, 3, 17, 515, 2100])
