@@ -346,8 +346,8 @@ int rnn_read_run_status(const rnn_problem* problem, const void* state_scratch, v
  * output may overlap an input or another output.
  *
  * Limits (RNN_ERR_UNSUPPORTED): channels above 2^24, batch or seq above 2^30,
- * a grid above 2^31 - 1 workgroups.  A tensor or a scratch above 2^52 bytes is
- * RNN_ERR_SHAPE. */
+ * sizes whose launch would hold 2^32 threads or more.  A tensor or a scratch
+ * above 2^52 bytes is RNN_ERR_SHAPE. */
 typedef struct {
   void* ptr;           /* device pointer, or NULL for an absent tensor */
   int64_t elem_offset; /* >= 0, in elements of the tensor's type */
@@ -409,7 +409,7 @@ int rnn_conv_encode_backward(const rnn_conv* conv, const rnn_conv_operands* oper
  *   h_s[c,n] = exp(d_s[c] * A[c,n]) * h_{s-1}[c,n] + d_s[c] * x_s[c] * B_s[g,n]
  *   y_s[c]   = sum_n C_s[g,n] * h_s[c,n] + D[c] * x_s[c]
  *   Y_s[c]   = y_s[c], or y_s[c] * z_s[c] * sigmoid(z_s[c]) when Z is given
- * with channel c in group g = c / (channels / groups). */
+ * with channel c in group g = c / (channels / groups).  A is finite. */
 typedef struct {
   int32_t dtype;           /* rnn_dtype of the row tensors */
   int32_t direction;       /* RNN_DIR_FORWARD or RNN_DIR_REVERSE */
@@ -439,8 +439,8 @@ typedef struct {
   rnn_tensor final_state;    /* [batch, C, N] f32       optional output (forward only) */
 } rnn_scan_operands;
 
-/* Gradients; states and y are computed again from the inputs.  dD needs D
- * only in its use (it may be asked for without one), dZ needs Z. */
+/* Gradients; states and y are computed again from the inputs.  dD may be
+ * asked for without D; dZ needs Z. */
 typedef struct {
   rnn_rows dY;                 /* [C] a row             required */
   rnn_tensor d_final_state;    /* [batch, C, N] f32     optional (zeros) */

@@ -7,7 +7,13 @@
 // forward, 4 channels backward) with the last K inputs in registers: each
 // element is read once but for the K-1 steps before a tile, which the cache
 // holds (the tile before has just read them).  Eight steps' loads are in
-// flight at once.
+// flight at once.  (8 rows of 1024 steps by 2048 channels, 4 taps, 16 bits: all
+// steps there 18.0 us for 67 MB, which is a copy's rate; its gradient 30.4 us
+// for 100 MB, at 41 vector instructions an element before the way without
+// questions, and 4.7 for the sums of 128 partials; 64 single tokens 5.3 us, the
+// time that a launch of any kind takes here, not their 2 MB.)
+#include <type_traits>
+
 #include "seq_device.h"
 
 namespace rnnhip {
@@ -143,7 +149,7 @@ __global__ __launch_bounds__(256) void conv_backward_kernel(ConvArgs a) {
   const int cb = int(blockIdx.x) % a.ncb;
   const int rest = int(blockIdx.x) / a.ncb;
   const int b = rest / a.ntb;
-  const int ty = int(threadIdx.x) >> 6, tx = int(threadIdx.x) & 63;
+  const int ty = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6), tx = int(threadIdx.x) & 63;   // (a wave's tile)
   const int tile = (rest % a.ntb) * 4 + ty;
   const int c = (cb * 64 + tx) * V;
   const int s0 = tile * a.tile;
@@ -207,63 +213,71 @@ __global__ __launch_bounds__(256) void conv_backward_kernel(ConvArgs a) {
       xp += 4 * xd;
       gp += 4 * gd;
       if (s + 4 < L && s + 4 - K + 1 < e1) fetch(s + 4);
+      // WHOLE: steps of this tile, and inputs that are its own and not the final
+      // state's, which leaves four steps without a question asked (measured:
+      // 32.3 us, with the questions 35.1)
+      auto four = [&](auto whole) {
+        constexpr bool WHOLE = decltype(whole)::value;
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int st = s + u;
-        const bool live = st < L;
-        const bool mine = st < send;
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-#pragma unroll
-          for (int j = 0; j < K - 1; ++j) dp[j][i] = dp[j + 1][i];
-          float x = 0.f, d = 0.f;
-          if (live) {
-            x = float(in[u].v[i]);
-            d = float(gin[u].v[i]);
-            if (a.silu) {
-              float p = bias[i];
-#pragma unroll
-              for (int j = 0; j < K - 1; ++j) p = __builtin_fmaf(w[j][i], win[j][i], p);
-              p = __builtin_fmaf(w[K - 1][i], x, p);
-              const float sg = logistic(p);
-              d *= sg * __builtin_fmaf(p, 1.f - sg, 1.f);
-            }
-          }
-          dp[K - 1][i] = d;
-          if (mine) {
-#pragma unroll
-            for (int j = 0; j < K - 1; ++j) dw[j][i] = __builtin_fmaf(d, win[j][i], dw[j][i]);
-            dw[K - 1][i] = __builtin_fmaf(d, x, dw[K - 1][i]);
-            db[i] += d;
-          }
-#pragma unroll
-          for (int j = 0; j + 1 < K - 1; ++j) win[j][i] = win[j + 1][i];
-          win[K - 2][i] = x;
-        }
-        const int e = st - K + 1;
-        if (e >= e0 && e < e1) {
-          float dx[V];
+        for (int u = 0; u < 4; ++u) {
+          const int st = s + u;
+          const bool live = WHOLE || st < L;
+          const bool mine = WHOLE || st < send;
 #pragma unroll
           for (int i = 0; i < V; ++i) {
-            float v = 0.f;
 #pragma unroll
-            for (int j = 0; j < K; ++j) v = __builtin_fmaf(w[K - 1 - j][i], dp[j][i], v);
-            dx[i] = v;
-          }
-          const int f = e - (L - K + 1);   // its place in the final state
-          if (dfin && f >= 0) {
-            float t[V];
-            load_v<T, V>(dfin + int64_t(f) * a.C, t);
+            for (int j = 0; j < K - 1; ++j) dp[j][i] = dp[j + 1][i];
+            float x = 0.f, d = 0.f;
+            if (live) {
+              x = float(in[u].v[i]);
+              d = float(gin[u].v[i]);
+              if (a.silu) {
+                float p = bias[i];
 #pragma unroll
-            for (int i = 0; i < V; ++i) dx[i] += t[i];
+                for (int j = 0; j < K - 1; ++j) p = __builtin_fmaf(w[j][i], win[j][i], p);
+                p = __builtin_fmaf(w[K - 1][i], x, p);
+                const float sg = logistic(p);
+                d *= sg * __builtin_fmaf(p, 1.f - sg, 1.f);
+              }
+            }
+            dp[K - 1][i] = d;
+            if (mine) {
+#pragma unroll
+              for (int j = 0; j < K - 1; ++j) dw[j][i] = __builtin_fmaf(d, win[j][i], dw[j][i]);
+              dw[K - 1][i] = __builtin_fmaf(d, x, dw[K - 1][i]);
+              db[i] += d;
+            }
+#pragma unroll
+            for (int j = 0; j + 1 < K - 1; ++j) win[j][i] = win[j + 1][i];
+            win[K - 2][i] = x;
           }
-          if (e >= 0) {
-            if (a.dX.p) store_v<T, V>(reinterpret_cast<T*>(a.dX.p) + c + (r.base + e * r.step) * a.dX.rs, dx);
-          } else if (a.dinit) {
-            store_v<T, V>(reinterpret_cast<T*>(a.dinit) + sb + int64_t(e + K - 1) * a.C, dx);
+          const int e = st - K + 1;
+          if (WHOLE || (e >= e0 && e < e1)) {
+            float dx[V];
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+              float v = 0.f;
+#pragma unroll
+              for (int j = 0; j < K; ++j) v = __builtin_fmaf(w[K - 1 - j][i], dp[j][i], v);
+              dx[i] = v;
+            }
+            const int f = e - (L - K + 1);   // its place in the final state
+            if (!WHOLE && dfin && f >= 0) {
+              float t[V];
+              load_v<T, V>(dfin + int64_t(f) * a.C, t);
+#pragma unroll
+              for (int i = 0; i < V; ++i) dx[i] += t[i];
+            }
+            if (WHOLE || e >= 0) {
+              if (a.dX.p) store_v<T, V>(reinterpret_cast<T*>(a.dX.p) + c + (r.base + e * r.step) * a.dX.rs, dx);
+            } else if (a.dinit) {
+              store_v<T, V>(reinterpret_cast<T*>(a.dinit) + sb + int64_t(e + K - 1) * a.C, dx);
+            }
           }
         }
-      }
+      };
+      if (s - K + 1 >= max(e0, 0) && s + 3 < send && s + 3 < L - K + 1) four(std::true_type{});
+      else four(std::false_type{});
     }
     if (a.dX.p) {
       float zero[V] = {};

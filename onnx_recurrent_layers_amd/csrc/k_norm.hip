@@ -11,7 +11,10 @@
 //
 // A row is taken by W threads (a part of a wave, or a workgroup), V
 // neighbouring values a time (16 bytes where rows and stride allow), M times;
-// rows too long for registers are read again for each use.
+// rows too long for registers are read again for each use.  (8192 rows of 2048,
+// 16 bits: forward 16.0 us for 67 MB, a copy's rate; gradient 25.1 us for 101 MB
+// and 4.0 for the sums of 512 partials, where 1024 partials took as long, 27.6
+// us together against 27.3.  64 rows of 1024, f32: 3.2 us.)
 #include "seq_device.h"
 
 namespace rnnhip {

@@ -71,7 +71,8 @@ __device__ __forceinline__ ScanPlace scan_place(const ScanArgs& a, int nchunk, i
   p.ch = rest % nchunk;
   p.b = rest / nchunk;
   // Rows of unequal length: by falling length, and with every second round
-  // turned a compute unit that got a long row gets a short one next.
+  // turned a compute unit that got a long row gets a short one next.  (16 rows
+  // of all lengths up to 1024 by 2048 channels: 125.6 us, as stored 147.6.)
   if (a.balance) p.b = scan_row_of_rank(a, p.b);
   p.g = p.cb / a.cbg;
   const int in = (p.cb % a.cbg) * 64 + lane;

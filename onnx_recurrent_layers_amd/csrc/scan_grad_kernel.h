@@ -8,7 +8,7 @@
 //   dx_s = d_s sum_n G_s B_s + D gy_s;           dB_s = sum_c G_s u_s
 //   dC_s = sum_c gy_s h_s;  dD = sum gy_s x_s;   dz_s = dY y_s silu'(z)
 //   d_initial = a_0 G_0
-// Nothing of the forward pass is kept.  After B and C in f32, three launches:
+// Nothing of the forward pass is kept.  Three launches:
 //   1. along time: states, written before each segment of 16 steps (fewer with
 //      many states), and each chunk's end state, sum of step sizes and gradient
 //      at its start.  That gradient needs no walk back: sum_s (prod_{r<=s} a_r)
@@ -28,6 +28,14 @@
 // at once are folded over a wave's 64 lanes (Fold), each exchange halving what
 // is left: two to three instructions a value, where one sum after another
 // would take twelve, and no meeting of waves.
+//
+// 8 rows of 512 steps by 1024 channels, 16 states, bf16: launch 1 39.2 us,
+// launch 2 85.2, launch 3 4.7.  Launch 2 issues 27 vector instructions a (step,
+// channel, state) where the forward pass issues 9 (by the counters, which show
+// the vector units busy for 65 of 100 clocks), and its registers and 118 KB of
+// shared memory leave a compute unit one workgroup: these bound it, not its 60
+// MB.  Four waves of four states instead of eight of
+// two: 129 us the whole pass at best against 123.
 #pragma once
 
 #include "scan_device.h"

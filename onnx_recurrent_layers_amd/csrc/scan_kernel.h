@@ -8,29 +8,36 @@
 // exponential is the hardware's 2^x.  With 16 states and more these
 // instructions bound a layer, with fewer and for few steps memory does.
 //
-// Why a lane a channel and the states over the waves: measured on register-only
-// loops of the five instructions, 64 of them take 20.8 clocks of a SIMD where B
-// and C are scalar operands and 28.8 where they are vector registers (three
-// vector operands an instruction cost more than two), and a wave alone on its
-// SIMD issues at half the rate of two.  So B and C are the same for a whole
-// wave (a launch before writes them in f32, and scalar loads fetch them a stage
-// ahead), and a workgroup of 64 channels is 4 or 8 waves: with 8, 256
-// workgroups already give each SIMD two.  Four lanes of a wave to a channel, B
-// and C from shared memory, took 186 us for 16 rows of 1024 steps by 2048
-// channels with 16 states (the figures now: below).
+// Why a lane a channel and the states over the waves: the five instructions in
+// a loop of registers take a SIMD 28.8 clocks for a wave's 64 (step, channel,
+// state) with two waves on it or more, 32.5 with one, which is nearly alone in
+// waiting for each result; a workgroup of 64 channels by 4 to 8 waves fills a
+// chip of 1024 SIMDs with the fewest rows.  And a wave's lanes share B and C
+// then, which cost it one register a 16 values instead of a read of shared
+// memory an operand (BCRegs).  For 16 rows of 1024 steps by 2048 channels, 16
+// states, bf16, rows of all lengths up to it: four lanes of a wave to a channel
+// with B and C read from shared memory 186 us (154 with rows in order of
+// length), B and C by scalar loads 148, this with an element a load 138, with
+// packs of four channels a load 118 (rows of full length: 168, 1.7 times the
+// bare loop's time, the rest being softplus, gate, sums of parts and barriers;
+// counters show the vector units busy for 80 of 100 clocks).  Sixteen states
+// on eight waves take 150 forward: each wave does the tile's fixed work for
+// half as many states.
 //
-// A tile is 16 steps.  Each wave prepares every NW-th of them (loads, softplus)
-// and puts step size and input into shared memory; all waves run the tile's
-// steps on their states and put their parts of y there; each wave then sums,
-// gates and stores the steps that it prepared.  One barrier a tile: the next
-// tile's preparation and the last tile's outputs come between barrier and
-// steps, in the other halves of the buffers.
+// A tile is 16 steps.  Each thread prepares its part of it, 4 neighbouring
+// channels of a step (Task: loads, softplus), and puts step size and input into
+// shared memory; all waves run the tile's steps on their states and put their
+// parts of y there; each thread then sums, gates and stores what it prepared.
+// One barrier a tile: the next tile's preparation and the last tile's outputs
+// come between barrier and steps, in the other halves of the buffers.
 //
 // Few rows: the time axis is cut into chunks.  A first launch gives each
 // chunk's end state from a zero state and its sum of step sizes (the decay
 // over a chunk is exp(A * sum)); the second joins them at its start.  That
 // costs the recurrence twice, so it is done only where the chunks fill a chip
-// that the rows alone leave empty (rule in seq_api.cpp).
+// that the rows alone leave empty (rule in seq_api.cpp).  (1 row of 4096 steps
+// by 2048 channels, 16 states, f16: 39.3 us of the first launch and 53.4 of the
+// second under a profiler, 87 together without.)
 #pragma once
 
 #include "scan_device.h"

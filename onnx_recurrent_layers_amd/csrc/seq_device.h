@@ -109,10 +109,4 @@ __device__ __forceinline__ float quad_sum4(float a0, float a1, float a2, float a
   return (q2 ? r1 : r0) + quad_x2(q2 ? r0 : r1);
 }
 
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int m = 32; m >= 1; m >>= 1) v += __shfl_xor(v, m, 64);
-  return v;
-}
-
 }  // namespace rnnhip
