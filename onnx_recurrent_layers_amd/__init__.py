@@ -428,7 +428,8 @@ class _Operator:
     one's shape, type and device are checked.  Sequence tensors may be views
     whose rows lie a constant stride apart (a slice of a wider projection); the
     others have to be contiguous.  Calls that overlap in time need an object
-    each, since an object holds one scratch (so do graphs that replay at once)."""
+    each, since an object holds one scratch (so do graphs that replay at once),
+    and an object is kept for as long as a graph replays its calls."""
 
     op = ""             # the C functions' middle name
     who = ""            # the name in messages
@@ -462,7 +463,13 @@ class _Operator:
         self._grads = layout(self._gradients, self.gradient_names)
         self._forward_scratch = self._backward_scratch = None
         if self.forward_bytes:
-            self._forward_scratch = torch.empty(self.forward_bytes, dtype=torch.uint8, device=self.device)
+            self._forward_scratch = self._new_scratch(self.forward_bytes)
+
+    def _new_scratch(self, size):
+        """Scratch and the stream that the allocator counts it to."""
+        import torch
+        return (torch.empty(size, dtype=torch.uint8, device=self.device),
+                torch.cuda.current_stream(self.device).cuda_stream if self.device.type == "cuda" else 0)
 
     def _bad(self, code, text):
         return RnnError(code, f"{self.who}: {text}")
@@ -510,9 +517,14 @@ class _Operator:
     def _call(self, encode, structs, scratch, stream):
         import torch
         st = stream if stream is not None else torch.cuda.current_stream(self.device)
-        if scratch is not None and st.cuda_stream and not torch.cuda.is_current_stream_capturing():
-            scratch.record_stream(st)   # (not reused, once this object is gone, before the call has run)
-        ptr = scratch.data_ptr() if scratch is not None else None
+        if st.device.index != self._index:
+            raise self._bad(RNN_ERR_ARG, f"stream: on {st.device}, expected {self.device}")
+        ptr = None
+        if scratch is not None:
+            memory, home = scratch
+            ptr = memory.data_ptr()
+            if st.cuda_stream != home and not torch.cuda.is_current_stream_capturing():
+                memory.record_stream(st)   # (not reused, once this object is gone, before the call has run)
         if torch.cuda.current_device() == self._index:
             _check(encode(self._handle, *structs, ptr, st.cuda_stream or None))
         else:
@@ -537,7 +549,7 @@ class _Operator:
         if self._backward_scratch is None and self.backward_bytes:
             if torch.cuda.is_current_stream_capturing():
                 raise self._bad(RNN_ERR_ARG, "scratch: call backward once before a graph captures it")
-            self._backward_scratch = torch.empty(self.backward_bytes, dtype=torch.uint8, device=self.device)
+            self._backward_scratch = self._new_scratch(self.backward_bytes)
         self._call(self._encode_backward, (ops, grads), self._backward_scratch, stream)
 
     def __del__(self):

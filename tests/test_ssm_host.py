@@ -240,3 +240,10 @@ def test_binding_refuses_tensors(scan):
     assert (ops.X.ptr, ops.X.elem_offset, ops.X.row_stride) == (x.data_ptr(), 0, 20) and ops.delta.ptr is None
     scan._index = 0
     refused(fill(), ARG, "scan: ", "X: on cpu")
+
+
+def test_binding_refuses_another_devices_stream(scan):
+    class Stream:
+        device, cuda_stream = torch.device("cuda", 1), 0
+
+    refused(lambda: scan.encode({"X": torch.zeros(3, 4, 6)}, Stream()), ARG, "scan: ", "stream: on cuda:1, expected cuda:0")
