@@ -12,7 +12,7 @@
 // A row is taken by W threads (a part of a wave, or a workgroup), V
 // neighbouring values a time (16 bytes where rows and stride allow), M times;
 // rows too long for registers are read again for each use.  (8192 rows of 2048,
-// 16 bits: forward 16.0 us for 67 MB, a copy's rate; gradient 25.1 us for 101 MB
+// 16 bits: forward 14.0 us for 67 MB, a copy's rate; gradient 25.1 us for 101 MB
 // and 4.0 for the sums of 512 partials, where 1024 partials took as long, 27.6
 // us together against 27.3.  64 rows of 1024, f32: 3.2 us.)
 #include "seq_device.h"
@@ -149,7 +149,7 @@ __global__ __launch_bounds__(256) void norm_kernel(NormArgs a) {
 // time) in steps of the grid.  M = 0: long rows; dX here, dScale and dB by
 // norm_columns_kernel.
 template <typename T, int W, int V, int M>
-__global__ __launch_bounds__(256) void norm_backward_kernel(NormArgs a) {
+__global__ __launch_bounds__(256, 2) void norm_backward_kernel(NormArgs a) {
   __shared__ float lds[2][16];
   constexpr int RB = 256 / W;
   constexpr int R = M > 0 ? M : 1;
@@ -329,8 +329,13 @@ __global__ __launch_bounds__(1024) void colsum_kernel(ColSumArgs a) {
   }
 }
 
-// The threads of a row and its shares: the least that hold the row in
-// registers with at most MAXM shares a thread.
+// The threads of a row and its shares: the least threads that hold the row in
+// registers.  Many rows: a wave of up to 3 shares a lane (forward 4), since
+// rows then need no meeting of waves and fewer lanes idle (16 bits, forward and
+// backward: 65536 rows of 1280 67 and 103 us, with a workgroup a row 104 and
+// 179; 8192 of 1536 11.1 and 20.7, 13.3 and 25.5; 8192 of 2048 13.7 forward,
+// 15.4; but backward, its registers full, 16384 of 2048 49, 46.8).  With few
+// rows compute units would idle so (64 rows of 1024 f32: 8.9 us, 8.4).
 template <typename T, int V, template <typename, int, int, int> class F>
 hipError_t norm_shape(const NormArgs& a, hipStream_t s) {
   const int n = (a.size + V - 1) / V;   // shares
@@ -338,6 +343,8 @@ hipError_t norm_shape(const NormArgs& a, hipStream_t s) {
   if (n <= 32) return F<T, 32, V, 1>::run(a, s);
   if (n <= 64) return F<T, 64, V, 1>::run(a, s);
   if (n <= 128) return F<T, 64, V, 2>::run(a, s);
+  if (n <= 192 && a.rows >= 1024) return F<T, 64, V, 3>::run(a, s);
+  if (n <= 256 && a.rows >= 4096 && !a.dY.p) return F<T, 64, V, 4>::run(a, s);
   if (n <= 256) return F<T, 256, V, 1>::run(a, s);
   if (n <= 512) return F<T, 256, V, 2>::run(a, s);
   if (n <= 1024) return F<T, 256, V, 4>::run(a, s);

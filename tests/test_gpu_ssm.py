@@ -457,6 +457,13 @@ def test_norm_long_rows(dtype, rows, size):
     norm_case(dtype, rows, size)
 
 
+@pytest.mark.parametrize("dtype,rows,size", [("bf16", 4099, 2048), ("f32", 4096, 250), ("f16", 1027, 1290), ("f32", 1024, 640),
+                                              ("bf16", 1025, 190)])
+def test_norm_many_rows(dtype, rows, size):
+    """Rows of a wave each."""
+    norm_case(dtype, rows, size)
+
+
 @pytest.mark.parametrize("rows", [0, 1, 3, 17, 515, 2100])
 @pytest.mark.parametrize("size,pad,odd", [(64, 0, 0), (96, 32, 0), (33, 2, 1), (1032, 8, 0)])
 def test_norm_rows(rows, size, pad, odd):
