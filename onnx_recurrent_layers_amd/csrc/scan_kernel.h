@@ -18,11 +18,12 @@
 // states, bf16, rows of all lengths up to it: four lanes of a wave to a channel
 // with B and C read from shared memory 186 us (154 with rows in order of
 // length), B and C by scalar loads 148, this with an element a load 138, with
-// packs of four channels a load 118 (rows of full length: 168, 1.7 times the
+// packs of four channels a load 117 to 124 (rows of full length: 168, 1.7 times the
 // bare loop's time, the rest being softplus, gate, sums of parts and barriers;
 // counters show the vector units busy for 80 of 100 clocks).  Sixteen states
-// on eight waves take 150 forward: each wave does the tile's fixed work for
-// half as many states.
+// on eight waves take 172 where four take 124, each wave doing the tile's fixed
+// work for half as many states; only with one workgroup a compute unit or less
+// do they win (8 rows 103 and 114).
 //
 // A tile is 16 steps.  Each thread prepares its part of it, 4 neighbouring
 // channels of a step (Task: loads, softplus), and puts step size and input into
