@@ -20,7 +20,9 @@
 namespace rnnhip {
 namespace {
 
-// Sums of N values over the W threads of a row; all threads get them.
+// Sums of N values over the W threads of a row; all threads get them.  Calls
+// one after another take two places in turn: whoever writes a place again has
+// passed the barrier of the call between, after which all had read it.
 template <int W, int N>
 __device__ __forceinline__ void row_sums(float (&v)[N], float (*lds)[16]) {
   constexpr int M = W < 64 ? W : 64;
@@ -30,7 +32,6 @@ __device__ __forceinline__ void row_sums(float (&v)[N], float (*lds)[16]) {
     for (int n = 0; n < N; ++n) v[n] += __shfl_xor(v[n], m, 64);
   if constexpr (W > 64) {
     const int w = int(threadIdx.x) >> 6;
-    __syncthreads();
     if ((threadIdx.x & 63) == 0)
 #pragma unroll
       for (int n = 0; n < N; ++n) lds[n][w] = v[n];
@@ -62,7 +63,7 @@ __device__ __forceinline__ void put(T* p, const float (&v)[V]) {
 // M = 0: the row is read three times.
 template <typename T, int W, int V, int M>
 __global__ __launch_bounds__(256) void norm_kernel(NormArgs a) {
-  __shared__ float lds[1][16];
+  __shared__ float lds[2][1][16];
   const int64_t row = int64_t(blockIdx.x) * (256 / W) + int(threadIdx.x) / W;
   const int t = int(threadIdx.x) % W;
   const bool in = row < a.rows;   // (uniform where a row takes the whole workgroup)
@@ -93,7 +94,7 @@ __global__ __launch_bounds__(256) void norm_kernel(NormArgs a) {
       for (int i = 0; i < V; ++i) v[0] += x[0][i];
     }
   }
-  row_sums<W, 1>(v, lds);
+  row_sums<W, 1>(v, lds[0]);
   const float mean = v[0] * per;
   v[0] = 0.f;
   if constexpr (M > 0) {
@@ -113,7 +114,7 @@ __global__ __launch_bounds__(256) void norm_kernel(NormArgs a) {
       for (int i = 0; i < V; ++i) v[0] = __builtin_fmaf(x[0][i] - mean, x[0][i] - mean, v[0]);
     }
   }
-  row_sums<W, 1>(v, lds);
+  row_sums<W, 1>(v, lds[1]);
   const float inv = 1.f / __builtin_sqrtf(__builtin_fmaf(v[0], per, a.eps));
   if (!in) return;
   if (t == 0) {
@@ -150,7 +151,7 @@ __global__ __launch_bounds__(256) void norm_kernel(NormArgs a) {
 // norm_columns_kernel.
 template <typename T, int W, int V, int M>
 __global__ __launch_bounds__(256, 2) void norm_backward_kernel(NormArgs a) {
-  __shared__ float lds[2][16];
+  __shared__ float lds[2][2][16];
   constexpr int RB = 256 / W;
   constexpr int R = M > 0 ? M : 1;
   const int t = int(threadIdx.x) % W, slot = int(threadIdx.x) / W;
@@ -182,7 +183,8 @@ __global__ __launch_bounds__(256, 2) void norm_backward_kernel(NormArgs a) {
     pi = a.inv[at];
   };
   if (M > 0 && int64_t(blockIdx.x) * RB < a.rows) fetch(int64_t(blockIdx.x) * RB + slot);
-  for (int64_t r0 = int64_t(blockIdx.x) * RB; r0 < a.rows; r0 += by) {
+  int place = 0;
+  for (int64_t r0 = int64_t(blockIdx.x) * RB; r0 < a.rows; r0 += by, place ^= 1) {
     const int64_t row = r0 + slot;
     const bool in = row < a.rows;
     const int64_t at = in ? row : a.rows - 1;
@@ -207,7 +209,7 @@ __global__ __launch_bounds__(256, 2) void norm_backward_kernel(NormArgs a) {
       }
       if (r0 + by < a.rows) fetch(row + by);   // uniform
       if (a.dX.p) {
-        row_sums<W, 2>(v, lds);
+        row_sums<W, 2>(v, lds[place]);
         const float m0 = v[0] * per, m1 = v[1] * per;
 #pragma unroll
         for (int m = 0; m < M; ++m) {
@@ -236,7 +238,7 @@ __global__ __launch_bounds__(256, 2) void norm_backward_kernel(NormArgs a) {
           v[1] = __builtin_fmaf(gs, (x[i] - mean) * inv, v[1]);
         }
       }
-      row_sums<W, 2>(v, lds);
+      row_sums<W, 2>(v, lds[place]);
       const float m0 = v[0] * per, m1 = v[1] * per;
       for (int c = t * V; c < a.size; c += W * V) {
         float x[V], g[V], s[V];
