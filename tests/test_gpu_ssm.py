@@ -381,6 +381,24 @@ def test_scan_many_rows_of_unequal_length(b, c, groups):
     scan_case("f32", b, 21, c, 3, groups, lens=lens, dead=float("nan"), backward=b == 40)
 
 
+@pytest.mark.parametrize("s,lens", [(1, [0, 1, -3, 1, 7]), (2, [2, 0, 1, 1, 2]), (4, [4, 3, 0, 2, 1])])
+@pytest.mark.parametrize("n,c,groups,odd,carried,reverse", [(16, 64, 1, 0, True, False), (16, 66, 2, 1, False, True),
+                                                            (64, 20, 1, 0, True, True), (128, 12, 1, 0, False, False),
+                                                            (3, 70, 1, 0, True, True), (100, 5, 1, 1, True, False)])
+def test_scan_few_steps_of_unequal_length(s, lens, n, c, groups, odd, carried, reverse):
+    """Tokens, some rows without one: whole aligned states and others."""
+    for layout in (0, 1):
+        scan_case("bf16", 5, s, c, n, groups, layout=layout, reverse=reverse, lens=lens, carried=carried, odd=odd,
+                  dead=float("nan"), backward=layout == 0)
+
+
+@pytest.mark.parametrize("k,act", [(2, True), (4, False), (5, True), (8, True)])
+@pytest.mark.parametrize("lens", [None, [150, 16, 17, 0, 33]])
+def test_conv_gradient_inside_tiles(k, act, lens):
+    """Rows of many whole tiles, ends at and beside a tile's."""
+    conv_case("f32", 5, 150, 12, k, lens=lens, act=act, dead=float("nan"))
+
+
 @pytest.mark.parametrize("s", [3, 5, 17, 40])
 def test_scan_infinite_last_step(s):
     """An infinite B at a row's last step makes that channel's states infinite, not NaN, wherever the step lies in a tile;
