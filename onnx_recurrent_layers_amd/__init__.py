@@ -516,20 +516,24 @@ class _Operator:
 
     def _call(self, encode, structs, scratch, stream):
         import torch
-        st = stream if stream is not None else torch.cuda.current_stream(self.device)
-        if st.device.index != self._index:
-            raise self._bad(RNN_ERR_ARG, f"stream: on {st.device}, expected {self.device}")
+        if stream is None:
+            raw = torch._C._cuda_getCurrentRawStream(self._index)   # (the handle alone: a Stream object takes 1.8 us)
+        else:
+            if stream.device.index != self._index:
+                raise self._bad(RNN_ERR_ARG, f"stream: on {stream.device}, expected {self.device}")
+            raw = stream.cuda_stream
         ptr = None
         if scratch is not None:
             memory, home = scratch
             ptr = memory.data_ptr()
-            if st.cuda_stream != home and not torch.cuda.is_current_stream_capturing():
-                memory.record_stream(st)   # (not reused, once this object is gone, before the call has run)
+            if raw != home and not torch.cuda.is_current_stream_capturing():
+                # (not reused, once this object is gone, before the call has run)
+                memory.record_stream(stream if stream is not None else torch.cuda.current_stream(self.device))
         if torch.cuda.current_device() == self._index:
-            _check(encode(self._handle, *structs, ptr, st.cuda_stream or None))
+            _check(encode(self._handle, *structs, ptr, raw or None))
         else:
             with torch.cuda.device(self.device):
-                _check(encode(self._handle, *structs, ptr, st.cuda_stream or None))
+                _check(encode(self._handle, *structs, ptr, raw or None))
 
     def _known(self, tensors):
         if not tensors.keys() <= self._specs.keys():
