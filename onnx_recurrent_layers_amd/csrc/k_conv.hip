@@ -10,8 +10,8 @@
 // flight at once.  (8 rows of 1024 steps by 2048 channels, 4 taps, 16 bits: all
 // steps there 18.0 us for 67 MB, which is a copy's rate; its gradient 30.4 us
 // for 100 MB, at 41 vector instructions an element before the way without
-// questions, and 4.7 for the sums of 128 partials; 64 single tokens 5.3 us, the
-// time that a launch of any kind takes here, not their 2 MB.)
+// questions, and 4.7 for the sums of 128 partials; 64 single tokens 5.3 us,
+// a few trips to memory one after another, not their 2 MB.)
 #include <type_traits>
 
 #include "seq_device.h"

@@ -29,13 +29,13 @@
 // is left: two to three instructions a value, where one sum after another
 // would take twelve, and no meeting of waves.
 //
-// 8 rows of 512 steps by 1024 channels, 16 states, bf16: launch 1 39.2 us,
-// launch 2 85.2, launch 3 4.7.  Launch 2 issues 27 vector instructions a (step,
+// 8 rows of 512 steps by 1024 channels, 16 states, bf16: launch 1 39.5 us,
+// launch 2 86, launch 3 4.8.  Launch 2 issues 27 vector instructions a (step,
 // channel, state) where the forward pass issues 9 (by the counters, which show
 // the vector units busy for 65 of 100 clocks), and its registers and 118 KB of
 // shared memory leave a compute unit one workgroup: these bound it, not its 60
-// MB.  Four waves of four states instead of eight of
-// two: 129 us the whole pass at best against 123.
+// MB.  Four waves of four states instead of eight of two: 129 us the whole pass
+// at best against 123.
 #pragma once
 
 #include "scan_device.h"
