@@ -423,7 +423,8 @@ def rnn_norm_encode_backward(handle, operands: rnn_norm_operands, gradients: rnn
 
 
 class _Operator:
-    """One created problem of the operators below plus its scratch, for repeated
+    """One created problem of the operators below plus its scratch (made by the
+    first call, forward and backward, on that call's stream), for repeated
     calls.  The tensors of a call are torch tensors keyed by the C names; each
     one's shape, type and device are checked.  Sequence tensors may be views
     whose rows lie a constant stride apart (a slice of a wider projection); the
@@ -462,14 +463,25 @@ class _Operator:
         self._inputs = layout(self._operands, self.input_names)
         self._grads = layout(self._gradients, self.gradient_names)
         self._forward_scratch = self._backward_scratch = None
-        if self.forward_bytes:
-            self._forward_scratch = self._new_scratch(self.forward_bytes)
 
-    def _new_scratch(self, size):
-        """Scratch and the stream that the allocator counts it to."""
+    def _new_scratch(self, size, stream, raw):
+        """Scratch and the stream that the allocator counts it to: the stream of
+        the first call that takes it.  What the allocator hands out may still be
+        in use by work queued on the stream that it counts the memory to (its
+        last holder's), so on that stream only it may be written at once; calls
+        after the first do not overlap with it."""
         import torch
-        return (torch.empty(size, dtype=torch.uint8, device=self.device),
-                torch.cuda.current_stream(self.device).cuda_stream if self.device.type == "cuda" else 0)
+        with torch.cuda.stream(stream):
+            return torch.empty(size, dtype=torch.uint8, device=self.device), raw
+
+    def _raw(self, stream):
+        """The handle of a call's stream."""
+        import torch
+        if stream is None:
+            return torch._C._cuda_getCurrentRawStream(self._index)   # (the handle alone: a Stream object takes 1.8 us)
+        if stream.device.index != self._index:
+            raise self._bad(RNN_ERR_ARG, f"stream: on {stream.device}, expected {self.device}")
+        return stream.cuda_stream
 
     def _bad(self, code, text):
         return RnnError(code, f"{self.who}: {text}")
@@ -514,19 +526,18 @@ class _Operator:
             raise self._bad(RNN_ERR_ARG, f"{name}: its rows overlap, stride {step}")
         return 0 if step is None else step
 
-    def _call(self, encode, structs, scratch, stream):
+    def _capturing(self, stream):
         import torch
-        if stream is None:
-            raw = torch._C._cuda_getCurrentRawStream(self._index)   # (the handle alone: a Stream object takes 1.8 us)
-        else:
-            if stream.device.index != self._index:
-                raise self._bad(RNN_ERR_ARG, f"stream: on {stream.device}, expected {self.device}")
-            raw = stream.cuda_stream
+        with torch.cuda.stream(stream):
+            return torch.cuda.is_current_stream_capturing()
+
+    def _call(self, encode, structs, scratch, stream, raw):
+        import torch
         ptr = None
         if scratch is not None:
             memory, home = scratch
             ptr = memory.data_ptr()
-            if raw != home and not torch.cuda.is_current_stream_capturing():
+            if raw != home and not self._capturing(stream):
                 # (not reused, once this object is gone, before the call has run)
                 memory.record_stream(stream if stream is not None else torch.cuda.current_stream(self.device))
         if torch.cuda.current_device() == self._index:
@@ -542,19 +553,21 @@ class _Operator:
     def encode(self, tensors: dict, stream=None) -> None:
         """Enqueue the operator on `stream` (default: the current one)."""
         self._known(tensors)
-        self._call(self._encode, (self._fill(self._forward, tensors),), self._forward_scratch, stream)
+        ops, raw = self._fill(self._forward, tensors), self._raw(stream)
+        if self._forward_scratch is None and self.forward_bytes:
+            self._forward_scratch = self._new_scratch(self.forward_bytes, stream, raw)
+        self._call(self._encode, (ops,), self._forward_scratch, stream, raw)
 
     def backward(self, tensors: dict, stream=None) -> None:
         """Enqueue the gradient.  `tensors` holds the forward pass's inputs too.
         The first call allocates its scratch, so it cannot be the captured one."""
-        import torch
         self._known(tensors)
-        ops, grads = self._fill(self._inputs, tensors), self._fill(self._grads, tensors)
+        ops, grads, raw = self._fill(self._inputs, tensors), self._fill(self._grads, tensors), self._raw(stream)
         if self._backward_scratch is None and self.backward_bytes:
-            if torch.cuda.is_current_stream_capturing():
+            if self._capturing(stream):
                 raise self._bad(RNN_ERR_ARG, "scratch: call backward once before a graph captures it")
-            self._backward_scratch = self._new_scratch(self.backward_bytes)
-        self._call(self._encode_backward, (ops, grads), self._backward_scratch, stream)
+            self._backward_scratch = self._new_scratch(self.backward_bytes, stream, raw)
+        self._call(self._encode_backward, (ops, grads), self._backward_scratch, stream, raw)
 
     def __del__(self):
         try:
