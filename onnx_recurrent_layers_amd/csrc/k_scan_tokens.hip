@@ -95,7 +95,8 @@ __global__ __launch_bounds__(256) void scan_tokens_kernel(ScanArgs a) {
       float v = 0.f;
 #pragma unroll
       for (int i = 0; i < NS; ++i) {
-        h[i] = __builtin_fmaf(__builtin_amdgcn_exp2f(dj * A[i]), h[i], uj * B.value(i, a.N, q));
+        const float next = __builtin_fmaf(__builtin_amdgcn_exp2f(dj * A[i]), h[i], uj * B.value(i, a.N, q));
+        h[i] = VEC || state_of<NS>(q, i) < a.N ? next : 0.f;   // (0 times an infinite step is not 0)
         v = __builtin_fmaf(h[i], C.value(i, a.N, q), v);
       }
       return v;

@@ -47,8 +47,10 @@ namespace rnnhip {
 namespace {
 
 // LOCAL: the first of two launches (end states and sums of all chunks but
-// each row's last); else the outputs.
-template <typename T, int NW, int NS, bool LOCAL, bool VEC>
+// each row's last); else the outputs.  PAD: there are states past N among a
+// wave's, which are kept zero in a step's y: their B and C are zero, but times
+// an infinite step or state that is not a number.
+template <typename T, int NW, int NS, bool LOCAL, bool VEC, bool PAD>
 __global__ __launch_bounds__(NW * 64) void scan_kernel(ScanArgs a) {
   constexpr int TT = kScanTile, D = 2;   // steps of a tile, tiles of rows in flight
   typedef Task<NW, TT> Mine;
@@ -182,7 +184,8 @@ __global__ __launch_bounds__(NW * 64) void scan_kernel(ScanArgs a) {
         const float2 f = du[buf][t][lane];
         each<NS>([&](auto I) {
           constexpr int i = decltype(I)::value;
-          h[i] = __builtin_fmaf(__builtin_amdgcn_exp2f(f.x * A[i]), h[i], bc_mul<at + i>(bc, f.y));
+          const float next = __builtin_fmaf(__builtin_amdgcn_exp2f(f.x * A[i]), h[i], bc_mul<at + i>(bc, f.y));
+          h[i] = PAD && n0 + i >= a.N ? 0.f : next;   // (uniform)
         });
         if constexpr (LOCAL) {
           total += f.x;
@@ -217,22 +220,25 @@ __global__ __launch_bounds__(NW * 64) void scan_kernel(ScanArgs a) {
   }
 }
 
-template <typename T, bool LOCAL, bool VEC>
+template <typename T, bool LOCAL, bool VEC, bool PAD>
 hipError_t scan_split_of(const ScanArgs& a, hipStream_t s) {
   const int64_t blocks = int64_t(a.geo.B) * (LOCAL ? a.nchunk - 1 : a.nchunk) * a.G * a.cbg;
   switch (a.nw * 32 + a.np / a.nw) {   // the splits of scan_split
-    case 4 * 32 + 2: return go(scan_kernel<T, 4, 2, LOCAL, VEC>, blocks, 256, a, s);
-    case 4 * 32 + 4: return go(scan_kernel<T, 4, 4, LOCAL, VEC>, blocks, 256, a, s);
-    case 6 * 32 + 4: return go(scan_kernel<T, 6, 4, LOCAL, VEC>, blocks, 384, a, s);
-    case 8 * 32 + 4: return go(scan_kernel<T, 8, 4, LOCAL, VEC>, blocks, 512, a, s);
-    case 8 * 32 + 8: return go(scan_kernel<T, 8, 8, LOCAL, VEC>, blocks, 512, a, s);
-    case 8 * 32 + 16: return go(scan_kernel<T, 8, 16, LOCAL, VEC>, blocks, 512, a, s);
+    case 4 * 32 + 2: return go(scan_kernel<T, 4, 2, LOCAL, VEC, PAD>, blocks, 256, a, s);
+    case 4 * 32 + 4: return go(scan_kernel<T, 4, 4, LOCAL, VEC, PAD>, blocks, 256, a, s);
+    case 6 * 32 + 4: return go(scan_kernel<T, 6, 4, LOCAL, VEC, PAD>, blocks, 384, a, s);
+    case 8 * 32 + 4: return go(scan_kernel<T, 8, 4, LOCAL, VEC, PAD>, blocks, 512, a, s);
+    case 8 * 32 + 8: return go(scan_kernel<T, 8, 8, LOCAL, VEC, PAD>, blocks, 512, a, s);
+    case 8 * 32 + 16: return go(scan_kernel<T, 8, 16, LOCAL, VEC, PAD>, blocks, 512, a, s);
     default: return hipErrorInvalidValue;
   }
 }
 template <typename T, bool LOCAL>
 hipError_t scan_of(const ScanArgs& a, hipStream_t s) {
-  return a.vec_rows ? scan_split_of<T, LOCAL, true>(a, s) : scan_split_of<T, LOCAL, false>(a, s);
+  if constexpr (!LOCAL) {
+    if (a.N < a.np) return a.vec_rows ? scan_split_of<T, LOCAL, true, true>(a, s) : scan_split_of<T, LOCAL, false, true>(a, s);
+  }
+  return a.vec_rows ? scan_split_of<T, LOCAL, true, false>(a, s) : scan_split_of<T, LOCAL, false, false>(a, s);
 }
 
 }  // namespace

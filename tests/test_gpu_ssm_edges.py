@@ -1,11 +1,15 @@
-"""The state space operators on the GPU at the edges: scratch that another
-stream's work may still hold."""
+"""The state space operators on the GPU at the edges: infinite values; scratch
+that another stream's work may still hold."""
 import pytest
 import torch
 
 import onnx_recurrent_layers_amd as rl
+from tests import ssm_bounds as bounds
+from tests import ssm_reference as ref
+from tests.gpu_harness import note
 
 pytestmark = pytest.mark.gpu
+INF = float("inf")
 
 
 def positive(b, s, c, n, groups=1, seed=0):
@@ -17,6 +21,69 @@ def positive(b, s, c, n, groups=1, seed=0):
     v["A"] = -v["A"]
     v["delta"] = (v["delta"] - 1).float().double()
     return v
+
+
+def scan_both(v, groups=1, lens=None, softplus=True, gate=True, chunk=1 << 30, finite=None, backward=True):
+    """Forward and backward in f32 against the 64-bit forms: infinite where those are; what is not a number there may be
+    anything.  `finite`: the inputs by whose bounds finite outputs are judged (default: v)."""
+    b, s, c = v["X"].shape
+    n = v["A"].shape[1]
+    op = rl.SelectiveScan(dtype="f32", seq=s, batch=b, channels=c, state=n, groups=groups, delta_softplus=softplus)
+    t = {k: v[k].float().cuda() for k in ("X", "delta", "A", "B", "C", "D")} | {"delta_bias": v["bias"].float().cuda()}
+    if gate:
+        t["Z"] = v["Z"].float().cuda()
+    if lens is not None:
+        t["sequence_lens"] = torch.tensor(lens, dtype=torch.int32).cuda()
+    t["initial_state"] = v["init"].float().cuda()
+    f = {"Y": torch.empty_like(t["X"]), "final_state": torch.empty_like(t["initial_state"])}
+    op.encode(t | f)
+    g = {"dX": torch.empty_like(t["X"]), "ddelta": torch.empty_like(t["X"]), "dA": torch.empty_like(t["A"]), "dB": torch.empty_like(t["B"]),
+         "dC": torch.empty_like(t["C"]), "dD": torch.empty_like(t["D"]), "ddelta_bias": torch.empty_like(t["D"]),
+         "d_initial_state": torch.empty_like(t["initial_state"])}
+    if gate:
+        g["dZ"] = torch.empty_like(t["X"])
+    if backward:
+        op.backward(t | g | {"dY": v["dY"].float().cuda(), "d_final_state": v["dF"].float().cuda()})
+    torch.cuda.synchronize()
+
+    def args(w):
+        return [w[k] for k in ("X", "delta", "A", "B", "C")], dict(D=w["D"], Z=w["Z"] if gate else None, delta_bias=w["bias"], lens=lens,
+                                                                   initial_state=w["init"], groups=groups, softplus=softplus)
+
+    main, kw = args(v)
+    y, h = ref.scan(*main, **kw)
+    want = {"Y": y, "final_state": h} | (ref.scan_grad(*main, v["dY"], d_final=v["dF"], **kw) if backward else {})
+    w = finite or v
+    main, kw = args(w)
+    room = bounds.scan_bounds(*main, dY=w["dY"], d_final=w["dF"], chunk=chunk, **kw)
+    for name, value in want.items():
+        bounds.check((f | g)[name], value, room[name], "f32", name)
+    return want
+
+
+@pytest.mark.parametrize("n", [1, 5, 8, 10, 16, 20, 33, 100])
+@pytest.mark.parametrize("chunk", [0, 16])
+@pytest.mark.parametrize("name,step", [("X", 7), ("X", 19), ("delta", 7), ("delta", 19)])
+def test_scan_infinite_value(monkeypatch, n, chunk, name, step):
+    """An infinite input of one channel: infinite outputs there, not NaN by states that do not exist, and nothing elsewhere."""
+    monkeypatch.setenv("RNN_SCAN_CHUNK", str(chunk or 1 << 20))
+    note(f"n {n} chunk {chunk} {name} at {step}")
+    v = positive(2, 20, 6, n)
+    bad = dict(v, **{name: v[name].clone()})
+    bad[name][1, step, 2] = INF
+    want = scan_both(bad, finite=v, chunk=chunk or 1 << 30, backward=False)
+    assert want["Y"][1, step, 2] == INF
+
+
+@pytest.mark.parametrize("s", [1, 2, 4])
+@pytest.mark.parametrize("n", [1, 3, 4, 5, 16, 18, 100])
+def test_scan_tokens_infinite_value(s, n):
+    v = positive(3, s, 6, n)
+    for name in ("X", "delta"):
+        bad = dict(v, **{name: v[name].clone()})
+        bad[name][1, s - 1, 2] = INF
+        want = scan_both(bad, finite=v, backward=False)
+        assert want["Y"][1, s - 1, 2] == INF
 
 
 def test_scratch_while_its_memory_is_in_use():
