@@ -217,8 +217,11 @@ __global__ __launch_bounds__(NW * 64) void scan_ahead_kernel(ScanArgs a) {
   }
 }
 
-// Launch 2.
-template <typename T, int NW, int NS, bool VEC>
+// Launch 2.  PAD: there are states past N among a wave's, or lanes past a
+// group's channels, which are kept zero: their inputs are, but zero times an
+// infinite one is not a number, and would enter the sums over states (dX,
+// ddelta, dZ) and over lanes (dB, dC).
+template <typename T, int NW, int NS, bool VEC, bool PAD>
 __global__ __launch_bounds__(NW * 64) void scan_back_kernel(ScanArgs a) {
   constexpr int TS = scan_segment(NS);
   typedef Task<NW, TS> Mine;
@@ -258,11 +261,11 @@ __global__ __launch_bounds__(NW * 64) void scan_back_kernel(ScanArgs a) {
 #pragma unroll
       for (int i = 0; i < NS; ++i) G[i] = __builtin_fmaf(__builtin_amdgcn_exp2f(A[i] * sum), G[i], l[i]);
     }
-    // a lane past its group's channels adds nothing to dB and dC: all its
-    // values are zero
-    if (!p.ok) {
+    auto is = [&](int i) { return !PAD || (p.ok && n0 + i < a.N); };   // whether a lane's state is one
 #pragma unroll
-      for (int i = 0; i < NS; ++i) A[i] = G[i] = hs[i] = 0.f;
+    for (int i = 0; i < NS; ++i) {
+      A[i] = is(i) ? A[i] : 0.f;
+      G[i] = is(i) ? G[i] : 0.f;
     }
     float bias[V], skip[V];
 #pragma unroll
@@ -326,8 +329,9 @@ __global__ __launch_bounds__(NW * 64) void scan_back_kernel(ScanArgs a) {
       BC.put(nbc, s, send, sbc);
 #pragma unroll
       for (int i = 0; i < NS; ++i) {
-        h0[i] = p.ok ? nh[i] : 0.f;
+        h0[i] = nh[i];
         if (joined) h0[i] = __builtin_fmaf(__builtin_amdgcn_exp2f(A[i] * ncum), hs[i], h0[i]);
+        h0[i] = is(i) ? h0[i] : 0.f;
       }
       if (s > s0) fetch(s - TS);
       __syncthreads();
@@ -340,8 +344,10 @@ __global__ __launch_bounds__(NW * 64) void scan_back_kernel(ScanArgs a) {
         const float4 f = in[t][lane];
         each<NS>([&](auto I) {
           constexpr int i = decltype(I)::value;
-          e[t][i] = __builtin_amdgcn_exp2f(f.x * A[i]);
-          h[t][i] = __builtin_fmaf(e[t][i], t ? h[t ? t - 1 : 0][i] : h0[i], bc_mul<at + i>(bc, f.y));
+          const float decay = __builtin_amdgcn_exp2f(f.x * A[i]);
+          const float next = __builtin_fmaf(decay, t ? h[t ? t - 1 : 0][i] : h0[i], bc_mul<at + i>(bc, f.y));
+          e[t][i] = is(i) ? decay : 0.f;
+          h[t][i] = is(i) ? next : 0.f;
         });
         if (a.dZ.p) {
           float v = 0.f;
@@ -360,6 +366,10 @@ __global__ __launch_bounds__(NW * 64) void scan_back_kernel(ScanArgs a) {
           if (at < TS * 2 * NS && st < send) pbc[int64_t(st) * (2 * a.np) + at % (2 * NS)] = v;
         };
         bc_add<t * 2 * NS + NS, NS>(bc, G, f.z);
+        if constexpr (PAD) {
+#pragma unroll
+          for (int i = 0; i < NS; ++i) G[i] = is(i) ? G[i] : 0.f;
+        }
         bc_dot<t * 2 * NS, NS>(bc, sb, G);
         each<NS>([&](auto I) {
           constexpr int i = decltype(I)::value;
@@ -539,7 +549,8 @@ template <typename T, int NW, int NS, bool VEC>
 hipError_t back_of(const ScanArgs& a, hipStream_t s) {
   const int64_t blocks = int64_t(a.geo.B) * a.nchunk * a.G * a.cbg;
   if (hipError_t e = go(scan_ahead_kernel<T, NW, NS, VEC>, blocks, NW * 64, a, s); e != hipSuccess) return e;
-  return go(scan_back_kernel<T, NW, NS, VEC>, blocks, NW * 64, a, s);
+  return a.N < a.np || a.cpg % 64 ? go(scan_back_kernel<T, NW, NS, VEC, true>, blocks, NW * 64, a, s)
+                                  : go(scan_back_kernel<T, NW, NS, VEC, false>, blocks, NW * 64, a, s);
 }
 
 template <typename T>

@@ -86,6 +86,33 @@ def test_scan_tokens_infinite_value(s, n):
         assert want["Y"][1, s - 1, 2] == INF
 
 
+@pytest.mark.parametrize("n", [1, 5, 8, 10, 16, 20, 33, 100])
+@pytest.mark.parametrize("chunk", [0, 16])
+@pytest.mark.parametrize("name,step", [("X", 7), ("delta", 7), ("dY", 7), ("dY", 31), ("Z", 3)])
+def test_scan_gradient_infinite_value(monkeypatch, n, chunk, name, step):
+    """The same of the gradient."""
+    monkeypatch.setenv("RNN_SCAN_CHUNK", str(chunk or 1 << 20))
+    note(f"n {n} chunk {chunk} {name} at {step}")
+    v = positive(2, 32, 6, n)
+    bad = dict(v, **{name: v[name].clone()})
+    bad[name][1, step, 2] = INF
+    want = scan_both(bad, finite=v, chunk=chunk or 1 << 30)
+    assert name in ("X", "delta") or want["dX"][1, step, 2] == INF
+
+
+@pytest.mark.parametrize("n,c,groups", [(4, 6, 1), (16, 66, 1), (5, 6, 2), (64, 3, 3), (8, 64, 1)])
+@pytest.mark.parametrize("name,step", [("B", 7), ("C", 7), ("B", 31), ("C", 31)])
+def test_scan_infinite_weight(monkeypatch, n, c, groups, name, step):
+    """An infinite B or C of one state: no NaN from the lanes that have no channel."""
+    monkeypatch.setenv("RNN_SCAN_CHUNK", str(1 << 20))
+    note(f"n {n} c {c} {name} at {step}")
+    v = positive(2, 32, c, n, groups)
+    bad = dict(v, **{name: v[name].clone()})
+    bad[name][1, step, 1] = INF
+    want = scan_both(bad, groups, finite=v)
+    assert name == "B" or want["dB"][1, step, 1] == INF
+
+
 def test_scratch_while_its_memory_is_in_use():
     """The first calls of an object on one stream, while work queued on the current one still writes memory that was
     given back: the size of the scratch, many times."""
