@@ -356,9 +356,17 @@ __global__ __launch_bounds__(NW * 64) void scan_back_kernel(ScanArgs a) {
         }
         __builtin_amdgcn_sched_barrier(0);
       });
+      // Steps past the row's end (in the segment that is taken first) add q * 0 to
+      // dA, which is not 0 where a state or gradient is infinite: with the row's
+      // last step the sum begins anew.
+      const int edge = s + TS > send ? send - 1 - s : -1;
       each<TS>([&](auto TT) {
         constexpr int t = TS - 1 - decltype(TT)::value, base = decltype(TT)::value * 2 * NS;
         const float4 f = in[t][lane];
+        if (t == edge) {   // (uniform)
+#pragma unroll
+          for (int i = 0; i < NS; ++i) dA[i] = 0.f;
+        }
         float sb = 0.f, sq = 0.f;
         auto out = [&](int fold_at, float v) {   // 64 sums are there
           const int at = fold_at * 64 + mine;

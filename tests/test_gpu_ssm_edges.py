@@ -50,9 +50,19 @@ def scan_both(v, groups=1, lens=None, softplus=True, gate=True, chunk=1 << 30, f
         return [w[k] for k in ("X", "delta", "A", "B", "C")], dict(D=w["D"], Z=w["Z"] if gate else None, delta_bias=w["bias"], lens=lens,
                                                                    initial_state=w["init"], groups=groups, softplus=softplus)
 
-    main, kw = args(v)
-    y, h = ref.scan(*main, **kw)
-    want = {"Y": y, "final_state": h} | (ref.scan_grad(*main, v["dY"], d_final=v["dF"], **kw) if backward else {})
+    # each row by itself, as long as it is: no products with steps that do not exist
+    want = {}
+    for i, m in enumerate(ref.lengths(lens, b, s)):
+        row = {k: x if k in ("A", "D", "bias") else x[i:i + 1] if k in ("init", "dF") else x[i:i + 1, :m] for k, x in v.items()}
+        main, kw = args(row)
+        kw["lens"] = None
+        y, h = ref.scan(*main, **kw)
+        one = {"Y": y, "final_state": h} | (ref.scan_grad(*main, row["dY"], d_final=row["dF"], **kw) if backward else {})
+        for k, x in one.items():
+            if x.dim() == 3 and k not in ("final_state", "d_initial_state"):
+                x = torch.cat([x, x.new_zeros(1, s - m, x.shape[2])], 1)
+            want.setdefault(k, []).append(x)
+    want = {k: sum(x) if k in ("dA", "dD", "ddelta_bias") else torch.cat(x) for k, x in want.items()}
     w = finite or v
     main, kw = args(w)
     room = bounds.scan_bounds(*main, dY=w["dY"], d_final=w["dF"], chunk=chunk, **kw)
@@ -111,6 +121,23 @@ def test_scan_infinite_weight(monkeypatch, n, c, groups, name, step):
     bad[name][1, step, 1] = INF
     want = scan_both(bad, groups, finite=v)
     assert name == "B" or want["dB"][1, step, 1] == INF
+
+
+@pytest.mark.parametrize("n,c", [(1, 6), (8, 64), (16, 64), (24, 66), (64, 3), (128, 5)])
+@pytest.mark.parametrize("s,lens", [(20, None), (32, [29, 1]), (40, [40, 21]), (3, None)])
+@pytest.mark.parametrize("chunk", [0, 16])
+def test_scan_gradient_infinite_last_step(monkeypatch, n, c, s, lens, chunk):
+    """An infinite input or weight at a row's last step, inside a tile: dA, which takes the state before that step, is
+    finite, whatever stands past the row's end."""
+    monkeypatch.setenv("RNN_SCAN_CHUNK", str(chunk or 1 << 20))
+    note(f"n {n} c {c} s {s} lens {lens} chunk {chunk}")
+    v = positive(2, s, c, n)
+    for name, at in (("X", c - 1), ("B", n - 1)):
+        bad = dict(v, **{name: v[name].clone()})
+        for i, m in enumerate(lens or [s, s]):
+            bad[name][i, m - 1, at] = INF
+        want = scan_both(bad, lens=lens, finite=v, chunk=chunk or 1 << 30)
+        assert want["dA"].isfinite().all()
 
 
 def test_scratch_while_its_memory_is_in_use():
