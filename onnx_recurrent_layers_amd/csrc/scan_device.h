@@ -331,6 +331,18 @@ __device__ __forceinline__ void bc_add(const float (&v)[R], float* acc, float x)
 }
 #undef RNN_DPP
 
+// 2^x h + l for a sum x of many steps' exponents, where 2^x may leave f32
+// though the product does not (steps one by one would not have left it either):
+// 2^x as two factors, the second 1 for |x| <= 120, and none but the first, which
+// is neither zero nor infinite, for a zero or infinite h, which no finite number
+// of steps changes.
+__device__ __forceinline__ float scan_carry(float x, float h, float l) {
+  const float x1 = __builtin_amdgcn_fmed3f(x, -120.f, 120.f);
+  const float beyond = __builtin_amdgcn_exp2f(x - x1) * h;
+  const bool keep = h == 0.f || __builtin_fabsf(h) == __builtin_huge_valf();
+  return __builtin_fmaf(__builtin_amdgcn_exp2f(x1), keep ? h : beyond, l);
+}
+
 // The state at the start of chunk ch > 0 (live), from the end states of the
 // chunks before it: h = decay_j h + loc_j, decay_j = 2^(A sum_j).
 template <int NS>
@@ -343,7 +355,7 @@ __device__ __forceinline__ void scan_join(const ScanArgs& a, int b, int ch, int 
     scan_get<NS>(a, a.loc, at + j, n0, c, l);
     const float sum = a.sum[(at + j) * a.C + c];
 #pragma unroll
-    for (int i = 0; i < NS; ++i) h[i] = __builtin_fmaf(__builtin_amdgcn_exp2f(A[i] * sum), h[i], l[i]);
+    for (int i = 0; i < NS; ++i) h[i] = scan_carry(A[i] * sum, h[i], l[i]);
   }
 }
 

@@ -259,7 +259,7 @@ __global__ __launch_bounds__(NW * 64) void scan_back_kernel(ScanArgs a) {
       scan_get<NS>(a, a.gloc, at, n0, p.c, l);
       const float sum = a.sum[at * a.C + p.c];
 #pragma unroll
-      for (int i = 0; i < NS; ++i) G[i] = __builtin_fmaf(__builtin_amdgcn_exp2f(A[i] * sum), G[i], l[i]);
+      for (int i = 0; i < NS; ++i) G[i] = scan_carry(A[i] * sum, G[i], l[i]);
     }
     auto is = [&](int i) { return !PAD || (p.ok && n0 + i < a.N); };   // whether a lane's state is one
 #pragma unroll
@@ -330,7 +330,7 @@ __global__ __launch_bounds__(NW * 64) void scan_back_kernel(ScanArgs a) {
 #pragma unroll
       for (int i = 0; i < NS; ++i) {
         h0[i] = nh[i];
-        if (joined) h0[i] = __builtin_fmaf(__builtin_amdgcn_exp2f(A[i] * ncum), hs[i], h0[i]);
+        if (joined) h0[i] = scan_carry(A[i] * ncum, hs[i], h0[i]);
         h0[i] = is(i) ? h0[i] : 0.f;
       }
       if (s > s0) fetch(s - TS);

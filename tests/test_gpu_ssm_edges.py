@@ -1,5 +1,5 @@
-"""The state space operators on the GPU at the edges: infinite values; scratch
-that another stream's work may still hold."""
+"""The state space operators on the GPU at the edges: infinite values; decays
+whose product leaves f32; scratch that another stream's work may still hold."""
 import pytest
 import torch
 
@@ -138,6 +138,48 @@ def test_scan_gradient_infinite_last_step(monkeypatch, n, c, s, lens, chunk):
             bad[name][i, m - 1, at] = INF
         want = scan_both(bad, lens=lens, finite=v, chunk=chunk or 1 << 30)
         assert want["dA"].isfinite().all()
+
+
+def growing(b, s, c, n, rate, quiet):
+    """States that grow by e^rate a step, nothing happening for `quiet` steps."""
+    v = positive(b, s, c, n)
+    v["A"] = torch.full((c, n), float(rate), dtype=torch.float64)
+    v["delta"] = torch.ones(b, s, c, dtype=torch.float64)
+    v["bias"] = torch.zeros(c, dtype=torch.float64)
+    v["X"][:, :quiet] = 0
+    return v
+
+
+@pytest.mark.parametrize("n", [3, 16, 24])
+@pytest.mark.parametrize("chunk", [0, 64])
+def test_scan_growing_states(monkeypatch, n, chunk):
+    """Decays above 1 whose product over a chunk, e^128, passes the largest f32, on states that are zero or small."""
+    monkeypatch.setenv("RNN_SCAN_CHUNK", str(chunk or 1 << 20))
+    v = growing(2, 192, 5, n, 2.0, 170)
+    for name in ("init", "dY", "dF"):
+        v[name] = torch.zeros_like(v[name])
+    want = scan_both(v, softplus=False, chunk=chunk or 1 << 30, backward=False)
+    assert want["Y"][:, 175].abs().min() > 1
+    v["delta"][:, :64], v["delta"][:, 128:] = 0, 0
+    v["init"] = torch.full_like(v["init"], 1e-30).float().double()
+    want = scan_both(v, softplus=False, chunk=chunk or 1 << 30, backward=False)
+    assert want["final_state"].min() > 1e25
+
+
+@pytest.mark.parametrize("chunk", [0, 32])
+def test_scan_decay_to_nothing(monkeypatch, chunk):
+    """Decays whose product over a chunk, e^-134, is below the least f32: a large state keeps what is left of it, an
+    infinite one stays infinite."""
+    monkeypatch.setenv("RNN_SCAN_CHUNK", str(chunk or 1 << 20))
+    v = growing(2, 96, 5, 4, -3.0, 96)
+    v["delta"][:] = 0
+    v["delta"][:, 32:64] = float(torch.tensor(1.4))
+    v["init"] = torch.full_like(v["init"], 1e30).float().double()
+    scan_both(v, softplus=False, chunk=chunk or 1 << 30)
+    bad = dict(v, init=v["init"].clone())
+    bad["init"][1, 2, 1] = INF
+    want = scan_both(bad, softplus=False, chunk=chunk or 1 << 30, finite=v, backward=False)
+    assert want["final_state"][1, 2, 1] == INF
 
 
 def test_scratch_while_its_memory_is_in_use():
