@@ -13,7 +13,8 @@
 //      many states), and each chunk's end state, sum of step sizes and gradient
 //      at its start.  That gradient needs no walk back: sum_s (prod_{r<=s} a_r)
 //      C_s gy_s runs forward with the product, at three operations and no
-//      exponential.
+//      exponential.  (Where steps grow the states, and so much that the product
+//      may leave f32, it is walked back after all.)
 //   2. each chunk, segment after segment from its end: the segment's states
 //      and decays forward from the one written, kept in registers (at most 64
 //      of each a lane), then the gradients backward.
@@ -117,7 +118,7 @@ __global__ __launch_bounds__(NW * 64) void scan_ahead_kernel(ScanArgs a) {
     Q[i] = 1.f;
     G[i] = 0.f;
   }
-  float total = 0.f;
+  float total = 0.f, span = 0.f;   // sums of step sizes and of their magnitudes
   const bool behind = ch > 0;   // a chunk before this one needs the gradient at its start
   const bool gz = behind && a.have_z;
   float bias[V];
@@ -194,6 +195,7 @@ __global__ __launch_bounds__(NW * 64) void scan_ahead_kernel(ScanArgs a) {
         h[i] = __builtin_fmaf(e[i], h[i], bc_mul<at + i>(bc, f.y));
       });
       if (behind) {
+        span += __builtin_fabsf(f.x);
         const float g = dg[buf][t][lane];
         each<NS>([&](auto I) {
           constexpr int i = decltype(I)::value;
@@ -209,6 +211,34 @@ __global__ __launch_bounds__(NW * 64) void scan_ahead_kernel(ScanArgs a) {
   // (tiles past the end change and store nothing; a way out between two bodies
   // would have the compiler move registers whose loads are in flight)
   while (s < send) each<D>(body);
+  if (behind) {
+    // Q is within 2^100 of 1 unless the steps' exponents add up to more; and one
+    // that only falls loses nothing by falling to zero, since no later step's
+    // share would have been seen.  (With steps of one sign, both sums are the
+    // same number.)
+    bool risk = false;
+#pragma unroll
+    for (int i = 0; i < NS; ++i) {
+      const float all = __builtin_fabsf(A[i]) * span;
+      risk = risk || (all > 100.f && A[i] * total != -all);
+    }
+    if (__any(risk)) {
+#pragma unroll
+      for (int i = 0; i < NS; ++i) G[i] = 0.f;
+      const float db = a.dbias ? a.dbias[p.c] : 0.f;
+      for (int t = send - 1; t >= s0; --t) {
+        const int64_t row = r.base + t * r.step;
+        float d = float((reinterpret_cast<const T*>(a.delta.p) + p.c)[row * a.delta.rs]) + db;
+        if (a.softplus) d = softplus(d);
+        float g = float((reinterpret_cast<const T*>(a.dY.p) + p.c)[row * a.dY.rs]);
+        if (a.have_z) g *= gate_of(float((reinterpret_cast<const T*>(a.Z.p) + p.c)[row * a.Z.rs]));
+        const T* C = reinterpret_cast<const T*>(a.Cm.p) + row * a.Cm.rs + int64_t(p.g) * a.N;
+#pragma unroll
+        for (int i = 0; i < NS; ++i)
+          if (n0 + i < a.N) G[i] = __builtin_amdgcn_exp2f(d * A[i]) * __builtin_fmaf(float(C[n0 + i]), g, G[i]);
+      }
+    }
+  }
   if (p.ok && a.nchunk > 1) {
     const int64_t at = int64_t(b) * a.nchunk + ch;
     scan_put<NS>(a, a.loc, at, n0, p.c, h);

@@ -182,6 +182,45 @@ def test_scan_decay_to_nothing(monkeypatch, chunk):
     assert want["final_state"][1, 2, 1] == INF
 
 
+@pytest.mark.parametrize("n,c,groups,gate", [(3, 5, 1, True), (16, 130, 2, False), (24, 5, 1, True), (128, 3, 1, True)])
+@pytest.mark.parametrize("chunk", [0, 64])
+@pytest.mark.parametrize("lens", [None, [190, 129]])
+def test_scan_growing_gradient(monkeypatch, n, c, groups, gate, chunk, lens):
+    """The same of the gradient on its way back: of none, and of a small one to 1e22 and more."""
+    monkeypatch.setenv("RNN_SCAN_CHUNK", str(chunk or 1 << 20))
+    note(f"n {n} c {c} groups {groups} chunk {chunk} lens {lens}")
+    v = growing(2, 192, c, n, 2.0, 170)
+    v["B"], v["C"] = v["B"].repeat(1, 1, groups), v["C"].repeat(1, 1, groups)
+    for name in ("init", "dY", "dF"):
+        v[name] = torch.zeros_like(v[name])
+    v["dY"][:, :20] = 1.0                   # nothing but zeros comes back to step 20, and grows from there
+    v["X"][:] = 0
+    more = dict(groups=groups, gate=gate, lens=lens, softplus=False, chunk=chunk or 1 << 30)
+    scan_both(v, **more)
+    v["delta"][:, :64], v["delta"][:, 128:] = 0, 0
+    v["dY"] = torch.zeros_like(v["dY"])
+    v["dF"] = torch.full_like(v["dF"], 1e-33).float().double()
+    v["dY"][:, 127] = float(torch.tensor(1e-33))
+    want = scan_both(v, **more)
+    assert want["d_initial_state"].min() > 1e22
+    v["dF"] = torch.zeros_like(v["dF"])
+    want = scan_both(v, **more)
+    assert want["d_initial_state"].min() > 1e20
+
+
+@pytest.mark.parametrize("chunk", [0, 32])
+def test_scan_steps_of_both_signs(monkeypatch, chunk):
+    """A product of decays that leaves f32 downwards, by e^-120, and comes back within a chunk."""
+    monkeypatch.setenv("RNN_SCAN_CHUNK", str(chunk or 1 << 20))
+    v = growing(2, 96, 5, 4, -8.0, 96)
+    for k in range(96):
+        v["delta"][:, k] = 1.0 if 1 <= k % 32 <= 15 else -1.0 if 16 <= k % 32 <= 30 else 0.0
+    for name in ("init", "dY", "dF"):
+        v[name] = torch.zeros_like(v[name])
+    v["dY"][:, 31::32] = float(torch.tensor(1e-25))
+    scan_both(v, softplus=False, chunk=chunk or 1 << 30)
+
+
 def test_scratch_while_its_memory_is_in_use():
     """The first calls of an object on one stream, while work queued on the current one still writes memory that was
     given back: the size of the scratch, many times."""
