@@ -342,21 +342,53 @@ __device__ __forceinline__ float scan_carry(float x, float h, float l) {
   const bool keep = h == 0.f || __builtin_fabsf(h) == __builtin_huge_valf();
   return __builtin_fmaf(__builtin_amdgcn_exp2f(x1), keep ? h : beyond, l);
 }
+// Where the plain product does: no more than 2^120, and of an h that falls to
+// nothing without being missed (to 2^-80 or less).  `up`: the largest x, `big`:
+// the largest |h|.  Uniform.
+__device__ __forceinline__ bool scan_carry_plain(float up, float big) { return !__any(up > 120.f || big >= 0x1p40f); }
+
+// h, a state (or, going back, its gradient) at the end of one chunk, through
+// `n` chunks more: h = decay h + local of each, decay = 2^(A sum).  `at(k)` is
+// the k-th one's place in `local` and in `sum`.  (With scan_carry in the loop a
+// long prompt took 2 us more.)
+template <int NS, typename At>
+__device__ __forceinline__ void scan_through(const ScanArgs& a, const float* local, int n, int c, int n0, const float (&A)[NS],
+                                             float (&h)[NS], At at) {
+  float first[NS], up = 0.f, big = 0.f;
+#pragma unroll
+  for (int i = 0; i < NS; ++i) first[i] = h[i];
+#pragma unroll 4
+  for (int k = 0; k < n; ++k) {
+    float l[NS];
+    scan_get<NS>(a, local, at(k), n0, c, l);
+    const float sum = a.sum[at(k) * a.C + c];
+#pragma unroll
+    for (int i = 0; i < NS; ++i) {
+      const float x = A[i] * sum;
+      up = __builtin_fmaxf(up, x);
+      big = __builtin_fmaxf(big, __builtin_fabsf(h[i]));
+      h[i] = __builtin_fmaf(__builtin_amdgcn_exp2f(x), h[i], l[i]);
+    }
+  }
+  if (scan_carry_plain(up, big)) return;
+#pragma unroll
+  for (int i = 0; i < NS; ++i) h[i] = first[i];
+  for (int k = 0; k < n; ++k) {
+    float l[NS];
+    scan_get<NS>(a, local, at(k), n0, c, l);
+    const float sum = a.sum[at(k) * a.C + c];
+#pragma unroll
+    for (int i = 0; i < NS; ++i) h[i] = scan_carry(A[i] * sum, h[i], l[i]);
+  }
+}
 
 // The state at the start of chunk ch > 0 (live), from the end states of the
-// chunks before it: h = decay_j h + loc_j, decay_j = 2^(A sum_j).
+// chunks before it.
 template <int NS>
 __device__ __forceinline__ void scan_join(const ScanArgs& a, int b, int ch, int c, int n0, const float (&A)[NS], float (&h)[NS]) {
   const int64_t at = int64_t(b) * a.nchunk;
   scan_get<NS>(a, a.loc, at, n0, c, h);
-#pragma unroll 4
-  for (int j = 1; j < ch; ++j) {
-    float l[NS];
-    scan_get<NS>(a, a.loc, at + j, n0, c, l);
-    const float sum = a.sum[(at + j) * a.C + c];
-#pragma unroll
-    for (int i = 0; i < NS; ++i) h[i] = scan_carry(A[i] * sum, h[i], l[i]);
-  }
+  scan_through<NS>(a, a.loc, ch - 1, c, n0, A, h, [&](int k) { return at + 1 + k; });
 }
 
 }  // namespace rnnhip

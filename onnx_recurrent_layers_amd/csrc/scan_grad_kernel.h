@@ -283,19 +283,16 @@ __global__ __launch_bounds__(NW * 64) void scan_back_kernel(ScanArgs a) {
     if (joined) scan_join<NS>(a, b, ch, p.c, n0, A, hs);
     // the gradient at the chunk's end, from the chunks after it
     scan_load_state<NS>(a, a.dfin, cs, n0, G);
-    for (int j = (L - 1) / a.chunk; j > ch; --j) {
-      const int64_t at = int64_t(b) * a.nchunk + j;
-      float l[NS];
-      scan_get<NS>(a, a.gloc, at, n0, p.c, l);
-      const float sum = a.sum[at * a.C + p.c];
-#pragma unroll
-      for (int i = 0; i < NS; ++i) G[i] = scan_carry(A[i] * sum, G[i], l[i]);
-    }
+    const int last_chunk = (L - 1) / a.chunk;
+    scan_through<NS>(a, a.gloc, last_chunk - ch, p.c, n0, A, G, [&](int k) { return int64_t(b) * a.nchunk + last_chunk - k; });
+    float big = 0.f;   // the largest state at the chunk's start
     auto is = [&](int i) { return !PAD || (p.ok && n0 + i < a.N); };   // whether a lane's state is one
 #pragma unroll
     for (int i = 0; i < NS; ++i) {
       A[i] = is(i) ? A[i] : 0.f;
       G[i] = is(i) ? G[i] : 0.f;
+      if (joined) hs[i] = is(i) ? hs[i] : 0.f;
+      if (joined) big = __builtin_fmaxf(big, __builtin_fabsf(hs[i]));
     }
     float bias[V], skip[V];
 #pragma unroll
@@ -358,11 +355,21 @@ __global__ __launch_bounds__(NW * 64) void scan_back_kernel(ScanArgs a) {
       }
       BC.put(nbc, s, send, sbc);
 #pragma unroll
-      for (int i = 0; i < NS; ++i) {
-        h0[i] = nh[i];
-        if (joined) h0[i] = scan_carry(A[i] * ncum, hs[i], h0[i]);
-        h0[i] = is(i) ? h0[i] : 0.f;
+      for (int i = 0; i < NS; ++i) h0[i] = nh[i];
+      if (joined) {
+        float up = 0.f;
+#pragma unroll
+        for (int i = 0; i < NS; ++i) up = __builtin_fmaxf(up, A[i] * ncum);
+        if (scan_carry_plain(up, big)) {
+#pragma unroll
+          for (int i = 0; i < NS; ++i) h0[i] = __builtin_fmaf(__builtin_amdgcn_exp2f(A[i] * ncum), hs[i], h0[i]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < NS; ++i) h0[i] = scan_carry(A[i] * ncum, hs[i], h0[i]);
+        }
       }
+#pragma unroll
+      for (int i = 0; i < NS; ++i) h0[i] = is(i) ? h0[i] : 0.f;
       if (s > s0) fetch(s - TS);
       __syncthreads();
       float bc[BCRegs<NW, NS, TS>::R];
