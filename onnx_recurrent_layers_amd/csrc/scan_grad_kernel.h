@@ -251,10 +251,10 @@ __global__ __launch_bounds__(NW * 64) void scan_ahead_kernel(ScanArgs a) {
 // group's channels, which are kept zero: their inputs are, but zero times an
 // infinite one is not a number, and would enter the sums over states (dX,
 // ddelta, dZ) and over lanes (dB, dC).  (8 rows of 512 steps by 1024 channels,
-bf16, the whole pass: 10 states 130 us, 124.5 if they were left alone; 16 states
-by 1000 channels 131, 126.5.  Only where a value is not finite, as the first
-launch would leave word of it: 127.4 and 129.9, but 16 states by 1024 channels,
-which have none, 126.5 instead of 125.)
+// bf16, the whole pass: 10 states 130 us, 124.5 if they were left alone; 16
+// states by 1000 channels 131, 126.5.  Only where a value is not finite, as the
+// first launch would leave word of it: 127.4 and 129.9, but 16 states by 1024
+// channels, which have none, 126.5 instead of 125.)
 template <typename T, int NW, int NS, bool VEC, bool PAD>
 __device__ __forceinline__ void scan_back(const ScanArgs& a, float4 (*in)[64], float (*part)[NW][scan_segment(NS)][64],
                                           float (*sbc)[2 * NW * NS]) {
