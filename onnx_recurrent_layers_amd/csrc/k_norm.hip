@@ -346,7 +346,9 @@ hipError_t norm_shape(const NormArgs& a, hipStream_t s) {
   if (n <= 64) return F<T, 64, V, 1>::run(a, s);
   if (n <= 128) return F<T, 64, V, 2>::run(a, s);
   if (n <= 192 && a.rows >= 1024) return F<T, 64, V, 3>::run(a, s);
-  if (n <= 256 && a.rows >= 4096 && !a.dY.p) return F<T, 64, V, 4>::run(a, s);
+  if constexpr (!F<T, 64, V, 1>::back) {
+    if (n <= 256 && a.rows >= 4096) return F<T, 64, V, 4>::run(a, s);
+  }
   if (n <= 256) return F<T, 256, V, 1>::run(a, s);
   if (n <= 512) return F<T, 256, V, 2>::run(a, s);
   if (n <= 1024) return F<T, 256, V, 4>::run(a, s);
@@ -356,12 +358,14 @@ hipError_t norm_shape(const NormArgs& a, hipStream_t s) {
 
 template <typename T, int W, int V, int M>
 struct Forward {
+  static constexpr bool back = false;
   static hipError_t run(const NormArgs& a, hipStream_t s) {
     return go(norm_kernel<T, W, V, M>, (a.rows + 256 / W - 1) / (256 / W), 256, a, s);
   }
 };
 template <typename T, int W, int V, int M>
 struct Backward {
+  static constexpr bool back = true;
   static hipError_t run(const NormArgs& a, hipStream_t s) {
     if (M > 0 || a.dX.p) {
       const int64_t blocks = (a.rows + 256 / W - 1) / (256 / W);

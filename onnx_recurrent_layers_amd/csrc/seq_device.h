@@ -14,15 +14,6 @@ namespace rnnhip {
 typedef _Float16 f16_t;
 typedef __bf16 bf16_t;
 
-template <typename T>
-struct Elem;
-template <>
-struct Elem<float> { static constexpr int vec = 4; };
-template <>
-struct Elem<f16_t> { static constexpr int vec = 8; };
-template <>
-struct Elem<bf16_t> { static constexpr int vec = 8; };
-
 template <typename T, int V>
 struct alignas(sizeof(T) * V > 16 ? 16 : sizeof(T) * V) Pack { T v[V]; };
 
@@ -96,10 +87,6 @@ __device__ __forceinline__ float quad_x1(float v) {
 }
 __device__ __forceinline__ float quad_x2(float v) {
   return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), 0x4e, 0xf, 0xf, true));
-}
-__device__ __forceinline__ float quad_sum(float v) {
-  v += quad_x1(v);
-  return v + quad_x2(v);
 }
 // Four sums over a group of four lanes at once: lane q gets that of a[q].
 // Each exchange halves what is left, so three exchanges do for four sums.
