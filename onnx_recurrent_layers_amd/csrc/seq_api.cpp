@@ -212,6 +212,41 @@ const char kInitial[] = "initial_state", kFinal[] = "final_state";
 
 // ---------------------------------------------------------------- convolution
 
+namespace {
+
+// The workgroups of a launch of `v` channels a thread: `tx` threads of each
+// along the channels, the others along time, `tile` steps each.
+struct ConvGrid {
+  int tx;
+  int64_t ncb, ntb, blocks;
+};
+ConvGrid conv_grid_of(const rnn_conv_desc& d, int tile, int v, int tx) {
+  ConvGrid g;
+  g.tx = tx;
+  g.ncb = ceil_div(ceil_div(d.channels, v), tx);
+  g.ntb = std::max<int64_t>(ceil_div(ceil_div(d.seq, tile), 256 / tx), 1);
+  g.blocks = bytes_of({d.batch, g.ncb, g.ntb});   // (-1: past any limit)
+  if (g.blocks < 0) g.blocks = kMaxBytes;
+  return g;
+}
+ConvGrid conv_grid(const rnn_conv_desc& d, int tile, int v) {
+  int tx = 8;
+  while (tx < 256 && tx < ceil_div(d.channels, v)) tx *= 2;
+  return conv_grid_of(d, tile, v, tx);
+}
+ConvGrid conv_back_grid(const rnn_conv_desc& d, int tile, int v) { return conv_grid_of(d, tile, v, 64); }
+
+int conv_launch_fits(const ConvGrid& g, ConvArgs& a) {
+  if (g.blocks > kMaxThreads / 256)
+    return fail(RNN_ERR_UNSUPPORTED, kConv, "seq x batch x channels: too large for one launch of tensors like these");
+  a.tx = g.tx;
+  a.ncb = int(g.ncb);
+  a.ntb = int(g.ntb);
+  return RNN_OK;
+}
+
+}  // namespace
+
 extern "C" int rnn_conv_create(const rnn_conv_desc* desc, rnn_conv** out) {
   set_error_of(RNN_OK, nullptr, nullptr);
   if (out) *out = nullptr;
@@ -236,13 +271,10 @@ extern "C" int rnn_conv_create(const rnn_conv_desc* desc, rnn_conv** out) {
     return int(t);
   };
   const int tf = tile(8, 16 / es, 262144), tb = tile(16, 4, 131072);
-  // the most workgroups a launch may need (element-wise channels; a workgroup
-  // spans 8 channels at least)
-  const int64_t grid_f = d.batch * std::max<int64_t>(ceil_div(d.seq, tf), 1) * ceil_div(d.channels, 8);
-  const int64_t ntb = std::max<int64_t>(ceil_div(ceil_div(d.seq, tb), 4), 1);
-  const int64_t grid_b = d.batch * ntb * ceil_div(d.channels, 64);
-  if (grid_f > kMaxThreads / 256 || grid_b > kMaxThreads / 256)
+  // (with the most channels a thread; the calls see to what their tensors allow)
+  if (conv_grid(d, tf, d.channels % (16 / es) ? 1 : 16 / es).blocks > kMaxThreads / 256)
     return fail(RNN_ERR_UNSUPPORTED, kConv, "seq x batch x channels: too large for one launch");
+  const int64_t ntb = conv_back_grid(d, tb, 1).ntb;
   Regions r;
   r.take({d.batch, ntb, d.width + 1, d.channels, 4});
   if (!r.ok) return fail(RNN_ERR_SHAPE, kConv, "scratch: size overflows");
@@ -314,12 +346,8 @@ extern "C" int rnn_conv_encode(const rnn_conv* conv, const rnn_conv_operands* op
   const int v = 16 / c.es;
   const bool vec = d.channels % v == 0 && aligned(a.X, 16, c.es) && aligned(a.Y, 16, c.es) && aligned(a.W, 16) &&
                    aligned(a.bias, 16) && aligned(a.init, 16) && aligned(a.fin, 16);
-  const int64_t n = vec ? d.channels / v : d.channels;   // threads along the channels
   a.tile = c.tile;
-  a.tx = 8;
-  while (a.tx < 256 && a.tx < n) a.tx *= 2;
-  a.ncb = int(ceil_div(n, a.tx));
-  a.ntb = int(std::max<int64_t>(ceil_div(ceil_div(d.seq, a.tile), 256 / a.tx), 1));
+  if (int rc = conv_launch_fits(conv_grid(d, a.tile, vec ? v : 1), a)) return rc;
   hipStream_t s = static_cast<hipStream_t>(stream);
   OnDevice on(s);
   if (hipError_t e = launch_conv(a, d.dtype, vec ? v : 1, s); e != hipSuccess)
@@ -357,9 +385,7 @@ extern "C" int rnn_conv_encode_backward(const rnn_conv* conv, const rnn_conv_ope
                    aligned(a.W, al) && aligned(a.bias, al) && aligned(a.init, al) && aligned(a.dfin, al) &&
                    aligned(a.dinit, al);
   a.tile = c.tile_b;
-  a.tx = 64;
-  a.ncb = int(ceil_div(d.channels, vec ? 256 : 64));
-  a.ntb = int(std::max<int64_t>(ceil_div(ceil_div(d.seq, a.tile), 4), 1));
+  if (int rc = conv_launch_fits(conv_back_grid(d, a.tile, vec ? 4 : 1), a)) return rc;
   hipStream_t s = static_cast<hipStream_t>(stream);
   OnDevice on(s);
   if (hipError_t e = launch_conv_backward(a, d.dtype, vec ? 4 : 1, s); e != hipSuccess)

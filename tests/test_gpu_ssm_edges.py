@@ -221,6 +221,24 @@ def test_scan_steps_of_both_signs(monkeypatch, chunk):
     scan_both(v, softplus=False, chunk=chunk or 1 << 30)
 
 
+def test_conv_many_tokens():
+    """One token of each of 16400 rows of 8200 channels: 2^24 groups of eight and more."""
+    b, c, k = 16400, 8200, 3
+    gen = torch.Generator("cuda").manual_seed(1)
+    X, W = (torch.randn(*s, generator=gen, device="cuda").to(torch.bfloat16) for s in ((b, 1, c), (c, k)))
+    state = torch.randn(b, k - 1, c, generator=gen, device="cuda").to(torch.bfloat16)
+    Y, final = torch.empty_like(X), torch.empty_like(state)
+    op = rl.CausalConv(dtype="bf16", seq=1, batch=b, channels=c, width=k, silu=False)
+    op.encode({"X": X, "W": W, "initial_state": state, "Y": Y, "final_state": final})
+    assert torch.equal(final[:, 0], state[:, 1]) and torch.equal(final[:, 1], X[:, 0])
+    for rows in (slice(0, 100), slice(b - 100, b)):
+        seen = torch.cat([state[rows], X[rows]], 1).double()
+        want = (seen * W.double().t()).sum(1)
+        off = (Y[rows, 0].double() - want).abs()
+        room = 4 * 2.0 ** -24 * (seen * W.double().t()).abs().sum(1)     # three roundings, and that to 16 bits
+        assert (off <= room + 2.0 ** -8 * (want.abs() + room)).all()
+
+
 def test_scratch_while_its_memory_is_in_use():
     """The first calls of an object on one stream, while work queued on the current one still writes memory that was
     given back: the size of the scratch, many times."""

@@ -1,0 +1,45 @@
+"""The largest sizes that the state space operators and layer normalization
+take, just below and at each limit (no GPU: nothing that is accepted is run)."""
+import pytest
+
+import onnx_recurrent_layers_amd as rl
+from tests.test_ssm_host import FAKE, OPS, UNSUPPORTED, filled, refused
+
+
+def created(op, fields):
+    """Created and destroyed; with backward also its scratch sizes."""
+    create, destroy, desc, _ = OPS[op]
+    h = create(desc(**fields))
+    destroy(h)
+
+
+def at_call(op, fields, backward=False, **odd):
+    """The call is refused, though the description is not: tensors named in `odd` are moved by so many bytes."""
+    create, destroy, desc, start = OPS[op]
+    h = create(desc(**fields))
+    try:
+        ops, grads = filled(op, "operands"), filled(op, "gradients")
+        for name, by in odd.items():
+            getattr(ops, name).ptr += by
+        if backward:
+            refused(lambda: getattr(rl, f"rnn_{op}_encode_backward")(h, ops, grads, FAKE << 8), UNSUPPORTED, start, "too large for one launch")
+        else:
+            refused(lambda: getattr(rl, f"rnn_{op}_encode")(h, ops, FAKE << 8), UNSUPPORTED, start, "too large for one launch")
+    finally:
+        destroy(h)
+
+
+BF16 = dict(dtype=2)
+# 8 channels a thread, 256 threads a workgroup: 4 workgroups for a row of 8192 channels; one thread a channel: 32
+CONV = BF16 | dict(seq=1, channels=8192, width=4)
+
+
+def test_conv_limits():
+    created("conv", BF16 | dict(seq=65536, batch=16, channels=8192))
+    created("conv", BF16 | dict(seq=65536, batch=16, channels=8190))
+    created("conv", CONV | dict(batch=(1 << 22) - 1))
+    refused(lambda: created("conv", CONV | dict(batch=1 << 22)), UNSUPPORTED, "conv: ", "too large for one launch")
+    at_call("conv", CONV | dict(batch=1 << 19), X=2)
+    at_call("conv", CONV | dict(batch=1 << 19), backward=True)      # four channels a thread, 64 such threads a workgroup
+    created("conv", CONV | dict(channels=8191, batch=(1 << 19) - 1))
+    refused(lambda: created("conv", CONV | dict(channels=8191, batch=1 << 19)), UNSUPPORTED, "conv: ", "too large for one launch")
