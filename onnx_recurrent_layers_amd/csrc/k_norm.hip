@@ -331,29 +331,26 @@ __global__ __launch_bounds__(1024) void colsum_kernel(ColSumArgs a) {
   }
 }
 
-// The threads of a row and its shares: the least threads that hold the row in
-// registers.  Many rows: a wave of up to 3 shares a lane (forward 4), since
-// rows then need no meeting of waves and fewer lanes idle (16 bits, forward and
-// backward: 65536 rows of 1280 67 and 103 us, with a workgroup a row 104 and
-// 179; 8192 of 1536 11.1 and 20.7, 13.3 and 25.5; 8192 of 2048 13.7 forward,
-// 15.4; but backward, its registers full, 16384 of 2048 49, 46.8).  With few
-// rows compute units would idle so (64 rows of 1024 f32: 8.9 us, 8.4).
 template <typename T, int V, template <typename, int, int, int> class F>
 hipError_t norm_shape(const NormArgs& a, hipStream_t s) {
-  const int n = (a.size + V - 1) / V;   // shares
-  if (n <= 16) return F<T, 16, V, 1>::run(a, s);
-  if (n <= 32) return F<T, 32, V, 1>::run(a, s);
-  if (n <= 64) return F<T, 64, V, 1>::run(a, s);
-  if (n <= 128) return F<T, 64, V, 2>::run(a, s);
-  if (n <= 192 && a.rows >= 1024) return F<T, 64, V, 3>::run(a, s);
-  if constexpr (!F<T, 64, V, 1>::back) {
-    if (n <= 256 && a.rows >= 4096) return F<T, 64, V, 4>::run(a, s);
+  const NormRow r = norm_row(a.size, V, a.rows, F<T, 64, V, 1>::back);
+  switch (r.threads * 16 + r.shares) {
+    case 16 * 16 + 1: return F<T, 16, V, 1>::run(a, s);
+    case 32 * 16 + 1: return F<T, 32, V, 1>::run(a, s);
+    case 64 * 16 + 1: return F<T, 64, V, 1>::run(a, s);
+    case 64 * 16 + 2: return F<T, 64, V, 2>::run(a, s);
+    case 64 * 16 + 3: return F<T, 64, V, 3>::run(a, s);
+    case 64 * 16 + 4:
+      if constexpr (!F<T, 64, V, 1>::back) return F<T, 64, V, 4>::run(a, s);
+      return hipErrorInvalidValue;
+    case 256 * 16 + 1: return F<T, 256, V, 1>::run(a, s);
+    case 256 * 16 + 2: return F<T, 256, V, 2>::run(a, s);
+    case 256 * 16 + 4: return F<T, 256, V, 4>::run(a, s);
+    case 256 * 16 + 8:
+      if constexpr (V < 8) return F<T, 256, V, 8>::run(a, s);
+      return hipErrorInvalidValue;
+    default: return F<T, 256, V, 0>::run(a, s);
   }
-  if (n <= 256) return F<T, 256, V, 1>::run(a, s);
-  if (n <= 512) return F<T, 256, V, 2>::run(a, s);
-  if (n <= 1024) return F<T, 256, V, 4>::run(a, s);
-  if (V < 8 && n <= 2048) return F<T, 256, V, V < 8 ? 8 : 0>::run(a, s);
-  return F<T, 256, V, 0>::run(a, s);
 }
 
 template <typename T, int W, int V, int M>

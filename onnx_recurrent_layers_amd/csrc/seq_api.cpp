@@ -652,6 +652,19 @@ extern "C" int rnn_scan_encode_backward(const rnn_scan* scan, const rnn_scan_ope
 
 // --------------------------------------------------------- layer normalization
 
+namespace {
+
+// Whether a launch of `v` values a time holds all rows.  (The gradient's walks
+// them with fewer workgroups, but for rows too long for registers.)
+int norm_launch_fits(const rnn_norm_desc& d, int v, bool backward) {
+  const NormRow r = norm_row(d.size, v, d.rows, backward);
+  if ((!backward || r.shares == 0) && ceil_div(d.rows, 256 / r.threads) > kMaxThreads / 256)
+    return fail(RNN_ERR_UNSUPPORTED, kNorm, "rows: too large for one launch");
+  return RNN_OK;
+}
+
+}  // namespace
+
 extern "C" int rnn_norm_create(const rnn_norm_desc* desc, rnn_norm** out) {
   set_error_of(RNN_OK, nullptr, nullptr);
   if (out) *out = nullptr;
@@ -666,9 +679,8 @@ extern "C" int rnn_norm_create(const rnn_norm_desc* desc, rnn_norm** out) {
   if (d.rows > (int64_t(1) << 30)) return fail(RNN_ERR_UNSUPPORTED, kNorm, "rows: above 2^30");
   const int es = elem_size(d.dtype);
   if (bytes_of({d.rows, d.size, es}) < 0) return fail(RNN_ERR_SHAPE, kNorm, "X: size overflows");
-  // a launch holds rows x the threads of a row (16 to 256; 64 for at most
-  // 1024 values of 16 bits, 256 above)
-  if (d.rows > kMaxThreads / 256 - 256) return fail(RNN_ERR_UNSUPPORTED, kNorm, "rows: too many for one launch");
+  // (with the widest accesses; the calls see to what their tensors allow)
+  if (int rc = norm_launch_fits(d, d.size % (16 / es) ? 1 : 16 / es, false)) return rc;
   rnn_norm* n = new (std::nothrow) rnn_norm();
   if (!n) return fail(RNN_ERR_ARG, kNorm, "out of host memory");
   n->d = d;
@@ -721,6 +733,7 @@ extern "C" int rnn_norm_encode(const rnn_norm* norm, const rnn_norm_operands* op
   a.eps = d.epsilon;
   a.vec = d.size % (16 / p.es) == 0 && aligned(a.X, 16, p.es) && aligned(a.Y, 16, p.es) && aligned(a.scale, 16) &&
           aligned(a.shift, 16);
+  if (int rc = norm_launch_fits(d, a.vec ? 16 / p.es : 1, false)) return rc;
   hipStream_t s = static_cast<hipStream_t>(stream);
   OnDevice on(s);
   if (hipError_t e = launch_norm(a, d.dtype, s); e != hipSuccess)
@@ -761,6 +774,7 @@ extern "C" int rnn_norm_encode_backward(const rnn_norm* norm, const rnn_norm_ope
   a.part = sums ? static_cast<float*>(scratch) : nullptr;
   a.vec = d.size % (16 / p.es) == 0 && aligned(a.X, 16, p.es) && aligned(a.dY, 16, p.es) && aligned(a.dX, 16, p.es) &&
           aligned(a.scale, 16);
+  if (int rc = norm_launch_fits(d, a.vec ? 16 / p.es : 1, true)) return rc;
   hipStream_t s = static_cast<hipStream_t>(stream);
   OnDevice on(s);
   if (hipError_t e = launch_norm_backward(a, d.dtype, s); e != hipSuccess)

@@ -80,6 +80,32 @@ struct NormArgs {
   int32_t vec;        // 16-byte accesses
 };
 
+// The threads of a row, and the shares of `v` values that each holds in
+// registers (0: rows too long for that).  The least threads that hold the row.
+// Many rows: a wave of up to 3 shares a lane (forward 4), since rows then need no
+// meeting of waves and fewer lanes idle (16 bits, forward and backward: 65536
+// rows of 1280 67 and 103 us, with a workgroup a row 104 and 179; 8192 of 1536
+// 11.1 and 20.7, 13.3 and 25.5; 8192 of 2048 13.7 forward, 15.4; but backward,
+// its registers full, 16384 of 2048 49, 46.8).  With few rows compute units
+// would idle so (64 rows of 1024 f32: 8.9 us, 8.4).
+struct NormRow {
+  int threads, shares;
+};
+inline NormRow norm_row(int64_t size, int v, int64_t rows, bool backward) {
+  const int64_t n = (size + v - 1) / v;
+  if (n <= 16) return {16, 1};
+  if (n <= 32) return {32, 1};
+  if (n <= 64) return {64, 1};
+  if (n <= 128) return {64, 2};
+  if (n <= 192 && rows >= 1024) return {64, 3};
+  if (n <= 256 && rows >= 4096 && !backward) return {64, 4};
+  if (n <= 256) return {256, 1};
+  if (n <= 512) return {256, 2};
+  if (n <= 1024) return {256, 4};
+  if (v < 8 && n <= 2048) return {256, 8};
+  return {256, 0};
+}
+
 // Column sums of part[P][cols] in a fixed order, f32.  Column j of a block of
 // (K+1)*C columns [k][c] goes to out[c*K + k] (k < K) or out2[c].
 struct ColSumArgs {

@@ -239,6 +239,30 @@ def test_conv_many_tokens():
         assert (off <= room + 2.0 ** -8 * (want.abs() + room)).all()
 
 
+def test_norm_many_rows():
+    """2^24 rows and more of a few values, forward and backward."""
+    rows, size = (1 << 24) + 19, 16
+    gen = torch.Generator("cuda").manual_seed(2)
+    X, dY = (torch.randn(rows, size, generator=gen, device="cuda").to(torch.float16) for _ in range(2))
+    scale = torch.randn(size, generator=gen, device="cuda").to(torch.float16)
+    op = rl.LayerNorm(dtype="f16", rows=rows, size=size)
+    t = {"X": X, "Scale": scale, "Y": torch.empty_like(X), "Mean": torch.empty(rows, device="cuda"), "InvStdDev": torch.empty(rows, device="cuda")}
+    op.encode(t)
+    g = {"dY": dY, "dX": torch.empty_like(X), "dB": torch.empty(size, device="cuda")}
+    op.backward({k: t[k] for k in ("X", "Scale", "Mean", "InvStdDev")} | g)
+    few = rl.LayerNorm(dtype="f16", rows=300, size=size)
+    for at in (slice(0, 300), slice(rows - 300, rows)):        # a row does not depend on the others
+        u = {"X": X[at], "Scale": scale, "Y": torch.empty_like(X[at]), "Mean": torch.empty(300, device="cuda"), "InvStdDev": torch.empty(300, device="cuda")}
+        few.encode(u)
+        assert all(torch.equal(u[k], t[k][at]) for k in ("Y", "Mean", "InvStdDev"))
+        d = torch.empty_like(X[at])
+        few.backward({k: u[k] for k in ("X", "Scale", "Mean", "InvStdDev")} | {"dY": dY[at], "dX": d})
+        assert torch.equal(d, g["dX"][at])
+    # 512 parts of 32768 rows, 16 of them at a time: no value goes through more than some 2200 additions
+    want = dY.double().sum(0).cpu()
+    assert ((g["dB"].cpu().double() - want).abs() <= 2200 * 2.0 ** -24 * dY.double().abs().sum(0).cpu()).all()
+
+
 def test_scratch_while_its_memory_is_in_use():
     """The first calls of an object on one stream, while work queued on the current one still writes memory that was
     given back: the size of the scratch, many times."""

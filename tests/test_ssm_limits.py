@@ -43,3 +43,23 @@ def test_conv_limits():
     at_call("conv", CONV | dict(batch=1 << 19), backward=True)      # four channels a thread, 64 such threads a workgroup
     created("conv", CONV | dict(channels=8191, batch=(1 << 19) - 1))
     refused(lambda: created("conv", CONV | dict(channels=8191, batch=1 << 19)), UNSUPPORTED, "conv: ", "too large for one launch")
+
+
+def test_norm_limits():
+    created("norm", BF16 | dict(rows=1 << 24, size=64))             # 16 threads a row
+    created("norm", BF16 | dict(rows=(1 << 28) - 16, size=128))
+    created("norm", BF16 | dict(rows=(1 << 28) - 16, size=1))
+    refused(lambda: created("norm", BF16 | dict(rows=1 << 28, size=128)), UNSUPPORTED, "layer norm: ", "too large for one launch")
+    created("norm", BF16 | dict(rows=(1 << 27) - 8, size=256))      # 32
+    refused(lambda: created("norm", BF16 | dict(rows=1 << 27, size=256)), UNSUPPORTED, "layer norm: ", "too large for one launch")
+    created("norm", BF16 | dict(rows=(1 << 26) - 4, size=512))      # a wave
+    created("norm", BF16 | dict(rows=(1 << 26) - 4, size=2048))
+    created("norm", BF16 | dict(rows=(1 << 24) - 1, size=2056))     # a workgroup
+    refused(lambda: created("norm", BF16 | dict(rows=1 << 24, size=2056)), UNSUPPORTED, "layer norm: ", "too large for one launch")
+    at_call("norm", BF16 | dict(rows=1 << 26, size=128), X=2)       # 128 values of one access each: a wave a row
+    at_call("norm", BF16 | dict(rows=1 << 24, size=2048), X=2)
+    at_call("norm", dict(dtype=0, rows=1 << 24, size=1024), X=4)    # (f32: a wave a row in whole pieces)
+    h = OPS["norm"][0](OPS["norm"][2](**BF16, rows=1 << 24, size=64))
+    parts = 512     # of sums over the rows, whatever their number
+    assert rl.rnn_norm_scratch_size(h) == (0, parts * 2 * 64 * 4)
+    rl.rnn_norm_destroy(h)
