@@ -347,8 +347,9 @@ int rnn_read_run_status(const rnn_problem* problem, const void* state_scratch, v
  *
  * Limits (RNN_ERR_UNSUPPORTED): channels above 2^24, batch or seq above 2^30,
  * sizes whose launch would hold 2^32 threads or more (refused by the call where
- * it is its tensors' alignment, or the gradient, that takes so many).  A tensor
- * or a scratch above 2^52 bytes is RNN_ERR_SHAPE. */
+ * it is its tensors' alignment, or the gradient, that takes so many), a scan
+ * whose B has 2^40 elements or more.  A tensor or a scratch above 2^52 bytes is
+ * RNN_ERR_SHAPE. */
 typedef struct {
   void* ptr;           /* device pointer, or NULL for an absent tensor */
   int64_t elem_offset; /* >= 0, in elements of the tensor's type */

@@ -39,6 +39,8 @@
 // at best against 123.
 #pragma once
 
+#include <algorithm>
+
 #include "scan_device.h"
 
 namespace rnnhip {
@@ -550,8 +552,9 @@ __global__ __launch_bounds__(256) void scan_sums_kernel(ScanArgs a) {
   const int tid = int(threadIdx.x);
   const int64_t gn = int64_t(a.G) * a.N;
   const int64_t nbc = (a.dB.p || a.dC.p) ? (int64_t(a.geo.B) * a.geo.S * 2 * gn + 255) / 256 : 0;
-  if (int64_t(blockIdx.x) < nbc) {
-    const int64_t i = int64_t(blockIdx.x) * 256 + tid;
+  const int64_t block = a.sums0 + blockIdx.x;
+  if (block < nbc) {
+    const int64_t i = block * 256 + tid;
     if (i >= int64_t(a.geo.B) * a.geo.S * 2 * gn) return;
     const int64_t row = i / (2 * gn);
     const int in = int(i - row * 2 * gn);
@@ -577,7 +580,7 @@ __global__ __launch_bounds__(256) void scan_sums_kernel(ScanArgs a) {
   }
   __shared__ float red[3][64];
   const int64_t ncA = a.dA ? (int64_t(a.C) * a.np + 63) / 64 : 0;
-  const int64_t blk = int64_t(blockIdx.x) - nbc;
+  const int64_t blk = block - nbc;
   const bool isA = blk < ncA;
   const int64_t cols = isA ? int64_t(a.C) * a.np : 2 * int64_t(a.C);
   const float* part = isA ? a.pA : a.pD;
@@ -627,7 +630,10 @@ hipError_t scan_backward_of(const ScanArgs& a, hipStream_t s) {
   if (a.dB.p || a.dC.p) blocks += (int64_t(a.geo.B) * a.geo.S * 2 * a.G * a.N + 255) / 256;
   if (a.dA) blocks += (int64_t(a.C) * a.np + 63) / 64;
   if (a.dD || a.ddbias) blocks += (2 * int64_t(a.C) + 63) / 64;
-  return go(scan_sums_kernel<T>, blocks, 256, a, s);
+  constexpr int64_t most = (int64_t(1) << 24) - 1;   // workgroups of a launch
+  for (ScanArgs part = a; part.sums0 < blocks; part.sums0 += most)
+    if (e = go(scan_sums_kernel<T>, std::min(blocks - part.sums0, most), 256, part, s); e != hipSuccess) return e;
+  return hipSuccess;
 }
 
 }  // namespace

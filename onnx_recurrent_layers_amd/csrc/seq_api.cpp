@@ -423,6 +423,9 @@ ScanPlan scan_plan(const rnn_scan_desc& d, bool backward, int64_t blocks, int64_
   return p;
 }
 
+// Rows times channel blocks that a launch of `nw` waves a workgroup holds.
+int64_t scan_most_blocks(int nchunk, int nw) { return kMaxThreads / (64 * nw) / nchunk; }
+
 // The scratch regions of the two directions, in the order that they are taken.
 struct ScanScratch {
   size_t sink, loc, sum, first, ckpt, cum, pbc, pA, pD, gloc;
@@ -484,10 +487,12 @@ extern "C" int rnn_scan_create(const rnn_scan_desc* desc, rnn_scan** out) {
   p.f = scan_plan(d, false, blocks, blocks <= 160 ? 512 : 0);
   p.b = scan_plan(d, true, blocks, 256);
   p.nseg = int(std::max<int64_t>(ceil_div(d.seq, scan_segment(p.b.np / p.b.nw)), 1));
-  const int64_t most = kMaxThreads / 512;
-  const int64_t sums = ceil_div(d.seq * d.batch * 2, 256) * d.groups * d.state + d.channels * (p.b.np + 2);
-  if (blocks > most / std::max(p.f.nchunk, p.b.nchunk) || sums > most)
+  // (the gradient's launches are seen to by its call; its sums go in as many as
+  // they need, so that what they write is the only limit)
+  if (blocks > scan_most_blocks(p.f.nchunk, p.tokens ? 4 : p.f.nw))
     return fail(RNN_ERR_UNSUPPORTED, kScan, "seq x batch x channels: too large for one launch");
+  if (bytes_of({d.seq, d.batch, d.groups, d.state}) >= int64_t(1) << 40)
+    return fail(RNN_ERR_UNSUPPORTED, kScan, "seq x batch x groups x state: 2^40 or more");
   ScanScratch at;
   if (!scan_scratch(p, false, &at, &p.forward_bytes) || !scan_scratch(p, true, &at, &p.backward_bytes))
     return fail(RNN_ERR_SHAPE, kScan, "scratch: size overflows");
@@ -640,6 +645,8 @@ extern "C" int rnn_scan_encode_backward(const rnn_scan* scan, const rnn_scan_ope
   t.apart();
   if (t.status != RNN_OK) return t.status;
   if (a.dZ.p && !a.have_z) return fail(RNN_ERR_ARG, kScan, "dZ: there is no Z");
+  if (d.batch * d.groups * p.cbg > scan_most_blocks(p.b.nchunk, p.b.nw))
+    return fail(RNN_ERR_UNSUPPORTED, kScan, "seq x batch x channels: too large for one launch of the gradient");
   if (!a.dX.p && !a.ddelta.p && !a.dA && !a.dB.p && !a.dC.p && !a.dD && !a.dZ.p && !a.ddbias && !a.dinit) return RNN_OK;
   if (int rc = check_scratch(kScan, scratch, p.backward_bytes)) return rc;
   scan_lay(p, true, scratch, a);

@@ -66,6 +66,7 @@ struct ScanArgs {
   float* pA;      // [B*nchunk][NP][C]
   float* pD;      // [B*nchunk][2][C]: dD, ddelta_bias
   int32_t nseg;   // segments of a row (chunks begin on segment borders)
+  int64_t sums0;  // first workgroup of a launch of the sums
 };
 
 struct NormArgs {

@@ -263,6 +263,63 @@ def test_norm_many_rows():
     assert ((g["dB"].cpu().double() - want).abs() <= 2200 * 2.0 ** -24 * dY.double().abs().sum(0).cpu()).all()
 
 
+def test_scan_token_of_many_channels():
+    """A token of 65536 channels by 128 states, forward and backward, by its first and last channels alone."""
+    c, n = 65536, 128
+    gen = torch.Generator("cuda").manual_seed(3)
+
+    def rand(*size):
+        return torch.rand(*size, generator=gen, device="cuda")
+
+    t = {"X": rand(1, 1, c), "delta": rand(1, 1, c), "A": -rand(c, n), "B": rand(1, 1, n), "C": rand(1, 1, n), "initial_state": rand(1, c, n)}
+    outs = {"Y": rand(1, 1, c), "final_state": rand(1, c, n)}
+    grads = {"dX": rand(1, 1, c), "dA": rand(c, n), "d_initial_state": rand(1, c, n)}
+    dY = rand(1, 1, c)
+    op = rl.SelectiveScan(dtype="f32", seq=1, batch=1, channels=c, state=n)
+    op.encode(t | outs)
+    op.backward(t | grads | {"dY": dY})
+    few = rl.SelectiveScan(dtype="f32", seq=1, batch=1, channels=64, state=n)
+    for at in (slice(0, 64), slice(c - 64, c)):
+
+        def part(name, x):
+            return x[at].contiguous() if name in ("A", "dA") else x if name in ("B", "C") else x[:, at].contiguous() if name[-5:] == "state" else x[..., at].contiguous()
+
+        u = {k: part(k, x) for k, x in t.items()}
+        o = {k: torch.empty_like(part(k, x)) for k, x in outs.items()}
+        g = {k: torch.empty_like(part(k, x)) for k, x in grads.items()}
+        few.encode(u | o)
+        few.backward(u | g | {"dY": part("dY", dY)})
+        assert all(torch.equal(o[k], part(k, outs[k])) for k in o) and all(torch.equal(g[k], part(k, grads[k])) for k in g)
+
+
+def test_scan_gradient_sums_in_two_launches(monkeypatch):
+    """2^20 rows of B and C with 2048 weights each: 2^32 sums of dB and dC.  Rows of the batch do not depend on each other."""
+    monkeypatch.setenv("RNN_SCAN_CHUNK", str(1 << 20))
+    b, s, g, n = 64, 16384, 16, 128
+    gen = torch.Generator("cuda").manual_seed(4)
+
+    def rand(*size):
+        return torch.empty(*size, dtype=torch.bfloat16, device="cuda").uniform_(0.1, 1, generator=gen)
+
+    t = {k: rand(b, s, g) for k in ("X", "delta")} | {k: rand(b, s, g * n) for k in ("B", "C")} | {"A": -torch.rand(g, n, generator=gen, device="cuda")}
+    dY = rand(b, s, g)
+    out = {k: torch.empty_like(t["B"]) for k in ("dB", "dC")} | {"dA": torch.empty_like(t["A"]), "dD": torch.empty(g, device="cuda")}
+    op = rl.SelectiveScan(dtype="bf16", seq=s, batch=b, channels=g, state=n, groups=g)
+    op.backward(t | out | {"dY": dY})
+    half = rl.SelectiveScan(dtype="bf16", seq=s, batch=b // 2, channels=g, state=n, groups=g)
+    dA, dD = torch.zeros(g, n, dtype=torch.float64, device="cuda"), torch.zeros(g, dtype=torch.float64, device="cuda")
+    for at in (slice(0, b // 2), slice(b // 2, b)):
+        u = {k: x if k == "A" else x[at] for k, x in t.items()}
+        o = {k: torch.empty_like(u["B"]) for k in ("dB", "dC")} | {"dA": torch.empty_like(t["A"]), "dD": torch.empty(g, device="cuda")}
+        half.backward(u | o | {"dY": dY[at]})
+        assert torch.equal(o["dB"], out["dB"][at]) and torch.equal(o["dC"], out["dC"][at])
+        dA += o["dA"]
+        dD += o["dD"]
+    # sums of 64 rows' sums, all of one sign: 16 additions and three more; 8 and three in each half
+    for got, want in ((out["dA"], dA), (out["dD"], dD)):
+        assert ((got.double() - want).abs() <= 31 * 2.0 ** -24 * want.abs()).all()
+
+
 def test_scratch_while_its_memory_is_in_use():
     """The first calls of an object on one stream, while work queued on the current one still writes memory that was
     given back: the size of the scratch, many times."""

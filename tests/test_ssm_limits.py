@@ -63,3 +63,21 @@ def test_norm_limits():
     parts = 512     # of sums over the rows, whatever their number
     assert rl.rnn_norm_scratch_size(h) == (0, parts * 2 * 64 * 4)
     rl.rnn_norm_destroy(h)
+
+
+def test_scan_limits(monkeypatch):
+    monkeypatch.delenv("RNN_SCAN_CHUNK", raising=False)
+    scan = BF16 | dict(groups=1, state=128)
+    created("scan", scan | dict(seq=131072, batch=64, channels=2048))
+    created("scan", scan | dict(seq=16384, batch=64, channels=2048, groups=8))
+    created("scan", scan | dict(seq=1, batch=1, channels=65536))
+    created("scan", scan | dict(seq=1 << 20, batch=1 << 10, channels=2048, state=16, groups=32))     # B of 2^39 elements
+    refused(lambda: created("scan", scan | dict(seq=1 << 20, batch=1 << 10, channels=2048, state=16, groups=64)), UNSUPPORTED, "scan: ", "2^40")
+    # a token: workgroups of 256 threads, 64 channels each; the gradient of 128 states takes 512
+    token = scan | dict(seq=1, channels=2048)
+    created("scan", token | dict(batch=(1 << 19) - 1))
+    refused(lambda: created("scan", token | dict(batch=1 << 19)), UNSUPPORTED, "scan: ", "too large for one launch")
+    at_call("scan", token | dict(batch=1 << 18), backward=True)
+    many = scan | dict(seq=5, channels=2048)
+    created("scan", many | dict(batch=(1 << 18) - 1))
+    refused(lambda: created("scan", many | dict(batch=1 << 18)), UNSUPPORTED, "scan: ", "too large for one launch")
