@@ -301,14 +301,14 @@ template <int I, int N, int R>
 __device__ __forceinline__ void bc_dot(const float (&v)[R], float& acc, const float* x) {   // acc += sum_i value(I + i) x[i]
   static_assert(I / 16 == (I + N - 1) / 16, "one register");
   if constexpr (N == 1) {
-    asm("s_nop 1\n\tv_fmac_f32_dpp %0, %1, %2 row_newbcast:%3 " RNN_DPP : "+v"(acc) : "v"(v[I / 16]), "v"(x[0]), "n"(I % 16));
+    asm("s_nop 1\n\tv_fmac_f32_dpp %0, %1, %2 row_newbcast:%3 " RNN_DPP : "+&v"(acc) : "v"(v[I / 16]), "v"(x[0]), "n"(I % 16));
   } else if constexpr (N == 2) {
     asm("s_nop 1\n\tv_fmac_f32_dpp %0, %1, %2 row_newbcast:%4 " RNN_DPP "\n\tv_fmac_f32_dpp %0, %1, %3 row_newbcast:%5 " RNN_DPP
-        : "+v"(acc) : "v"(v[I / 16]), "v"(x[0]), "v"(x[1]), "n"(I % 16), "n"(I % 16 + 1));
+        : "+&v"(acc) : "v"(v[I / 16]), "v"(x[0]), "v"(x[1]), "n"(I % 16), "n"(I % 16 + 1));
   } else {
     asm("s_nop 1\n\tv_fmac_f32_dpp %0, %1, %2 row_newbcast:%6 " RNN_DPP "\n\tv_fmac_f32_dpp %0, %1, %3 row_newbcast:%7 " RNN_DPP
         "\n\tv_fmac_f32_dpp %0, %1, %4 row_newbcast:%8 " RNN_DPP "\n\tv_fmac_f32_dpp %0, %1, %5 row_newbcast:%9 " RNN_DPP
-        : "+v"(acc)
+        : "+&v"(acc)
         : "v"(v[I / 16]), "v"(x[0]), "v"(x[1]), "v"(x[2]), "v"(x[3]), "n"(I % 16), "n"(I % 16 + 1), "n"(I % 16 + 2), "n"(I % 16 + 3));
     if constexpr (N > 4) bc_dot<I + 4, N - 4>(v, acc, x + 4);
   }
@@ -317,14 +317,14 @@ template <int I, int N, int R>
 __device__ __forceinline__ void bc_add(const float (&v)[R], float* acc, float x) {   // acc[i] += value(I + i) x
   static_assert(I / 16 == (I + N - 1) / 16, "one register");
   if constexpr (N == 1) {
-    asm("s_nop 1\n\tv_fmac_f32_dpp %0, %1, %2 row_newbcast:%3 " RNN_DPP : "+v"(acc[0]) : "v"(v[I / 16]), "v"(x), "n"(I % 16));
+    asm("s_nop 1\n\tv_fmac_f32_dpp %0, %1, %2 row_newbcast:%3 " RNN_DPP : "+&v"(acc[0]) : "v"(v[I / 16]), "v"(x), "n"(I % 16));
   } else if constexpr (N == 2) {
     asm("s_nop 1\n\tv_fmac_f32_dpp %0, %2, %3 row_newbcast:%4 " RNN_DPP "\n\tv_fmac_f32_dpp %1, %2, %3 row_newbcast:%5 " RNN_DPP
-        : "+v"(acc[0]), "+v"(acc[1]) : "v"(v[I / 16]), "v"(x), "n"(I % 16), "n"(I % 16 + 1));
+        : "+&v"(acc[0]), "+&v"(acc[1]) : "v"(v[I / 16]), "v"(x), "n"(I % 16), "n"(I % 16 + 1));
   } else {
     asm("s_nop 1\n\tv_fmac_f32_dpp %0, %4, %5 row_newbcast:%6 " RNN_DPP "\n\tv_fmac_f32_dpp %1, %4, %5 row_newbcast:%7 " RNN_DPP
         "\n\tv_fmac_f32_dpp %2, %4, %5 row_newbcast:%8 " RNN_DPP "\n\tv_fmac_f32_dpp %3, %4, %5 row_newbcast:%9 " RNN_DPP
-        : "+v"(acc[0]), "+v"(acc[1]), "+v"(acc[2]), "+v"(acc[3])
+        : "+&v"(acc[0]), "+&v"(acc[1]), "+&v"(acc[2]), "+&v"(acc[3])
         : "v"(v[I / 16]), "v"(x), "n"(I % 16), "n"(I % 16 + 1), "n"(I % 16 + 2), "n"(I % 16 + 3));
     if constexpr (N > 4) bc_add<I + 4, N - 4>(v, acc + 4, x);
   }
