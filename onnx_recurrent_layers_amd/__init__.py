@@ -316,11 +316,31 @@ class Layer:
         self.device = torch.device(device)
         self.xw = torch.empty(max(self.xw_bytes, 256), dtype=torch.uint8, device=self.device)
         self.state = torch.empty(max(self.state_bytes, 256), dtype=torch.uint8, device=self.device)
+        # what the allocator hands out may still be in use by work queued on the
+        # stream that it counts it to: another stream's call waits for that
+        home = torch.cuda.current_stream(self.device)
+        self._home = home.cuda_stream
+        with torch.cuda.stream(home):
+            self._ready = None if torch.cuda.is_current_stream_capturing() else home.record_event()
+
+    def _take(self, stream):
+        """The scratch, for a call on `stream`."""
+        import torch
+        if stream.cuda_stream == self._home:
+            return
+        with torch.cuda.stream(stream):
+            if torch.cuda.is_current_stream_capturing():
+                return
+        if self._ready is not None:
+            stream.wait_event(self._ready)
+        for memory in (self.xw, self.state):
+            memory.record_stream(stream)     # (not reused, once this object is gone, before the call has run)
 
     def encode(self, tensors: dict, offsets: Optional[dict] = None, stream=None, events=None) -> None:
         import torch
         ops = make_operands(tensors, offsets)
         st = stream if stream is not None else torch.cuda.current_stream(self.device)
+        self._take(st)
         xw = self.xw.data_ptr() if self.xw_bytes else 0
         if events is None:
             rnn_encode(self.handle, ops, xw, self.state.data_ptr(), st.cuda_stream)

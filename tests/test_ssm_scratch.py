@@ -1,4 +1,4 @@
-"""Whose memory the operators' scratch is (no GPU: the stream, the allocator and
+"""Whose memory the operators' and layers' scratch is (no GPU: the stream, the allocator and
 the C calls are stand-ins)."""
 import contextlib
 
@@ -10,7 +10,13 @@ import onnx_recurrent_layers_amd as rl
 
 class Stream:
     def __init__(self, handle):
-        self.device, self.cuda_stream = torch.device("cuda", 0), handle
+        self.device, self.cuda_stream, self.waited = torch.device("cuda", 0), handle, []
+
+    def record_event(self):
+        return ("event", self.cuda_stream)
+
+    def wait_event(self, event):
+        self.waited.append(event)
 
 
 class Machine:
@@ -100,3 +106,20 @@ def test_another_devices_stream_takes_no_scratch(machine):
         with pytest.raises(rl.RnnError, match="stream: on cuda:1, expected cuda:0"):
             call({}, stream=other)
     assert machine.made == [] and op.calls == []
+
+
+def test_layer_on_another_stream_waits_for_its_scratch(machine, monkeypatch):
+    """A layer's scratch is made with the layer: a call on another stream waits for what was queued before it."""
+    from onnx_recurrent_layers_amd.synth import LayerSpec
+    calls = []
+    monkeypatch.setattr(rl, "rnn_encode", lambda *args: calls.append(args[-1]))
+    layer = rl.Layer(LayerSpec("LSTM", seq=5, batch=3, input=4, hidden=6), device="cuda:0")
+    other = Stream(7)
+    layer.encode({})
+    assert other.waited == machine.now.waited == [] and machine.recorded == []
+    layer.encode({}, stream=other)
+    assert calls == [0, 7] and other.waited == [("event", 0)] and machine.recorded == [7, 7]
+    machine.capturing = {9}
+    captured = Stream(9)
+    layer.encode({}, stream=captured)      # (no wait for uncaptured work may be captured)
+    assert captured.waited == [] and machine.recorded == [7, 7]
