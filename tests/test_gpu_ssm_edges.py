@@ -320,6 +320,40 @@ def test_scan_gradient_sums_in_two_launches(monkeypatch):
         assert ((got.double() - want).abs() <= 31 * 2.0 ** -24 * want.abs()).all()
 
 
+def test_first_call_captured(monkeypatch):
+    """An object whose first call, the one that makes its scratch, is captured: replays among eager calls of the same and
+    of another object, and eager calls once the graph is gone."""
+    monkeypatch.setenv("RNN_SCAN_CHUNK", "64")
+    v = positive(2, 300, 70, 16)
+    t = {k: v[k].float().cuda() for k in ("X", "delta", "B", "C", "Z", "A", "D")}
+
+    def outs():
+        return {"Y": torch.zeros_like(t["X"]), "final_state": torch.zeros(2, 70, 16, device="cuda")}
+
+    def new():
+        return rl.SelectiveScan(dtype="f32", seq=300, batch=2, channels=70, state=16)
+
+    other, want = new(), outs()
+    other.encode(t | want)
+    op, got, mine = new(), outs(), outs()
+    stream, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        op.encode(t | got)
+    for turn in range(4):
+        for x in got.values():
+            x.fill_(7)
+        graph.replay()
+        other.encode(t | outs())
+        op.encode(t | mine)
+        torch.cuda.synchronize()
+        assert all(torch.equal(got[k], want[k]) and torch.equal(mine[k], want[k]) for k in want), turn
+    del graph
+    held = [torch.full((op.forward_bytes // 4,), 5.0, device="cuda") for _ in range(8)]
+    op.encode(t | mine)
+    torch.cuda.synchronize()
+    assert all(torch.equal(mine[k], want[k]) for k in want) and all((h == 5).all() for h in held)
+
+
 def test_scratch_while_its_memory_is_in_use():
     """The first calls of an object on one stream, while work queued on the current one still writes memory that was
     given back: the size of the scratch, many times."""
