@@ -13,8 +13,10 @@
 //      many states), and each chunk's end state, sum of step sizes and gradient
 //      at its start.  That gradient needs no walk back: sum_s (prod_{r<=s} a_r)
 //      C_s gy_s runs forward with the product, at three operations and no
-//      exponential.  (Where steps grow the states, and so much that the product
-//      may leave f32, it is walked back after all.)
+//      exponential.  The product falls to zero harmlessly; but where steps grow
+//      the states it may leave f32 upwards, or come back from zero with steps of
+//      both signs.  The sum is not finite then, or marked so, and whoever wants
+//      it walks back after all.
 //   2. each chunk, segment after segment from its end: the segment's states
 //      and decays forward from the one written, kept in registers (at most 64
 //      of each a lane), then the gradients backward.
@@ -120,7 +122,7 @@ __global__ __launch_bounds__(NW * 64) void scan_ahead_kernel(ScanArgs a) {
     Q[i] = 1.f;
     G[i] = 0.f;
   }
-  float total = 0.f, span = 0.f;   // sums of step sizes and of their magnitudes
+  float total = 0.f;
   const bool behind = ch > 0;   // a chunk before this one needs the gradient at its start
   const bool gz = behind && a.have_z;
   float bias[V];
@@ -197,7 +199,6 @@ __global__ __launch_bounds__(NW * 64) void scan_ahead_kernel(ScanArgs a) {
         h[i] = __builtin_fmaf(e[i], h[i], bc_mul<at + i>(bc, f.y));
       });
       if (behind) {
-        span += __builtin_fabsf(f.x);
         const float g = dg[buf][t][lane];
         each<NS>([&](auto I) {
           constexpr int i = decltype(I)::value;
@@ -213,34 +214,6 @@ __global__ __launch_bounds__(NW * 64) void scan_ahead_kernel(ScanArgs a) {
   // (tiles past the end change and store nothing; a way out between two bodies
   // would have the compiler move registers whose loads are in flight)
   while (s < send) each<D>(body);
-  if (behind) {
-    // Q is within 2^100 of 1 unless the steps' exponents add up to more; and one
-    // that only falls loses nothing by falling to zero, since no later step's
-    // share would have been seen.  (With steps of one sign, both sums are the
-    // same number.)
-    bool risk = false;
-#pragma unroll
-    for (int i = 0; i < NS; ++i) {
-      const float all = __builtin_fabsf(A[i]) * span;
-      risk = risk || (all > 100.f && A[i] * total != -all);
-    }
-    if (__any(risk)) {
-#pragma unroll
-      for (int i = 0; i < NS; ++i) G[i] = 0.f;
-      const float db = a.dbias ? a.dbias[p.c] : 0.f;
-      for (int t = send - 1; t >= s0; --t) {
-        const int64_t row = r.base + t * r.step;
-        float d = float((reinterpret_cast<const T*>(a.delta.p) + p.c)[row * a.delta.rs]) + db;
-        if (a.softplus) d = softplus(d);
-        float g = float((reinterpret_cast<const T*>(a.dY.p) + p.c)[row * a.dY.rs]);
-        if (a.have_z) g *= gate_of(float((reinterpret_cast<const T*>(a.Z.p) + p.c)[row * a.Z.rs]));
-        const T* C = reinterpret_cast<const T*>(a.Cm.p) + row * a.Cm.rs + int64_t(p.g) * a.N;
-#pragma unroll
-        for (int i = 0; i < NS; ++i)
-          if (n0 + i < a.N) G[i] = __builtin_amdgcn_exp2f(d * A[i]) * __builtin_fmaf(float(C[n0 + i]), g, G[i]);
-      }
-    }
-  }
   if (p.ok && a.nchunk > 1) {
     const int64_t at = int64_t(b) * a.nchunk + ch;
     scan_put<NS>(a, a.loc, at, n0, p.c, h);
@@ -249,21 +222,51 @@ __global__ __launch_bounds__(NW * 64) void scan_ahead_kernel(ScanArgs a) {
   }
 }
 
+// Between the first two, where steps may be negative: the gradients at chunks'
+// starts are marked as not to be used for channels that have such steps.
+template <typename T>
+__global__ __launch_bounds__(256) void scan_signs_kernel(ScanArgs a) {
+  __shared__ int negative[64];
+  const int lane = int(threadIdx.x) & 63, w = int(threadIdx.x) >> 6;
+  const ScanPlace p = scan_place(a, a.nchunk, lane);
+  const int L = geo_len(a.geo, p.b), s0 = p.ch * a.chunk;
+  if (p.ch == 0 || s0 >= L) return;   // uniform
+  const int send = int(min(int64_t(s0) + a.chunk, int64_t(L)));
+  const StepRows r = step_rows(a.geo, p.b, L);
+  const float bias = a.dbias ? a.dbias[p.c] : 0.f;
+  if (w == 0) negative[lane] = 0;
+  __syncthreads();
+  bool below = false;
+#pragma unroll 4
+  for (int s = s0 + w; s < send; s += 4)
+    below = below || float((reinterpret_cast<const T*>(a.delta.p) + p.c)[(r.base + s * r.step) * a.delta.rs]) + bias < 0.f;
+  if (below) negative[lane] = 1;
+  __syncthreads();
+  if (!negative[lane] || !p.ok) return;
+  float* to = a.gloc + (int64_t(p.b) * a.nchunk + p.ch) * a.np * a.C + p.c;
+  for (int n = w; n < a.np; n += 4) to[int64_t(n) * a.C] = __builtin_nanf("");
+}
+
 // Launch 2.  PAD: there are states past N among a wave's, or lanes past a
-// group's channels, which are kept zero: their inputs are, but zero times an
-// infinite one is not a number, and would enter the sums over states (dX,
-// ddelta, dZ) and over lanes (dB, dC).  (8 rows of 512 steps by 1024 channels,
-// bf16, the whole pass: 10 states 130 us, 124.5 if they were left alone; 16
-// states by 1000 channels 131, 126.5.  Only where a value is not finite, as the
-// first launch would leave word of it: 127.4 and 129.9, but 16 states by 1024
-// channels, which have none, 126.5 instead of 125.)
+// group's channels.  They are zero as their inputs are, and stay so while values
+// are finite; but zero times an infinite one is not a number, and would enter
+// the sums over states (dX, ddelta, dZ) and over lanes (dB, dC).  So they are put
+// back to zero in the steps of a segment with such a value, or, where watching
+// costs more than that, with states past N in all.  (8 rows of 512 steps by 1024
+// channels, bf16, the whole pass, and what it took when they were left alone: 10
+// states 128 us, 125; 1 state 122, 120.5; 40 states 450, 415; 16 states by 1000
+// channels 129, 126; and 16 by 1024, which has none, 125.5, 125.)
 template <typename T, int NW, int NS, bool VEC, bool PAD>
-__device__ __forceinline__ void scan_back(const ScanArgs& a, float4 (*in)[64], float (*part)[NW][scan_segment(NS)][64],
-                                          float (*sbc)[2 * NW * NS]) {
+__global__ __launch_bounds__(NW * 64) void scan_back_kernel(ScanArgs a) {
   constexpr int TS = scan_segment(NS);
   typedef Task<NW, TS> Mine;
   constexpr int V = Mine::V;
   constexpr int FOLDS = (TS * 2 * NS + 63) / 64;
+  __shared__ float4 in[TS][64];               // step size, input, gy of a step
+  __shared__ float part[3][NW][TS][64];       // the waves' parts of y, sum G B, sum q A
+  __shared__ float sbc[TS][2 * NW * NS];
+  constexpr bool WATCH = PAD && NS == 2;      // whether states past N are watched for an input that is not finite
+  __shared__ int marks[2];                    // WATCH: this segment and the next have one
   const int lane = int(threadIdx.x) & 63, w = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
   const ScanPlace p = scan_place(a, a.nchunk, lane);
   const int b = p.b, ch = p.ch, n0 = w * NS;
@@ -289,6 +292,24 @@ __device__ __forceinline__ void scan_back(const ScanArgs& a, float4 (*in)[64], f
     scan_load_state<NS>(a, a.dfin, cs, n0, G);
     const int last_chunk = (L - 1) / a.chunk;
     scan_through<NS>(a, a.gloc, last_chunk - ch, p.c, n0, A, G, [&](int k) { return int64_t(b) * a.nchunk + last_chunk - k; });
+    bool walk = false;
+#pragma unroll
+    for (int i = 0; i < NS; ++i) walk = walk || !(__builtin_fabsf(G[i]) < __builtin_huge_valf());
+    if (__any(walk)) {
+      scan_load_state<NS>(a, a.dfin, cs, n0, G);
+      const float step_bias = a.dbias ? a.dbias[p.c] : 0.f;
+      for (int t = L - 1; t >= send; --t) {
+        const int64_t row = r.base + t * r.step;
+        float d = float((reinterpret_cast<const T*>(a.delta.p) + p.c)[row * a.delta.rs]) + step_bias;
+        if (a.softplus) d = softplus(d);
+        float g = float((reinterpret_cast<const T*>(a.dY.p) + p.c)[row * a.dY.rs]);
+        if (a.have_z) g *= gate_of(float((reinterpret_cast<const T*>(a.Z.p) + p.c)[row * a.Z.rs]));
+        const T* C = reinterpret_cast<const T*>(a.Cm.p) + row * a.Cm.rs + int64_t(p.g) * a.N;
+#pragma unroll
+        for (int i = 0; i < NS; ++i)
+          if (n0 + i < a.N) G[i] = __builtin_amdgcn_exp2f(d * A[i]) * __builtin_fmaf(float(C[n0 + i]), g, G[i]);
+      }
+    }
     float big = 0.f;   // the largest state at the chunk's start
     auto is = [&](int i) { return !PAD || (p.ok && n0 + i < a.N); };   // whether a lane's state is one
 #pragma unroll
@@ -328,6 +349,11 @@ __device__ __forceinline__ void scan_back(const ScanArgs& a, float4 (*in)[64], f
     const int mine = int(__builtin_bitreverse32(unsigned(lane)) >> 26);
     float* pbc = a.pbc + (int64_t(p.cb) * a.geo.B + b) * a.geo.S * (2 * a.np) + w * 2 * NS;
 
+    int mark = 0;
+    if constexpr (WATCH) {
+      if (threadIdx.x < 2) marks[threadIdx.x] = 0;
+      __syncthreads();
+    }
     fetch(last);
     for (int s = last; s >= s0; s -= TS) {
       float x[V], d[V], g[V], gy[V], z[V], raw[V], h0[NS];
@@ -357,6 +383,12 @@ __device__ __forceinline__ void scan_back(const ScanArgs& a, float4 (*in)[64], f
         d[i] = there ? d[i] : 0.f;
         in[k.t][k.q + i] = make_float4(d[i], d[i] * x[i], gy[i], 0.f);
       }
+      if (WATCH && a.N < a.np) {
+        float odd = 0.f;   // (NaN for an infinite step size, input or gy)
+#pragma unroll
+        for (int i = 0; i < V; ++i) odd = __builtin_fmaf(d[i] * x[i], 0.f, __builtin_fmaf(gy[i], 0.f, odd));
+        if (__any(odd != odd)) marks[mark] = 1;
+      }
       BC.put(nbc, s, send, sbc);
 #pragma unroll
       for (int i = 0; i < NS; ++i) h0[i] = nh[i];
@@ -379,72 +411,90 @@ __device__ __forceinline__ void scan_back(const ScanArgs& a, float4 (*in)[64], f
       float bc[BCRegs<NW, NS, TS>::R];
       BCRegs<NW, NS, TS>::get(sbc, w, lane, bc);
 
-      float h[TS][NS], e[TS][NS];
-      each<TS>([&](auto TT) {
-        constexpr int t = decltype(TT)::value, at = t * 2 * NS;
-        const float4 f = in[t][lane];
-        each<NS>([&](auto I) {
-          constexpr int i = decltype(I)::value;
-          const float decay = __builtin_amdgcn_exp2f(f.x * A[i]);
-          const float next = __builtin_fmaf(decay, t ? h[t ? t - 1 : 0][i] : h0[i], bc_mul<at + i>(bc, f.y));
-          e[t][i] = is(i) ? decay : 0.f;
-          h[t][i] = is(i) ? next : 0.f;
-        });
-        if (a.dZ.p) {
-          float v = 0.f;
-          bc_dot<at + NS, NS>(bc, v, h[t]);
-          part[0][w][t][lane] = v;
-        }
-        __builtin_amdgcn_sched_barrier(0);
-      });
-      // Steps past the row's end (in the segment that is taken first) add q * 0 to
-      // dA, which is not 0 where a state or gradient is infinite: with the row's
-      // last step the sum begins anew.
-      const int edge = s + TS > send ? send - 1 - s : -1;
-      each<TS>([&](auto TT) {
-        constexpr int t = TS - 1 - decltype(TT)::value, base = decltype(TT)::value * 2 * NS;
-        const float4 f = in[t][lane];
-        if (t == edge) {   // (uniform)
-#pragma unroll
-          for (int i = 0; i < NS; ++i) dA[i] = 0.f;
-        }
-        float sb = 0.f, sq = 0.f;
-        auto out = [&](int fold_at, float v) {   // 64 sums are there
-          const int at = fold_at * 64 + mine;
-          const int st = s + TS - 1 - at / (2 * NS);
-          if (at < TS * 2 * NS && st < send) pbc[int64_t(st) * (2 * a.np) + at % (2 * NS)] = v;
-        };
-        bc_add<t * 2 * NS + NS, NS>(bc, G, f.z);
-        if constexpr (PAD) {
-#pragma unroll
-          for (int i = 0; i < NS; ++i) G[i] = is(i) ? G[i] : 0.f;
-        }
-        bc_dot<t * 2 * NS, NS>(bc, sb, G);
-        each<NS>([&](auto I) {
-          constexpr int i = decltype(I)::value;
-          const float v = fold.template push<base + i>(G[i] * f.y);
-          if constexpr ((base + i) % 64 == 63) out((base + i) / 64, v);
-          G[i] *= e[t][i];
-          const float qi = G[i] * (t ? h[t ? t - 1 : 0][i] : h0[i]);
-          sq = __builtin_fmaf(qi, A[i], sq);
-          dA[i] = __builtin_fmaf(qi, f.x, dA[i]);
-        });
-        each<NS>([&](auto I) {
-          constexpr int i = decltype(I)::value;
-          const float v = fold.template push<base + NS + i>(f.z * h[t][i]);
-          if constexpr ((base + NS + i) % 64 == 63) out((base + NS + i) / 64, v);
-        });
-        if constexpr (t == 0 && (TS * 2 * NS) % 64 != 0) {   // the last fold's empty places
-          each<FOLDS * 64 - TS * 2 * NS>([&](auto I) {
-            constexpr int at = TS * 2 * NS + decltype(I)::value;
-            const float v = fold.template push<at>(0.f);
-            if constexpr (at % 64 == 63) out(at / 64, v);
+      auto steps = [&](auto mask) {
+        constexpr bool MASK = decltype(mask)::value;
+        float h[TS][NS], e[TS][NS];
+        each<TS>([&](auto TT) {
+          constexpr int t = decltype(TT)::value, at = t * 2 * NS;
+          const float4 f = in[t][lane];
+          each<NS>([&](auto I) {
+            constexpr int i = decltype(I)::value;
+            const float decay = __builtin_amdgcn_exp2f(f.x * A[i]);
+            const float next = __builtin_fmaf(decay, t ? h[t ? t - 1 : 0][i] : h0[i], bc_mul<at + i>(bc, f.y));
+            e[t][i] = !MASK || is(i) ? decay : 0.f;
+            h[t][i] = !MASK || is(i) ? next : 0.f;
           });
+          if (a.dZ.p) {
+            float v = 0.f;
+            bc_dot<at + NS, NS>(bc, v, h[t]);
+            part[0][w][t][lane] = v;
+          }
+          __builtin_amdgcn_sched_barrier(0);
+        });
+        // Steps past the row's end (in the segment that is taken first) add q * 0 to
+        // dA, which is not 0 where a state or gradient is infinite: with the row's
+        // last step the sum begins anew.
+        const int edge = s + TS > send ? send - 1 - s : -1;
+        each<TS>([&](auto TT) {
+          constexpr int t = TS - 1 - decltype(TT)::value, base = decltype(TT)::value * 2 * NS;
+          const float4 f = in[t][lane];
+          if (t == edge) {   // (uniform)
+#pragma unroll
+            for (int i = 0; i < NS; ++i) dA[i] = 0.f;
+          }
+          float sb = 0.f, sq = 0.f;
+          auto out = [&](int fold_at, float v) {   // 64 sums are there
+            const int at = fold_at * 64 + mine;
+            const int st = s + TS - 1 - at / (2 * NS);
+            if (at < TS * 2 * NS && st < send) pbc[int64_t(st) * (2 * a.np) + at % (2 * NS)] = v;
+          };
+          bc_add<t * 2 * NS + NS, NS>(bc, G, f.z);
+          if constexpr (MASK) {
+#pragma unroll
+            for (int i = 0; i < NS; ++i) G[i] = is(i) ? G[i] : 0.f;
+          }
+          bc_dot<t * 2 * NS, NS>(bc, sb, G);
+          each<NS>([&](auto I) {
+            constexpr int i = decltype(I)::value;
+            const float v = fold.template push<base + i>(G[i] * f.y);
+            if constexpr ((base + i) % 64 == 63) out((base + i) / 64, v);
+            G[i] *= e[t][i];
+            const float qi = G[i] * (t ? h[t ? t - 1 : 0][i] : h0[i]);
+            sq = __builtin_fmaf(qi, A[i], sq);
+            dA[i] = __builtin_fmaf(qi, f.x, dA[i]);
+          });
+          each<NS>([&](auto I) {
+            constexpr int i = decltype(I)::value;
+            const float v = fold.template push<base + NS + i>(f.z * h[t][i]);
+            if constexpr ((base + NS + i) % 64 == 63) out((base + NS + i) / 64, v);
+          });
+          if constexpr (t == 0 && (TS * 2 * NS) % 64 != 0) {   // the last fold's empty places
+            each<FOLDS * 64 - TS * 2 * NS>([&](auto I) {
+              constexpr int at = TS * 2 * NS + decltype(I)::value;
+              const float v = fold.template push<at>(0.f);
+              if constexpr (at % 64 == 63) out(at / 64, v);
+            });
+          }
+          part[1][w][t][lane] = sb;
+          part[2][w][t][lane] = sq;
+          __builtin_amdgcn_sched_barrier(0);
+        });
+      };
+      if constexpr (PAD) {
+        float odd = 0.f;
+#pragma unroll
+        for (float v : bc) odd = __builtin_fmaf(v, 0.f, odd);
+        bool fix = a.N < a.np;
+        if (WATCH && fix) {
+          fix = __builtin_amdgcn_readfirstlane(marks[mark]);
+          mark ^= 1;
+          if (threadIdx.x == 0) marks[mark] = 0;
         }
-        part[1][w][t][lane] = sb;
-        part[2][w][t][lane] = sq;
-        __builtin_amdgcn_sched_barrier(0);
-      });
+        if (fix || __any(odd != odd)) steps(IntC<1>{});
+        else steps(IntC<0>{});
+      } else {
+        steps(IntC<0>{});
+      }
       __syncthreads();
       float y[V], sb[V], sq[V];
 #pragma unroll
@@ -533,17 +583,6 @@ __device__ __forceinline__ void scan_back(const ScanArgs& a, float4 (*in)[64], f
   }
 }
 
-template <typename T, int NW, int NS, bool VEC>
-__global__ __launch_bounds__(NW * 64) void scan_back_kernel(ScanArgs a) {
-  constexpr int TS = scan_segment(NS);
-  __shared__ float4 in[TS][64];               // step size, input, gy of a step
-  __shared__ float part[3][NW][TS][64];       // the waves' parts of y, sum G B, sum q A
-  __shared__ float sbc[TS][2 * NW * NS];
-  const int cb = scan_order(a.balance) % (a.G * a.cbg) % a.cbg;
-  if (a.N == a.np && (cb + 1) * 64 <= a.cpg) scan_back<T, NW, NS, VEC, false>(a, in, part, sbc);
-  else scan_back<T, NW, NS, VEC, true>(a, in, part, sbc);
-}
-
 // Launch 3: workgroups [0, nbc) sum dB and dC over their group's channel
 // blocks, one element of one row a thread; then 64 columns of dA, then of dD
 // and ddelta_bias, a workgroup, four threads a column.
@@ -610,7 +649,10 @@ template <typename T, int NW, int NS, bool VEC>
 hipError_t back_of(const ScanArgs& a, hipStream_t s) {
   const int64_t blocks = int64_t(a.geo.B) * a.nchunk * a.G * a.cbg;
   if (hipError_t e = go(scan_ahead_kernel<T, NW, NS, VEC>, blocks, NW * 64, a, s); e != hipSuccess) return e;
-  return go(scan_back_kernel<T, NW, NS, VEC>, blocks, NW * 64, a, s);
+  if (!a.softplus && a.nchunk > 1)
+    if (hipError_t e = go(scan_signs_kernel<T>, blocks, 256, a, s); e != hipSuccess) return e;
+  return a.N < a.np || a.cpg % 64 ? go(scan_back_kernel<T, NW, NS, VEC, true>, blocks, NW * 64, a, s)
+                                  : go(scan_back_kernel<T, NW, NS, VEC, false>, blocks, NW * 64, a, s);
 }
 
 template <typename T>

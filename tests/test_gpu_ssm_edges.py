@@ -110,6 +110,20 @@ def test_scan_gradient_infinite_value(monkeypatch, n, chunk, name, step):
     assert name in ("X", "delta") or want["dX"][1, step, 2] == INF
 
 
+@pytest.mark.parametrize("n,c", [(1, 6), (5, 70), (10, 64), (16, 70), (40, 6), (100, 66)])
+@pytest.mark.parametrize("chunk", [0, 32])
+@pytest.mark.parametrize("name", ["X", "dY", "B", "C"])
+def test_scan_gradient_infinite_value_between(monkeypatch, n, c, chunk, name):
+    """Infinite values with whole tiles of others before and after them, twice."""
+    monkeypatch.setenv("RNN_SCAN_CHUNK", str(chunk or 1 << 20))
+    note(f"n {n} c {c} chunk {chunk} {name}")
+    v = positive(2, 96, c, n)
+    bad = dict(v, **{name: v[name].clone()})
+    for row, step in ((0, 24), (0, 70), (1, 40)):
+        bad[name][row, step, 0] = INF
+    scan_both(bad, finite=v, chunk=chunk or 1 << 30)
+
+
 @pytest.mark.parametrize("n,c,groups", [(4, 6, 1), (16, 66, 1), (5, 6, 2), (64, 3, 3), (8, 64, 1)])
 @pytest.mark.parametrize("name,step", [("B", 7), ("C", 7), ("B", 31), ("C", 31)])
 def test_scan_infinite_weight(monkeypatch, n, c, groups, name, step):
