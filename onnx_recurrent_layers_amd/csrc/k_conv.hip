@@ -2,16 +2,21 @@
 // gradient.
 //
 // y_s = act(b + sum_k w_k x_{s-K+1+k}): 2K + about 6 operations for each
-// element read once and written once, so both directions are bound by memory.
-// A thread walks `tile` steps of V neighbouring channels (16 bytes of a row
-// forward, 4 channels backward) with the last K inputs in registers: each
-// element is read once but for the K-1 steps before a tile, which the cache
-// holds (the tile before has just read them).  Eight steps' loads are in
-// flight at once.  (8 rows of 1024 steps by 2048 channels, 4 taps, 16 bits: all
-// steps there 18.0 us for 67 MB, which is a copy's rate; its gradient 30.4 us
-// for 100 MB, at 41 vector instructions an element before the way without
-// questions, and 4.7 for the sums of 128 partials; 64 single tokens 5.3 us,
-// a few trips to memory one after another, not their 2 MB.)
+// element read once and written once, so memory is what the forward pass cannot
+// do without.  A thread walks `tile` steps of V neighbouring channels (16 bytes
+// of a row forward, 4 channels backward) with the last K inputs in registers:
+// each element is read once but for the K-1 steps before a tile, which the cache
+// holds (the tile before has just read them).  Eight steps' loads are in flight
+// at once; but before them the K-1 inputs before the tile and the bias, and
+// after the stores the final state's inputs, are loads behind branches, each
+// waited for, and with walks of eight steps these trips are what bounds it.
+// Kernel times, 4 taps, 16 bits, under a trace (the whole call in brackets): 8
+// rows of up to 1024 steps by 2048 channels, 55 MB, 16.5 us (15.7), 3.4 TB/s,
+// where layer normalization moves 67 MB in 14 to 15.6 (12.8); all steps there,
+// 67 MB, (17.0); the gradient, 100 MB, 30.4, at 34 vector instructions an element
+// with the vector units busy for 55 of 100 clocks, and 4.8 for the sums of 128
+// partials (32.6 both); 64 single tokens 5.2 (6.6): trips to memory one after
+// another, not their 2 MB.
 #include <type_traits>
 
 #include "seq_device.h"
@@ -214,8 +219,8 @@ __global__ __launch_bounds__(256) void conv_backward_kernel(ConvArgs a) {
       gp += 4 * gd;
       if (s + 4 < L && s + 4 - K + 1 < e1) fetch(s + 4);
       // WHOLE: steps of this tile, and inputs that are its own and not the final
-      // state's, which leaves four steps without a question asked (measured:
-      // 32.3 us, with the questions 35.1)
+      // state's, which leaves four steps without a question asked (8 x 1024 x
+      // 2048, the whole call: 32.6 us, with the questions 35.1)
       auto four = [&](auto whole) {
         constexpr bool WHOLE = decltype(whole)::value;
 #pragma unroll

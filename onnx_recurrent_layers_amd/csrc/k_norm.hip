@@ -11,10 +11,14 @@
 //
 // A row is taken by W threads (a part of a wave, or a workgroup), V
 // neighbouring values a time (16 bytes where rows and stride allow), M times;
-// rows too long for registers are read again for each use.  (8192 rows of 2048,
-// 16 bits: forward 14.0 us for 67 MB, a copy's rate; gradient 25.1 us for 101 MB
-// and 4.0 for the sums of 512 partials, where 1024 partials took as long, 27.6
-// us together against 27.3.  64 rows of 1024, f32: 3.2 us.)
+// rows too long for registers are read again for each use.  Rows that are not
+// whole 16-byte pieces go one value an access (8192 rows of 1290, 16 bits: 23 us,
+// of 1288 11), and above 2048 of them count as too long.  (8192 rows of 2048, 16
+// bits, the whole call: forward 12.8 us for 67 MB, 5.2 TB/s, a copy of 32 MiB
+// taking 10.1; gradient 27.6 for 101 MB, of which the sums of 512 partials are
+// 4.6, and 1024 partials took as long.  2048 rows of 8192, gradient: f32 76 us
+// for 201 MB, 16 bits 40 for 101, with 66 and 32 registers spilled.  64 rows of
+// 1024, f32: 3.2 us the kernel.)
 #include "seq_device.h"
 
 namespace rnnhip {

@@ -55,8 +55,9 @@ __device__ __forceinline__ int scan_row_of_rank(const ScanArgs& a, int rank) {
   return __builtin_amdgcn_readfirstlane(found);
 }
 
-// A workgroup's work.  A lane past its group's channels works on the last one,
-// as that channel's own lane does.
+// A workgroup's work.  A lane past its group's channels takes the last one's
+// states and weights, with inputs that are some other channel's or zero: what it
+// computes is stored nowhere.
 struct ScanPlace {
   int b, ch, g, cb;   // batch row, chunk, group, channel block of all groups
   unsigned c;         // channel
@@ -291,7 +292,8 @@ struct BCRegs {
 };
 // Value I of [step][B, C][NS] as a factor, and as one of fused multiply-adds
 // acc += value x.  (The two waits stand for a value just written: the compiler
-// looks after those of its own instructions only.)
+// looks after those of its own instructions only.  An accumulator is written
+// before the last factor is read: `&`.)
 template <int I, int R>
 __device__ __forceinline__ float bc_mul(const float (&v)[R], float x) {
   return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v[I / 16]), 0x150 + I % 16, 0xf, 0xf, true)) * x;

@@ -32,13 +32,23 @@
 // is left: two to three instructions a value, where one sum after another
 // would take twelve, and no meeting of waves.
 //
-// 8 rows of 512 steps by 1024 channels, 16 states, bf16: launch 1 39.5 us,
-// launch 2 86, launch 3 4.8.  Launch 2 issues 27 vector instructions a (step,
-// channel, state) where the forward pass issues 9 (by the counters, which show
-// the vector units busy for 65 of 100 clocks), and its registers and 118 KB of
-// shared memory leave a compute unit one workgroup: these bound it, not its 60
-// MB.  Four waves of four states instead of eight of two: 129 us the whole pass
-// at best against 123.
+// 8 rows of 512 steps by 1024 channels, 16 states, bf16: launch 1 40 us, launch
+// 2 87, launch 3 4.8.  Launch 2 issues 27 vector instructions a (step, channel,
+// state) where the forward pass issues 9 (by the counters, which show the vector
+// units busy for 66 of 100 clocks), and its registers and 118 KB of shared memory
+// leave a compute unit one workgroup: these bound it, not its 60 MB.  Four waves
+// of four states instead of eight of two: 129 us the whole pass at best against
+// 123.
+//
+// More states.  Launch 1 does not fit its 256 registers from 24 states on: 61 to
+// 102 are spilled at 24, 22 to 40 at 32, 77 to 98 at 64 and 157 to 183 at 128;
+// launch 2 spills 24 to 44 at 24 and 71 to 114 at 128, and 18 at 64 where there
+// are places without a state.  And segments of 8
+// steps at 64 states, of 4 at 128, are more states written ahead: for 8 x 1024 x
+// 4096 the scratch is 0.2 GB at 16 states, 1.4 at 64 and 4.9 at 128, most of it
+// written and read once.  (8 x 512 x 1024, the whole pass and launches 1 and 2: 24
+// states 245 us, 98 and 142; 32 206, 80 and 132; 64 420, 183 and 233; 128 1445,
+// 399 and 1037.)
 #pragma once
 
 #include <algorithm>

@@ -37,8 +37,11 @@
 // over a chunk is exp(A * sum)); the second joins them at its start.  That
 // costs the recurrence twice, so it is done only where the chunks fill a chip
 // that the rows alone leave empty (rule in seq_api.cpp).  (1 row of 4096 steps
-// by 2048 channels, 16 states, f16: 39.3 us of the first launch and 53.4 of the
-// second under a profiler, 87 together without.)
+// by 2048 channels, f16: 16 states 40 us of the first launch and 55 of the second
+// under a trace, 87.4 together without; 64 states, bf16, 113 and 142, 254; 128
+// states 665 and 258, 920.  At 64 and 128 the first launch does not fit its
+// registers: 4 to 10 and 174 to 182 of them are spilled, in its loop.  Rows
+// enough, 8 x 1024 x 2048: 64 states 254 us, 128 states 465.)
 #pragma once
 
 #include "scan_device.h"
@@ -49,7 +52,10 @@ namespace {
 // LOCAL: the first of two launches (end states and sums of all chunks but
 // each row's last); else the outputs.  PAD: there are states past N among a
 // wave's, which are kept zero in a step's y: their B and C are zero, but times
-// an infinite step or state that is not a number.
+// an infinite step or state that is not a number.  (8 x 1024 x 2048, bf16: 10
+// states 122 us, 114.5 if they are left alone; 20 states 174.5 and 162.5.  Zeroed
+// only in tiles with an infinite step, as whoever prepares them would mark it:
+// 127 and 173.5.)
 template <typename T, int NW, int NS, bool LOCAL, bool VEC, bool PAD>
 __global__ __launch_bounds__(NW * 64) void scan_kernel(ScanArgs a) {
   constexpr int TT = kScanTile, D = 2;   // steps of a tile, tiles of rows in flight

@@ -262,9 +262,10 @@ extern "C" int rnn_conv_create(const rnn_conv_desc* desc, rnn_conv** out) {
   if (bytes_of({d.batch, d.width, d.channels, es}) < 0) return fail(RNN_ERR_SHAPE, kConv, "initial_state: size overflows");
   // Steps a thread walks: long walks read the K-1 steps before them less
   // often, short ones give the chip more threads: as many steps as leave the
-  // chip this many threads.  (8 x 1024 x 2048, 16 bits, forward: 131072 threads
-  // 16.6 us, 262144 and 524288 15.4; backward, where a thread also writes a
-  // partial sum: 65536 45.0, 131072 35.1, 262144 36.6, 524288 40.9.)
+  // chip this many threads.  (8 x 1024 x 2048, 16 bits, the whole call.  Forward:
+  // 131072 threads 16.1 us, 262144 and 524288 17.0, but with rows of unequal
+  // length, as prompts have, 17.4, 16.1 and 16.1.  Backward, where a thread also
+  // writes a partial sum: 65536 40.6, 131072 33.4, 262144 38.3, 524288 38.1.)
   auto tile = [&](int64_t least, int v, int64_t threads) {
     int64_t t = 64;
     while (t > least && d.batch * ceil_div(d.seq, t) * ceil_div(d.channels, v) < threads) t /= 2;
@@ -695,9 +696,11 @@ extern "C" int rnn_norm_create(const rnn_norm_desc* desc, rnn_norm** out) {
   // partial sums of dScale and dB: two workgroups a compute unit, but four
   // rows at least for each
   n->parts = int(std::max<int64_t>(1, std::min<int64_t>(512, ceil_div(d.rows, 4))));
-  // rows too long for a workgroup's registers: their columns are summed 64 a
-  // workgroup, and 2048 of those fill the chip (1024 rows of 16384: 42.7 us
-  // the whole backward pass; 1024 of them 51.6, 8192 45.8)
+  // rows too long for a workgroup's registers whatever their alignment: their
+  // columns are summed 64 a workgroup, and 2048 of those fill the chip (1024
+  // rows of 16384: 42.7 us the whole backward pass; 1024 of them 51.6, 8192
+  // 45.8).  (Shorter rows go that way too, from 2049 values on, when they are
+  // not whole 16-byte pieces; they keep up to 512 parts.)
   if (d.size > 8192) n->parts = int(std::max<int64_t>(1, std::min<int64_t>(n->parts, ceil_div(2048, ceil_div(d.size, 64)))));
   Regions r;
   r.take({n->parts, 2, d.size, 4});

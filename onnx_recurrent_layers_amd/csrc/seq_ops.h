@@ -134,8 +134,9 @@ inline void scan_split(int64_t N, bool backward, int* nw, int* np) {
   *np = split[i].nw * split[i].ns;
   if (backward && split[i].upto == 16) *nw = 8;
 }
-// Steps of a segment of the backward pass, from a wave's states: what a lane's
-// registers hold of states and decays, at most 64 of each.
+// Steps of a segment of the backward pass, from a wave's states: at most 64
+// states and as many decays a lane.  (Its 256 registers hold them with all else
+// up to 16 states in all, and nearly so at 32 and 64; see scan_grad_kernel.h.)
 constexpr int scan_segment(int ns) { return ns <= 4 ? 16 : ns <= 8 ? 8 : 4; }
 
 hipError_t launch_conv(const ConvArgs& a, int dtype, int vec, hipStream_t s);
