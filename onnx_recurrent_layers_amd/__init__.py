@@ -318,10 +318,11 @@ class Layer:
         self.state = torch.empty(max(self.state_bytes, 256), dtype=torch.uint8, device=self.device)
         # what the allocator hands out may still be in use by work queued on the
         # stream that it counts it to: another stream's call waits for that
-        home = torch.cuda.current_stream(self.device)
-        self._home = home.cuda_stream
-        with torch.cuda.stream(home):
-            self._ready = None if torch.cuda.is_current_stream_capturing() else home.record_event()
+        if self.device.type == "cuda":
+            home = torch.cuda.current_stream(self.device)
+            self._home = home.cuda_stream
+            with torch.cuda.stream(home):
+                self._ready = None if torch.cuda.is_current_stream_capturing() else home.record_event()
 
     def _take(self, stream):
         """The scratch, for a call on `stream`."""

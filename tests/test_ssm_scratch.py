@@ -123,3 +123,10 @@ def test_layer_on_another_stream_waits_for_its_scratch(machine, monkeypatch):
     captured = Stream(9)
     layer.encode({}, stream=captured)      # (no wait for uncaptured work may be captured)
     assert captured.waited == [] and machine.recorded == [7, 7]
+
+
+def test_layer_off_the_device():
+    """A layer's plan and scratch sizes can be had where there is no GPU."""
+    from onnx_recurrent_layers_amd.synth import LayerSpec
+    layer = rl.Layer(LayerSpec("LSTM", seq=5, batch=3, input=4, hidden=6), device="cpu")
+    assert layer.plan.steps == 5 and layer.state.numel() >= layer.state_bytes
