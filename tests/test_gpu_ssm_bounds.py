@@ -15,12 +15,14 @@ pytestmark = pytest.mark.gpu
 
 
 def scan_case(monkeypatch, dtype, b, s, c, n, chunk, groups=1, lens=None, reverse=False, layout=1, gate=True, softplus=True, pad=0,
-              odd=0, seed=0):
-    """Forward and backward with everything there, chunks of `chunk` steps (0: one)."""
+              odd=0, seed=0, signed=False):
+    """Forward and backward with everything there, chunks of `chunk` steps (0: one).  `signed`: steps of both signs."""
     note(f"scan {dtype} b{b} s{s} c{c} n{n} chunk {chunk} groups {groups} lens {lens} reverse {reverse} layout {layout}")
     monkeypatch.setenv("RNN_SCAN_CHUNK", str(chunk or 1 << 20))
     dt, f32 = ref.TYPES[dtype], torch.float32
     v = scan_values(dtype, b, s, c, n, groups, softplus, seed)
+    if signed:
+        v["delta"] = v["delta"] * torch.where(torch.arange(s) % 3 == 0, -1.0, 1.0)[None, :, None]
     kw = dict(D=v["D"], Z=v["Z"] if gate else None, delta_bias=v["bias"], lens=lens, initial_state=v["init"], groups=groups,
               softplus=softplus, reverse=reverse)
     main = [v[k] for k in ("X", "delta", "A", "B", "C")]
@@ -88,6 +90,13 @@ def test_scan_many_states(monkeypatch, dtype, n, groups, c, chunk):
 @pytest.mark.parametrize("gate,softplus", [(False, True), (True, False), (False, False)])
 def test_scan_options(monkeypatch, gate, softplus):
     scan_case(monkeypatch, "f32", 2, 70, 66, 16, 32, 2, gate=gate, softplus=softplus)
+
+
+@pytest.mark.parametrize("dtype,c,n,groups,layout,reverse,lens,pad", [
+    ("f32", 130, 16, 2, 0, True, [130, 64, 33, 0], 0), ("bf16", 66, 24, 1, 1, False, None, 6), ("f16", 70, 5, 1, 1, True, [97, 130, 32, 65], 3)])
+def test_scan_steps_of_both_signs(monkeypatch, dtype, c, n, groups, layout, reverse, lens, pad):
+    """Without softplus, every third step back: gradients at chunks' starts are walked back to, not summed forward."""
+    scan_case(monkeypatch, dtype, 4, 130, c, n, 32, groups, lens, reverse, layout, softplus=False, pad=pad, signed=True)
 
 
 def norm_case(dtype, rows, size, far=0.0, pad=0, odd=0):
