@@ -503,6 +503,64 @@ int rnn_norm_encode(const rnn_norm* norm, const rnn_norm_operands* operands, voi
 int rnn_norm_encode_backward(const rnn_norm* norm, const rnn_norm_operands* operands,
                              const rnn_norm_gradients* gradients, void* scratch, void* stream);
 
+/* Linear attention with a decay for each head: a recurrence whose state is a
+ * matrix, key x value,
+ *   a_s[h]      = exp(min(G_s[h] + decay[h], 0))
+ *   S_s[h]      = a_s[h] * S_{s-1}[h] + K_s[g] V_s[h]^T
+ *   Y_s[h]      = scale * Q_s[g]^T S_s[h]
+ * for head h in group g = h / (heads / groups).  G + decay is a step's log
+ * decay: above 0 it acts as 0 (and has no gradient there), at -infinity a step
+ * forgets all before it.  Rows, steps, lengths and carried states are those of
+ * the operators above; S_{-1} is initial_state. */
+typedef struct {
+  int32_t dtype;      /* rnn_dtype of Q, K, V, Y and their gradients (G, the states and the rest are f32) */
+  int32_t direction;  /* RNN_DIR_FORWARD or RNN_DIR_REVERSE */
+  int32_t layout;     /* 0 or 1 */
+  float scale;        /* finite */
+  int64_t seq;        /* S >= 0 */
+  int64_t batch;      /* B >= 0 */
+  int64_t heads;      /* H >= 1 */
+  int64_t groups;     /* G >= 1, a divisor of heads: those of a group share Q and K */
+  int64_t key;        /* 1 to 256 (above: RNN_ERR_UNSUPPORTED) */
+  int64_t value;      /* 1 to 256 (above: RNN_ERR_UNSUPPORTED) */
+} rnn_attn_desc;
+
+typedef struct rnn_attn rnn_attn;
+
+typedef struct {
+  rnn_rows Q;                /* [groups * key] a row               required */
+  rnn_rows K;                /* [groups * key] a row               required */
+  rnn_rows V;                /* [heads * value] a row              required */
+  rnn_rows G;                /* [heads] a row, f32                 optional (zeros) */
+  rnn_tensor decay;          /* [heads] f32                        optional (zeros) */
+  rnn_tensor sequence_lens;  /* [batch] int32                      optional (all seq) */
+  rnn_tensor initial_state;  /* [batch, heads, key, value] f32     optional (zeros) */
+  rnn_rows Y;                /* [heads * value] a row              optional output (forward only) */
+  rnn_tensor final_state;    /* as initial_state                   optional output (forward only) */
+} rnn_attn_operands;
+
+/* Gradients; states are computed again from the inputs.  dG and d_decay may be
+ * asked for without G and decay. */
+typedef struct {
+  rnn_rows dY;                 /* [heads * value] a row            required */
+  rnn_tensor d_final_state;    /* as initial_state                 optional (zeros) */
+  rnn_rows dQ;                 /* [groups * key] a row             optional outputs from here on */
+  rnn_rows dK;                 /* [groups * key] a row */
+  rnn_rows dV;                 /* [heads * value] a row */
+  rnn_rows dG;                 /* [heads] a row, f32 */
+  rnn_tensor d_decay;          /* [heads] f32 */
+  rnn_tensor d_initial_state;  /* as initial_state; must not be d_final_state */
+} rnn_attn_gradients;
+
+int rnn_attn_create(const rnn_attn_desc* desc, rnn_attn** out);
+void rnn_attn_destroy(rnn_attn* attn);
+/* Scratch of rnn_attn_encode and of rnn_attn_encode_backward (either may be
+ * 0); 256-byte aligned device memory. */
+int rnn_attn_scratch_size(const rnn_attn* attn, size_t* forward_bytes, size_t* backward_bytes);
+int rnn_attn_encode(const rnn_attn* attn, const rnn_attn_operands* operands, void* scratch, void* stream);
+int rnn_attn_encode_backward(const rnn_attn* attn, const rnn_attn_operands* operands,
+                             const rnn_attn_gradients* gradients, void* scratch, void* stream);
+
 /* Message of the last failed call on this thread ("" if none): the cell
  * (LSTM, GRU or RNN) or operator (conv, scan or layer norm) and the argument at fault, as the page's shape
  * exception names them ("Scratch").  The string is owned by the library and

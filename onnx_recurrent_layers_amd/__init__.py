@@ -125,6 +125,24 @@ class rnn_norm_gradients(ctypes.Structure):
     _fields_ = [("dY", rnn_rows), ("dX", rnn_rows), ("dScale", rnn_tensor), ("dB", rnn_tensor)]
 
 
+class rnn_attn_desc(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("direction", ctypes.c_int32), ("layout", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("seq", ctypes.c_int64), ("batch", ctypes.c_int64),
+                ("heads", ctypes.c_int64), ("groups", ctypes.c_int64), ("key", ctypes.c_int64),
+                ("value", ctypes.c_int64)]
+
+
+class rnn_attn_operands(ctypes.Structure):
+    _fields_ = [("Q", rnn_rows), ("K", rnn_rows), ("V", rnn_rows), ("G", rnn_rows), ("decay", rnn_tensor),
+                ("sequence_lens", rnn_tensor), ("initial_state", rnn_tensor), ("Y", rnn_rows),
+                ("final_state", rnn_tensor)]
+
+
+class rnn_attn_gradients(ctypes.Structure):
+    _fields_ = [("dY", rnn_rows), ("d_final_state", rnn_tensor), ("dQ", rnn_rows), ("dK", rnn_rows), ("dV", rnn_rows),
+                ("dG", rnn_rows), ("d_decay", rnn_tensor), ("d_initial_state", rnn_tensor)]
+
+
 # rnn_products: which arithmetic units carry a stage's products
 PRODUCTS = {0: "f32 vector ALU", 1: "f32 matrix cores", 2: "f16 matrix cores", 3: "bf16x3 matrix cores"}
 
@@ -168,7 +186,8 @@ def load_library(path: str = LIB_PATH):
     lib.rnn_read_run_status.restype = ctypes.c_int
     for op, desc, operands, gradients in (("conv", rnn_conv_desc, rnn_conv_operands, rnn_conv_gradients),
                                           ("scan", rnn_scan_desc, rnn_scan_operands, rnn_scan_gradients),
-                                          ("norm", rnn_norm_desc, rnn_norm_operands, rnn_norm_gradients)):
+                                          ("norm", rnn_norm_desc, rnn_norm_operands, rnn_norm_gradients),
+                                          ("attn", rnn_attn_desc, rnn_attn_operands, rnn_attn_gradients)):
         def declare(name, restype, *argtypes):
             f = getattr(lib, f"rnn_{op}_{name}")
             f.argtypes, f.restype = list(argtypes), restype
@@ -363,7 +382,7 @@ class Layer:
             pass
 
 
-# ---- the operators of a state space block, and layer normalization
+# ---- the operators of state space and linear attention blocks, and layer normalization
 
 def _create(name: str, desc) -> ctypes.c_void_p:
     h = ctypes.c_void_p()
@@ -440,6 +459,28 @@ def rnn_norm_encode(handle, operands: rnn_norm_operands, scratch_ptr: int = 0, s
 def rnn_norm_encode_backward(handle, operands: rnn_norm_operands, gradients: rnn_norm_gradients, scratch_ptr: int = 0,
                              stream_ptr: int = 0) -> None:
     _check(load_library().rnn_norm_encode_backward(handle, operands, gradients, scratch_ptr or None,
+                                                   stream_ptr or None))
+
+
+def rnn_attn_create(desc: rnn_attn_desc) -> ctypes.c_void_p:
+    return _create("rnn_attn_create", desc)
+
+
+def rnn_attn_destroy(handle) -> None:
+    load_library().rnn_attn_destroy(handle)
+
+
+def rnn_attn_scratch_size(handle):
+    return _scratch("rnn_attn_scratch_size", handle)
+
+
+def rnn_attn_encode(handle, operands: rnn_attn_operands, scratch_ptr: int = 0, stream_ptr: int = 0) -> None:
+    _check(load_library().rnn_attn_encode(handle, operands, scratch_ptr or None, stream_ptr or None))
+
+
+def rnn_attn_encode_backward(handle, operands: rnn_attn_operands, gradients: rnn_attn_gradients, scratch_ptr: int = 0,
+                             stream_ptr: int = 0) -> None:
+    _check(load_library().rnn_attn_encode_backward(handle, operands, gradients, scratch_ptr or None,
                                                    stream_ptr or None))
 
 
@@ -680,6 +721,39 @@ class LayerNorm(_Operator):
             col, grad = ((size,), dt, False), ((size,), torch.float32, False)
             return {"X": row, "Scale": col, "B": col, "Y": row, "Mean": stat, "InvStdDev": stat, "dY": row, "dX": row,
                     "dScale": grad, "dB": grad}
+
+        self._open(desc, device, shapes)
+
+
+class LinearAttention(_Operator):
+    """Linear attention with a decay for each head (``rnn_attn_*``): the
+    recurrence whose state is a matrix, key x value, a head, for prompts and
+    (``seq = 1``, state carried) single tokens, and its gradient.  Rows hold the
+    heads one after another; ``groups`` (default: ``heads``) divides them into
+    groups that share Q and K.  G, decay, the states and their gradients are
+    f32."""
+
+    op, who = "attn", "linear attention"
+    _operands, _gradients = rnn_attn_operands, rnn_attn_gradients
+    operand_names = tuple(n for n, _ in rnn_attn_operands._fields_)
+    input_names = operand_names[:-2]
+    gradient_names = tuple(n for n, _ in rnn_attn_gradients._fields_)
+
+    def __init__(self, dtype: str, seq: int, batch: int, heads: int, key: int, value: int, groups: Optional[int] = None,
+                 scale: float = 1.0, direction: str = "forward", layout: int = 1, device: str = "cuda"):
+        self.dtype = dtype
+        groups = heads if groups is None else groups
+        desc = rnn_attn_desc(DTYPES[dtype], DIRECTIONS[direction], int(layout), float(scale), int(seq), int(batch),
+                             int(heads), int(groups), int(key), int(value))
+
+        def shapes(torch, dt):
+            lead = (seq, batch) if layout == 0 else (batch, seq)
+            f32 = torch.float32
+            k, v, g = (lead + (groups * key,), dt, True), (lead + (heads * value,), dt, True), (lead + (heads,), f32, True)
+            head, state = ((heads,), f32, False), ((batch, heads, key, value), f32, False)
+            return {"Q": k, "K": k, "V": v, "G": g, "decay": head, "sequence_lens": ((batch,), torch.int32, False),
+                    "initial_state": state, "Y": v, "final_state": state, "dY": v, "d_final_state": state, "dQ": k,
+                    "dK": k, "dV": v, "dG": g, "d_decay": head, "d_initial_state": state}
 
         self._open(desc, device, shapes)
 

@@ -1,0 +1,218 @@
+// attn_api.cpp -- the C ABI of linear attention: validation, scratch sizing,
+// the walks of a call.  Every check runs in 64-bit checked arithmetic before
+// anything is enqueued; messages name operator and argument.
+#include <cmath>
+#include <new>
+
+#include "seq_check.h"
+
+using namespace rnnhip;
+
+struct rnn_attn {
+  rnn_attn_desc d;
+  int es;
+  int per;                // heads of a group
+  int key_cols, value_cols;   // workgroups along a head's keys and values
+  size_t backward_bytes;
+};
+
+namespace {
+
+const char kAttn[] = "linear attention";
+
+// The scratch regions of the gradient, in the order that they are taken.
+struct AttnScratch {
+  size_t rows, cols, ends, decay, part;
+};
+bool attn_scratch(const rnn_attn& p, AttnScratch* at, size_t* total) {
+  const rnn_attn_desc& d = p.d;
+  Regions r;
+  at->rows = r.take({p.key_cols, d.batch, d.heads, d.seq, 4});
+  at->cols = r.take({p.key_cols, d.batch, d.heads, d.seq, 4});
+  at->ends = r.take({p.key_cols, d.batch, d.heads, 4});
+  at->decay = r.take({d.batch, d.heads, 4});
+  at->part = p.per > 1 ? r.take({d.seq, d.batch, d.heads, d.key, 4}) : r.off;
+  *total = r.off;
+  return r.ok;
+}
+
+HeadRows head_rows(const Rows& r, int per) { return HeadRows{r.p, r.rs, per}; }
+
+// The operands both directions read.
+struct AttnInputs {
+  HeadRows Q, K, V;
+  const float* init;
+};
+AttnInputs attn_inputs(const rnn_attn& p, const rnn_attn_operands& o, Tensors& t, AttnArgs& a) {
+  const rnn_attn_desc& d = p.d;
+  const int64_t rows = d.seq * d.batch, gk = d.groups * d.key, hv = d.heads * d.value;
+  const bool any = rows > 0;
+  AttnInputs in{};
+  in.Q = head_rows(t.rows(o.Q, p.es, gk, rows, "Q", any), p.per);
+  in.K = head_rows(t.rows(o.K, p.es, gk, rows, "K", any), p.per);
+  in.V = head_rows(t.rows(o.V, p.es, hv, rows, "V", any), 1);
+  a.G = t.rows(o.G, 4, d.heads, rows, "G", false);
+  a.decay = reinterpret_cast<const float*>(t.tensor(o.decay, 4, "decay", false));
+  a.geo = geometry(d.seq, d.batch, d.layout, d.direction, t.tensor(o.sequence_lens, 4, "sequence_lens", false));
+  in.init = reinterpret_cast<const float*>(t.tensor(o.initial_state, 4, kInitial, false));
+  a.H = int(d.heads);
+  return in;
+}
+
+int attn_launch(const char* what, hipError_t e) {
+  return e == hipSuccess ? RNN_OK : fail(RNN_ERR_HIP, kAttn, "%s launch: %s", what, hipGetErrorString(e));
+}
+
+}  // namespace
+
+extern "C" int rnn_attn_create(const rnn_attn_desc* desc, rnn_attn** out) {
+  set_error_of(RNN_OK, nullptr, nullptr);
+  if (out) *out = nullptr;
+  if (!desc) return fail(RNN_ERR_ARG, kAttn, "desc: NULL");
+  if (!out) return fail(RNN_ERR_ARG, kAttn, "out: NULL");
+  const rnn_attn_desc& d = *desc;
+  if (int rc = check_seq(kAttn, d.dtype, d.direction, d.layout, d.seq, d.batch, d.heads, "heads")) return rc;
+  if (!std::isfinite(d.scale)) return fail(RNN_ERR_ARG, kAttn, "scale: must be finite");
+  if (d.groups < 1 || d.groups > d.heads || d.heads % d.groups)
+    return fail(RNN_ERR_SHAPE, kAttn, "groups: must divide heads (%lld of %lld)", (long long)d.groups, (long long)d.heads);
+  if (d.key < 1) return fail(RNN_ERR_SHAPE, kAttn, "key: must be at least 1 (%lld)", (long long)d.key);
+  if (d.value < 1) return fail(RNN_ERR_SHAPE, kAttn, "value: must be at least 1 (%lld)", (long long)d.value);
+  if (d.key > kAttnMaxSize) return fail(RNN_ERR_UNSUPPORTED, kAttn, "key: above %d", kAttnMaxSize);
+  if (d.value > kAttnMaxSize) return fail(RNN_ERR_UNSUPPORTED, kAttn, "value: above %d", kAttnMaxSize);
+  rnn_attn p{};
+  p.d = d;
+  p.es = elem_size(d.dtype);
+  p.per = int(d.heads / d.groups);
+  p.key_cols = int(ceil_div(d.key, kAttnCols));
+  p.value_cols = int(ceil_div(d.value, kAttnCols));
+  if (bytes_of({d.seq, d.batch, d.heads, d.key, p.es}) < 0) return fail(RNN_ERR_SHAPE, kAttn, "Q: size overflows");
+  if (bytes_of({d.seq, d.batch, d.heads, d.value, p.es}) < 0) return fail(RNN_ERR_SHAPE, kAttn, "V: size overflows");
+  if (bytes_of({d.batch, d.heads, d.key, d.value, 4}) < 0) return fail(RNN_ERR_SHAPE, kAttn, "initial_state: size overflows");
+  if (bytes_of({d.batch, d.heads, std::max(p.key_cols, p.value_cols), 256}) > kMaxThreads)
+    return fail(RNN_ERR_UNSUPPORTED, kAttn, "batch x heads: too large for one launch");
+  AttnScratch at;
+  if (!attn_scratch(p, &at, &p.backward_bytes)) return fail(RNN_ERR_SHAPE, kAttn, "scratch: size overflows");
+  rnn_attn* q = new (std::nothrow) rnn_attn(p);
+  if (!q) return fail(RNN_ERR_ARG, kAttn, "out of host memory");
+  *out = q;
+  return RNN_OK;
+}
+
+extern "C" void rnn_attn_destroy(rnn_attn* attn) { delete attn; }
+
+extern "C" int rnn_attn_scratch_size(const rnn_attn* attn, size_t* forward_bytes, size_t* backward_bytes) {
+  set_error_of(RNN_OK, nullptr, nullptr);
+  if (!attn) return fail(RNN_ERR_ARG, kAttn, "attn: NULL");
+  if (forward_bytes) *forward_bytes = 0;
+  if (backward_bytes) *backward_bytes = attn->backward_bytes;
+  return RNN_OK;
+}
+
+extern "C" int rnn_attn_encode(const rnn_attn* attn, const rnn_attn_operands* operands, void* scratch, void* stream) {
+  (void)scratch;
+  set_error_of(RNN_OK, nullptr, nullptr);
+  if (!attn) return fail(RNN_ERR_ARG, kAttn, "attn: NULL");
+  if (!operands) return fail(RNN_ERR_ARG, kAttn, "operands: NULL");
+  const rnn_attn& p = *attn;
+  const rnn_attn_desc& d = p.d;
+  Tensors t(kAttn);
+  AttnArgs a{};
+  const AttnInputs in = attn_inputs(p, *operands, t, a);
+  a.a = in.Q, a.b = in.K, a.v = in.V;
+  a.init = in.init;
+  a.out = head_rows(t.rows(operands->Y, p.es, d.heads * d.value, d.seq * d.batch, "Y", false, true), 1);
+  a.fin = reinterpret_cast<float*>(t.tensor(operands->final_state, 4, kFinal, false, true));
+  t.apart({{kInitial, kFinal}});
+  if (t.status != RNN_OK) return t.status;
+  if (d.batch == 0 || (!a.out.p && !a.fin)) return RNN_OK;
+  a.K = int(d.key), a.V = int(d.value);
+  a.sk = int(d.value), a.sv = 1;
+  a.in_scale = 1.f, a.out_scale = d.scale;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  OnDevice on(s);
+  return attn_launch("forward", launch_attn_steps(a, d.dtype, s));
+}
+
+extern "C" int rnn_attn_encode_backward(const rnn_attn* attn, const rnn_attn_operands* operands,
+                                        const rnn_attn_gradients* gradients, void* scratch, void* stream) {
+  set_error_of(RNN_OK, nullptr, nullptr);
+  if (!attn) return fail(RNN_ERR_ARG, kAttn, "attn: NULL");
+  if (!operands) return fail(RNN_ERR_ARG, kAttn, "operands: NULL");
+  if (!gradients) return fail(RNN_ERR_ARG, kAttn, "gradients: NULL");
+  const rnn_attn& p = *attn;
+  const rnn_attn_desc& d = p.d;
+  const rnn_attn_gradients& g = *gradients;
+  const int64_t rows = d.seq * d.batch, gk = d.groups * d.key, hv = d.heads * d.value;
+  Tensors t(kAttn);
+  AttnArgs a{};
+  const AttnInputs in = attn_inputs(p, *operands, t, a);
+  const HeadRows dY = head_rows(t.rows(g.dY, p.es, hv, rows, "dY", rows > 0), 1);
+  const float* dfin = reinterpret_cast<const float*>(t.tensor(g.d_final_state, 4, "d_final_state", false));
+  const Rows dQ = t.rows(g.dQ, p.es, gk, rows, "dQ", false, true);
+  const Rows dK = t.rows(g.dK, p.es, gk, rows, "dK", false, true);
+  const Rows dV = t.rows(g.dV, p.es, hv, rows, "dV", false, true);
+  const Rows dG = t.rows(g.dG, 4, d.heads, rows, "dG", false, true);
+  float* ddecay = reinterpret_cast<float*>(t.tensor(g.d_decay, 4, "d_decay", false, true));
+  float* dinit = reinterpret_cast<float*>(t.tensor(g.d_initial_state, 4, "d_initial_state", false, true));
+  t.apart();
+  if (t.status != RNN_OK) return t.status;
+  const bool decays = dG.p || ddecay;
+  if (!dQ.p && !dK.p && !dV.p && !decays && !dinit) return RNN_OK;
+  if (int rc = check_scratch(kAttn, scratch, p.backward_bytes)) return rc;
+  AttnScratch at;
+  size_t total;
+  attn_scratch(p, &at, &total);
+  auto f = [&](size_t off) { return reinterpret_cast<float*>(static_cast<char*>(scratch) + off); };
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  OnDevice on(s);
+
+  // dQ and dK: of each head by itself, summed over a group's heads
+  auto shared = [&](const char* what, AttnArgs w, const Rows& out, const HeadRows& dot, float* dots) -> int {
+    w.K = int(d.value), w.V = int(d.key);
+    w.sk = 1, w.sv = int(d.value);
+    const bool sum = p.per > 1 && out.p;
+    w.out = sum ? HeadRows{reinterpret_cast<char*>(f(at.part)), d.heads * d.key, 1} : head_rows(out, 1);
+    w.out_f32 = sum;
+    w.dot = dot;
+    w.dots = decays ? dots : nullptr;
+    if (int rc = attn_launch(what, launch_attn_steps(w, d.dtype, s))) return rc;
+    if (!sum) return RNN_OK;
+    const HeadSumArgs hs{f(at.part), rows, int(d.heads), p.per, int(d.key), out};
+    return attn_launch("sum", launch_head_sum(hs, d.dtype, s));
+  };
+  if (dQ.p || decays) {
+    AttnArgs w = a;
+    w.a = dY, w.b = in.V, w.v = in.K;
+    w.init = in.init;
+    w.in_scale = 1.f, w.out_scale = d.scale;
+    if (decays && dfin) {
+      w.other = dfin;
+      w.ends = f(at.ends);
+    }
+    if (int rc = shared("dQ", w, dQ, in.Q, f(at.rows))) return rc;
+  }
+  a.back = 1;
+  a.in_scale = d.scale, a.out_scale = 1.f;
+  a.init = dfin;
+  if (dK.p || decays) {
+    AttnArgs w = a;
+    w.a = in.V, w.b = dY, w.v = in.Q;
+    if (int rc = shared("dK", w, dK, in.K, f(at.cols))) return rc;
+  }
+  if (dV.p || dinit) {
+    AttnArgs w = a;
+    w.a = in.K, w.b = in.Q, w.v = dY;
+    w.K = int(d.key), w.V = int(d.value);
+    w.sk = int(d.value), w.sv = 1;
+    w.out = head_rows(dV, 1);
+    w.fin = dinit;
+    if (int rc = attn_launch("dV", launch_attn_steps(w, d.dtype, s))) return rc;
+  }
+  if (!decays) return RNN_OK;
+  const AttnDecayArgs da{a.geo, a.H, p.key_cols, p.key_cols, f(at.rows), f(at.cols), dfin ? f(at.ends) : nullptr, a.G, a.decay, dG,
+                         ddecay ? f(at.decay) : nullptr};
+  if (int rc = attn_launch("decay", launch_attn_decay(da, s))) return rc;
+  if (!ddecay) return RNN_OK;
+  const ColSumArgs cs{f(at.decay), int(d.batch), d.heads, ddecay, nullptr, int(d.heads), 1};
+  return attn_launch("sums", launch_colsum(cs, s));
+}

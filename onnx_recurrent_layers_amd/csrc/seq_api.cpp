@@ -4,12 +4,10 @@
 // arithmetic before anything is enqueued; messages name operator and argument.
 #include <algorithm>
 #include <cmath>
-#include <cstdarg>
-#include <cstdio>
 #include <cstdlib>
 #include <new>
 
-#include "seq_ops.h"
+#include "seq_check.h"
 
 using namespace rnnhip;
 
@@ -46,167 +44,7 @@ struct rnn_norm {
 
 namespace {
 
-constexpr int64_t kMaxBytes = int64_t(1) << 52;
-constexpr int64_t kMaxThreads = (int64_t(1) << 32) - 1;   // of one launch
-
-int fail(int code, const char* who, const char* fmt, ...) {
-  char buf[512];
-  va_list ap;
-  va_start(ap, fmt);
-  vsnprintf(buf, sizeof buf, fmt, ap);
-  va_end(ap);
-  return set_error_of(code, who, buf);
-}
-
-// a*b*c*... in bytes, or -1 when it overflows the largest tensor accepted.
-int64_t bytes_of(std::initializer_list<int64_t> f) {
-  int64_t n = 1;
-  for (int64_t x : f) {
-    if (x < 0) return -1;
-    if (x == 0) return 0;
-  }
-  for (int64_t x : f) {
-    if (n > kMaxBytes / x) return -1;
-    n *= x;
-  }
-  return n;
-}
-
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-int elem_size(int dtype) { return dtype == RNN_DTYPE_F32 ? 4 : 2; }
-
-// Scratch regions, 256-byte aligned.
-struct Regions {
-  size_t off = 0;
-  bool ok = true;
-  size_t take(std::initializer_list<int64_t> f) {
-    const int64_t n = bytes_of(f);
-    const size_t at = off;
-    if (n < 0 || off > size_t(kMaxBytes)) ok = false;
-    else off = (off + size_t(n) + 255) & ~size_t(255);
-    return at;
-  }
-};
-
-// The stream's device for the time of a call.
-class OnDevice {
- public:
-  explicit OnDevice(hipStream_t s) {
-    if (!s || s == hipStreamPerThread) return;
-    hipDevice_t d = 0;
-    int cur = 0;
-    if (hipStreamGetDevice(s, &d) != hipSuccess || hipGetDevice(&cur) != hipSuccess || cur == int(d)) return;
-    if (hipSetDevice(int(d)) == hipSuccess) back_ = cur;
-  }
-  ~OnDevice() {
-    if (back_ >= 0) (void)hipSetDevice(back_);
-  }
-
- private:
-  int back_ = -1;
-};
-
-// The tensors of one call: resolved one by one, the first failure kept.
-class Tensors {
- public:
-  explicit Tensors(const char* who) : who_(who) {}
-  int status = RNN_OK;
-
-  char* tensor(const rnn_tensor& t, int es, const char* name, bool required, bool output = false) {
-    return resolve(t.ptr, t.elem_offset, es, name, required, output);
-  }
-  Rows rows(const rnn_rows& t, int es, int64_t length, int64_t count, const char* name, bool required, bool output = false) {
-    Rows r{nullptr, length};
-    if (status != RNN_OK) return r;
-    if (t.ptr) {
-      if (t.row_stride != 0 && t.row_stride < length) {
-        status = fail(RNN_ERR_SHAPE, who_, "%s: row_stride %lld below the row's length %lld", name, (long long)t.row_stride,
-                      (long long)length);
-        return r;
-      }
-      if (t.row_stride) r.rs = t.row_stride;
-      if (bytes_of({std::max<int64_t>(count, 1), r.rs, es}) < 0) {
-        status = fail(RNN_ERR_SHAPE, who_, "%s: size overflows", name);
-        return r;
-      }
-    }
-    r.p = resolve(t.ptr, t.elem_offset, es, name, required, output);
-    return r;
-  }
-  // An output may share its first element with no other tensor of the call;
-  // `pair` names the two that may be one buffer.
-  void apart(const char* pair_a = nullptr, const char* pair_b = nullptr) {
-    for (int i = 0; i < n_ && status == RNN_OK; ++i)
-      for (int j = 0; j < i && status == RNN_OK; ++j)
-        if (seen_[i].p == seen_[j].p && (seen_[i].output || seen_[j].output) &&
-            !(seen_[i].name == pair_b && seen_[j].name == pair_a))
-          status = fail(RNN_ERR_ARG, who_, "%s: the same memory as %s", seen_[i].name, seen_[j].name);
-  }
-
- private:
-  struct Seen {
-    const char* p;
-    const char* name;
-    bool output;
-  };
-  const char* who_;
-  Seen seen_[32];
-  int n_ = 0;
-
-  char* resolve(void* ptr, int64_t offset, int es, const char* name, bool required, bool output) {
-    if (status != RNN_OK) return nullptr;
-    if (!ptr) {
-      if (required) status = fail(RNN_ERR_ARG, who_, "%s: NULL", name);
-      return nullptr;
-    }
-    if (offset < 0) {
-      status = fail(RNN_ERR_ARG, who_, "%s: negative element offset", name);
-      return nullptr;
-    }
-    if (offset > kMaxBytes / es) {
-      status = fail(RNN_ERR_SHAPE, who_, "%s: element offset overflows", name);
-      return nullptr;
-    }
-    char* p = static_cast<char*>(ptr) + offset * es;
-    if (reinterpret_cast<uintptr_t>(p) % uintptr_t(es)) {
-      status = fail(RNN_ERR_ARG, who_, "%s: address not aligned to its %d-byte element", name, es);
-      return nullptr;
-    }
-    if (n_ < 32) seen_[n_++] = Seen{p, name, output};
-    return p;
-  }
-};
-
-bool aligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
-bool aligned(const Rows& r, size_t n, int es) { return aligned(r.p, n) && (size_t(r.rs) * size_t(es)) % n == 0; }
-
-int check_scratch(const char* who, void* scratch, size_t need) {
-  if (!need) return RNN_OK;
-  if (!scratch) return fail(RNN_ERR_ARG, who, "scratch: NULL (needs %zu bytes)", need);
-  if (!aligned(scratch, 256)) return fail(RNN_ERR_ARG, who, "scratch: not 256-byte aligned");
-  return RNN_OK;
-}
-
-int check_seq(const char* who, int dtype, int direction, int layout, int64_t seq, int64_t batch, int64_t channels) {
-  if (dtype < RNN_DTYPE_F32 || dtype > RNN_DTYPE_BF16) return fail(RNN_ERR_ARG, who, "dtype: unknown value %d", dtype);
-  if (direction == RNN_DIR_BIDIRECTIONAL)
-    return fail(RNN_ERR_ARG, who, "direction: forward or reverse (two problems for both)");
-  if (direction != RNN_DIR_FORWARD && direction != RNN_DIR_REVERSE)
-    return fail(RNN_ERR_ARG, who, "direction: unknown value %d", direction);
-  if (layout != 0 && layout != 1) return fail(RNN_ERR_ARG, who, "layout: must be 0 or 1, got %d", layout);
-  if (seq < 0) return fail(RNN_ERR_SHAPE, who, "seq: negative (%lld)", (long long)seq);
-  if (batch < 0) return fail(RNN_ERR_SHAPE, who, "batch: negative (%lld)", (long long)batch);
-  if (channels < 1) return fail(RNN_ERR_SHAPE, who, "channels: must be at least 1 (%lld)", (long long)channels);
-  if (channels > (int64_t(1) << 24)) return fail(RNN_ERR_UNSUPPORTED, who, "channels: above 16777216");
-  if (batch > (int64_t(1) << 30)) return fail(RNN_ERR_UNSUPPORTED, who, "batch: above 2^30");
-  if (seq > (int64_t(1) << 30)) return fail(RNN_ERR_UNSUPPORTED, who, "seq: above 2^30");
-  return RNN_OK;
-}
-
 const char kConv[] = "conv", kScan[] = "scan", kNorm[] = "layer norm";
-
-// Names that may be one buffer (compared by address).
-const char kInitial[] = "initial_state", kFinal[] = "final_state";
 
 }  // namespace
 
@@ -303,16 +141,6 @@ extern "C" int rnn_conv_scratch_size(const rnn_conv* conv, size_t* forward_bytes
 
 namespace {
 
-SeqGeom geometry(int64_t seq, int64_t batch, int layout, int direction, const char* lens) {
-  SeqGeom g;
-  g.S = int(seq);
-  g.B = int(batch);
-  g.layout = layout;
-  g.reverse = direction == RNN_DIR_REVERSE;
-  g.lens = reinterpret_cast<const int32_t*>(lens);
-  return g;
-}
-
 // The operands both directions read.
 void conv_inputs(const rnn_conv& c, const rnn_conv_operands& o, Tensors& t, ConvArgs& a) {
   const rnn_conv_desc& d = c.d;
@@ -341,7 +169,7 @@ extern "C" int rnn_conv_encode(const rnn_conv* conv, const rnn_conv_operands* op
   conv_inputs(c, *operands, t, a);
   a.Y = t.rows(operands->Y, c.es, d.channels, d.seq * d.batch, "Y", false, true);
   a.fin = t.tensor(operands->final_state, c.es, kFinal, false, true);
-  t.apart(kInitial, kFinal);
+  t.apart({{kInitial, kFinal}});
   if (t.status != RNN_OK) return t.status;
   if (d.batch == 0 || (!a.Y.p && !a.fin)) return RNN_OK;
   const int v = 16 / c.es;
@@ -590,7 +418,7 @@ extern "C" int rnn_scan_encode(const rnn_scan* scan, const rnn_scan_operands* op
   scan_inputs(p, *operands, t, a);
   a.Y = t.rows(operands->Y, p.es, d.channels, d.seq * d.batch, "Y", false, true);
   a.fin = reinterpret_cast<float*>(t.tensor(operands->final_state, 4, kFinal, false, true));
-  t.apart(kInitial, kFinal);
+  t.apart({{kInitial, kFinal}});
   if (t.status != RNN_OK) return t.status;
   if (d.batch == 0 || (!a.Y.p && !a.fin)) return RNN_OK;
   if (int rc = check_scratch(kScan, scratch, p.forward_bytes)) return rc;

@@ -1,0 +1,276 @@
+"""Linear attention on the GPU against its 64-bit plain form, at the sizes,
+masks, strides and types where it can go wrong; states carried, in place and
+from token to token; graphs and streams.  Bounds: attn_reference.walk."""
+import itertools
+
+import pytest
+import torch
+
+import onnx_recurrent_layers_amd as rl
+from tests import attn_reference as att
+from tests import ssm_reference as ref
+from tests.gpu_harness import note
+from tests.test_gpu_ssm import SENTINEL, Bufs, lead, rounded
+
+pytestmark = pytest.mark.gpu
+
+# 16-bit tensors: products of a value of 32 bits by a stored one take the first in two halves (2^-16 of a bf16
+# pair; a factor two for sums of such), three for the decays' gradient
+SPLIT = {"f32": 0.0, "f16": 2.0 ** -15, "bf16": 2.0 ** -15}
+FORWARD, BACKWARD = ("Y", "final_state"), ("dQ", "dK", "dV", "dG", "d_decay", "d_initial_state")
+ROWS = {"Y", "dQ", "dK", "dV", "dG"}
+
+
+def values(dtype, b, s, h, groups, k, v, seed=0, gate=0.05, fixed=0.02, carried=True):
+    gen = torch.Generator().manual_seed(seed)
+    t = {n: torch.randn(*w, generator=gen, dtype=torch.float64) for n, w in dict(
+        Q=(b, s, groups * k), K=(b, s, groups * k), V=(b, s, h * v), G=(b, s, h), decay=(h,), initial_state=(b, h, k, v),
+        dY=(b, s, h * v), d_final_state=(b, h, k, v)).items()}
+    t["G"], t["decay"] = -gate * t["G"].square(), -fixed * t["decay"].abs()
+    t = {n: rounded(x, dtype if n in ("Q", "K", "V", "dY") else "f32") for n, x in t.items()}
+    for n, on in (("G", gate), ("decay", fixed), ("initial_state", carried), ("d_final_state", carried)):
+        if not on:
+            del t[n]
+    return t
+
+
+def types(dtype):
+    f32 = torch.float32
+    return {n: f32 for n in ("G", "decay", "initial_state", "d_final_state", "final_state", "dG", "d_decay", "d_initial_state")} | {
+        n: ref.TYPES[dtype] for n in ("Q", "K", "V", "dY", "Y", "dQ", "dK", "dV")}
+
+
+def reference(t, dtype, h, groups, scale, lens, reverse, back, device="cpu"):
+    d = {n: x.to(device) for n, x in t.items()}
+    return att.attn(d["Q"], d["K"], d["V"], h, groups, d.get("G"), d.get("decay"), scale, lens, d.get("initial_state"), reverse,
+                    d["dY"] if back else None, d.get("d_final_state") if back else None, SPLIT[dtype])
+
+
+def fill(m, t, dtype, layout, names, lens, dead):
+    to = types(dtype)
+    for n in names:
+        if n not in t:
+            continue
+        x = t[n]
+        if n in ("Q", "K", "V", "G", "dY"):
+            x = x.clone()
+            for i, live in enumerate(ref.lengths(lens, *x.shape[:2])):   # what is past a row's length is not read
+                x[i, live:] = dead
+            m.rows(n, lead(x, layout), to[n])
+        else:
+            m.plain(n, x, to[n])
+    if lens is not None:
+        m.plain("sequence_lens", torch.tensor(lens), torch.int32)
+
+
+def attn_case(dtype, b, s, h, groups, k, v, layout=1, reverse=False, lens=None, pad=0, odd=0, seed=0, dead=float("nan"), back=True,
+              forward=True, scale=0.37, device="cpu", t=None, **kw):
+    note(f"attn {dtype} b{b} s{s} h{h}/{groups} k{k} v{v} layout {layout} reverse {reverse} lens {lens} pad {pad} odd {odd} {kw}")
+    t = values(dtype, b, s, h, groups, k, v, seed, **kw) if t is None else t
+    op = rl.LinearAttention(dtype=dtype, seq=s, batch=b, heads=h, groups=groups, key=k, value=v, scale=scale,
+                            direction="reverse" if reverse else "forward", layout=layout)
+    to = types(dtype)
+    shapes = {"Y": (b, s, h * v), "dV": (b, s, h * v), "dQ": (b, s, groups * k), "dK": (b, s, groups * k), "dG": (b, s, h), "d_decay": (h,),
+              "final_state": (b, h, k, v), "d_initial_state": (b, h, k, v)}
+    worst = {}
+    for on, call, ins, outs in ((forward, op.encode, ("Q", "K", "V", "G", "decay", "initial_state"), FORWARD),
+                                (back, op.backward, ("Q", "K", "V", "G", "decay", "initial_state", "dY", "d_final_state"), BACKWARD)):
+        if not on:
+            continue
+        m = Bufs(pad, odd)
+        fill(m, t, dtype, layout, ins, lens, dead)
+        for n in outs:
+            sh = shapes[n]
+            m.out(n, (sh[1], sh[0], sh[2]) if n in ROWS and layout == 0 else sh, to[n], row=n in ROWS)
+        call(m.t)
+        m.check()
+        want = reference(t, dtype, h, groups, scale, lens, reverse, outs is BACKWARD, device)
+        for n in outs:
+            got = lead(m.t[n], layout) if n in ROWS else m.t[n]
+            worst[n] = att.close(got, *want[n], dtype if to[n] != torch.float32 else "f32", n)
+    note("  worst " + " ".join(f"{n} {w:.2f}" for n, w in worst.items()))
+
+
+@pytest.mark.parametrize("dtype", ref.TYPES)
+@pytest.mark.parametrize("s", [1, 2, 3, 4, 5, 8, 17, 63, 64, 65, 130])
+def test_lengths(dtype, s):
+    attn_case(dtype, 2, s, 3, 3, 16, 16)
+    attn_case(dtype, 3, s, 4, 2, 32, 20, layout=0, reverse=True, lens=[s, 0, s // 2 + 1], seed=1)
+
+
+@pytest.mark.parametrize("dtype", ref.TYPES)
+@pytest.mark.parametrize("k,v", [(1, 1), (1, 70), (5, 3), (50, 42), (64, 64), (64, 128), (96, 33), (128, 128), (130, 16), (256, 64), (24, 256),
+                                 (256, 256)])
+def test_sizes(dtype, k, v):
+    attn_case(dtype, 2, 75, 2, 1, k, v, lens=[75, 66], device="cuda")
+    attn_case(dtype, 2, 3, 2, 2, k, v, seed=1)
+
+
+@pytest.mark.parametrize("dtype", ref.TYPES)
+@pytest.mark.parametrize("layout,reverse,pad,odd", [(0, False, 0, 0), (1, True, 8, 0), (0, True, 24, 4), (1, False, 3, 1), (1, True, 0, 5)])
+def test_strides_and_directions(dtype, layout, reverse, pad, odd):
+    for s, lens in ((2, [2, 1, 0]), (70, [70, 65, 3]), (200, [150, 200, 64])):
+        attn_case(dtype, 3, s, 4, 2, 40, 24, layout=layout, reverse=reverse, lens=lens, pad=pad, odd=odd, seed=s)
+
+
+@pytest.mark.parametrize("dtype", ref.TYPES)
+@pytest.mark.parametrize("gate,fixed,carried", itertools.product((0.05, 0.0), (0.02, 0.0), (True, False)))
+def test_optional_operands(dtype, gate, fixed, carried):
+    for s in (1, 100):
+        attn_case(dtype, 2, s, 2, 2, 32, 32, gate=gate, fixed=fixed, carried=carried, seed=s)
+
+
+@pytest.mark.parametrize("dtype", ref.TYPES)
+@pytest.mark.parametrize("s", [700, 1500])
+def test_long_rows(dtype, s):
+    attn_case(dtype, 1, s, 2, 2, 64, 64, gate=0.02, fixed=0.003, device="cuda")
+    attn_case(dtype, 2, s, 2, 1, 33, 64, gate=0.5, lens=[s - 1, s // 3], reverse=True, device="cuda", seed=2)
+    attn_case(dtype, 2, s, 1, 1, 48, 80, gate=0.0, fixed=0.0, lens=[s, s // 2], device="cuda", seed=3)
+
+
+@pytest.mark.parametrize("dtype", ref.TYPES)
+@pytest.mark.parametrize("gate", [3.0, 40.0, 400.0])
+def test_strong_decays(dtype, gate):
+    attn_case(dtype, 2, 150, 2, 2, 32, 32, gate=gate, lens=[150, 70])
+
+
+@pytest.mark.parametrize("dtype", ref.TYPES)
+@pytest.mark.parametrize("low", [-float("inf"), torch.finfo(torch.float32).min, -1e9])
+def test_a_step_that_forgets(dtype, low):
+    """A log decay of -infinity, or the type's lowest value: documents one after another in a row."""
+    b, s, h, k, v = 2, 140, 2, 32, 24
+    t = values(dtype, b, s, h, h, k, v, fixed=0.0)
+    for at in (0, 1, 50, 63, 64, 65, 139):
+        t["G"][:, at] = low
+    attn_case(dtype, b, s, h, h, k, v, t=t)
+    attn_case(dtype, b, s, h, h, k, v, t=t, reverse=True, lens=[140, 51])
+    t1 = {n: x[:, 50:53] if n in ("Q", "K", "V", "G", "dY") else x for n, x in t.items()}
+    attn_case(dtype, b, 3, h, h, k, v, t=t1)
+
+
+@pytest.mark.parametrize("dtype", ref.TYPES)
+def test_decays_above_one(dtype):
+    t = values(dtype, 2, 90, 2, 2, 16, 16)
+    t["G"][:, ::7] = 3.0
+    t["G"][:, 5] = float("inf")
+    attn_case(dtype, 2, 90, 2, 2, 16, 16, t=t)
+    attn_case(dtype, 2, 90, 2, 2, 16, 16, t=t, reverse=True)
+
+
+@pytest.mark.parametrize("dtype", ref.TYPES)
+def test_state_in_place_and_token_by_token(dtype):
+    b, s, h, k, v = 3, 70, 4, 64, 32
+    t = values(dtype, b, s, h, 2, k, v)
+    to = types(dtype)
+    d = {n: x.to(to[n]).cuda() for n, x in t.items()}
+    want = reference(t, dtype, h, 2, 1.0, None, False, False)
+    whole = rl.LinearAttention(dtype=dtype, seq=s, batch=b, heads=h, groups=2, key=k, value=v)
+    ins = {n: d[n] for n in ("Q", "K", "V", "G", "decay")}
+    state = d["initial_state"].clone()
+    y = torch.empty(b, s, h * v, dtype=to["Y"], device="cuda")
+    whole.encode({**ins, "initial_state": state, "final_state": state, "Y": y})
+    torch.cuda.synchronize()
+    att.close(y, *want["Y"], dtype, "Y")
+    att.close(state, *want["final_state"], "f32", "final_state")
+    token = rl.LinearAttention(dtype=dtype, seq=1, batch=b, heads=h, groups=2, key=k, value=v)
+    state, ys = d["initial_state"].clone(), []
+    for i in range(s):
+        y1 = torch.empty(b, 1, h * v, dtype=to["Y"], device="cuda")
+        one = {n: x[:, i:i + 1] if n != "decay" else x for n, x in ins.items()}
+        token.encode({**{n: x.contiguous() for n, x in one.items()}, "initial_state": state, "final_state": state, "Y": y1})
+        ys.append(y1)
+    torch.cuda.synchronize()
+    att.close(torch.cat(ys, 1), *want["Y"], dtype, "Y")
+    att.close(state, *want["final_state"], "f32", "final_state")
+
+
+@pytest.mark.parametrize("dtype", ref.TYPES)
+def test_chosen_outputs(dtype):
+    """Each output alone is bit for bit that of all together; the others are left alone."""
+    b, s, h, k, v = 2, 100, 4, 32, 48
+    t = values(dtype, b, s, h, 2, k, v)
+    to = types(dtype)
+    d = {n: x.to(to[n]).cuda() for n, x in t.items()}
+    op = rl.LinearAttention(dtype=dtype, seq=s, batch=b, heads=h, groups=2, key=k, value=v)
+    shapes = {"Y": (b, s, h * v), "dV": (b, s, h * v), "dQ": (b, s, 2 * k), "dK": (b, s, 2 * k), "dG": (b, s, h), "d_decay": (h,),
+              "final_state": (b, h, k, v), "d_initial_state": (b, h, k, v)}
+    for call, names, skip in ((op.encode, FORWARD, ("dY", "d_final_state")), (op.backward, BACKWARD, ())):
+        ins = {n: x for n, x in d.items() if n not in skip}
+        full = {n: torch.empty(shapes[n], dtype=to[n], device="cuda") for n in names}
+        call({**ins, **full})
+        for n in names:
+            one = torch.empty_like(full[n])
+            call({**ins, n: one})
+            torch.cuda.synchronize()
+            if n in ("dQ", "dK"):   # (with the decays' gradient the walk adds a step's own part last)
+                torch.testing.assert_close(one.double(), full[n].double(), rtol=2 * ref.EPS[dtype] + 1e-5, atol=1e-4)
+            else:
+                assert torch.equal(one, full[n]), n
+
+
+@pytest.mark.parametrize("dtype", ref.TYPES)
+def test_empty(dtype):
+    """No step: the state goes on as it is, the sums are zero."""
+    b, h, k, v = 2, 2, 8, 8
+    op = rl.LinearAttention(dtype=dtype, seq=0, batch=b, heads=h, key=k, value=v)
+    init, fin = torch.randn(b, h, k, v, device="cuda"), torch.empty(b, h, k, v, device="cuda")
+    empty = torch.empty(b, 0, h * k, dtype=ref.TYPES[dtype], device="cuda")
+    op.encode({"Q": empty, "K": empty, "V": empty, "initial_state": init, "final_state": fin})
+    dinit, dd = torch.empty_like(fin), torch.full((h,), SENTINEL, device="cuda")
+    op.backward({"Q": empty, "K": empty, "V": empty, "dY": empty, "initial_state": init, "d_final_state": init, "d_initial_state": dinit})
+    torch.cuda.synchronize()
+    assert torch.equal(fin, init) and torch.equal(dinit, init)
+    op.backward({"Q": empty, "K": empty, "V": empty, "dY": empty, "d_decay": dd})
+    torch.cuda.synchronize()
+    assert (dd == 0).all()
+    none = rl.LinearAttention(dtype=dtype, seq=3, batch=0, heads=h, key=k, value=v)
+    e = torch.empty(0, 3, h * k, dtype=ref.TYPES[dtype], device="cuda")
+    none.encode({"Q": e, "K": e, "V": e, "Y": torch.empty_like(e)})
+    none.backward({"Q": e, "K": e, "V": e, "dY": e, "dQ": torch.empty_like(e), "d_decay": dd.fill_(SENTINEL)})
+    torch.cuda.synchronize()
+    assert (dd == 0).all()
+
+
+@pytest.mark.parametrize("s", [1, 90])
+def test_graphs_and_streams(s):
+    """Captured, replayed on new inputs between eager calls, on a stream of its own."""
+    b, h, k, v = 2, 4, 64, 64
+    op = rl.LinearAttention(dtype="bf16", seq=s, batch=b, heads=h, groups=2, key=k, value=v)
+    to = types("bf16")
+
+    def new(seed):
+        return {n: x.to(to[n]).cuda() for n, x in values("bf16", b, s, h, 2, k, v, seed).items()}
+
+    held = new(0)
+    shapes = {"Y": (b, s, h * v), "dV": (b, s, h * v), "dQ": (b, s, 2 * k), "dK": (b, s, 2 * k), "dG": (b, s, h), "d_decay": (h,),
+              "final_state": (b, h, k, v), "d_initial_state": (b, h, k, v)}
+
+    def outs(names):
+        return {n: torch.full(shapes[n], SENTINEL, dtype=to[n], device="cuda") for n in names}
+
+    def calls(t, f, g, on=op):
+        on.encode({**{n: x for n, x in t.items() if n not in ("dY", "d_final_state")}, **f})
+        on.backward({**t, **g})
+
+    f, g = outs(FORWARD), outs(BACKWARD)
+    calls(held, f, g)
+    torch.cuda.synchronize()
+    stream = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(stream):
+        calls(held, f, g)
+        stream.synchronize()
+        with torch.cuda.graph(graph, stream=stream):
+            calls(held, f, g)
+    eager = rl.LinearAttention(dtype="bf16", seq=s, batch=b, heads=h, groups=2, key=k, value=v)
+    for seed in range(1, 5):
+        t = new(seed)
+        for n in held:
+            held[n].copy_(t[n])
+        graph.replay()
+        f2, g2 = outs(FORWARD), outs(BACKWARD)
+        calls(t, f2, g2, eager)
+        torch.cuda.synchronize()
+        for a, c in ((f, f2), (g, g2)):
+            for n in a:
+                assert torch.equal(a[n], c[n]), (seed, n)
