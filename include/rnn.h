@@ -57,9 +57,11 @@
  *
  * Beside the recurrent layers: the operators of a selective state space block
  * (rnn_conv_*: the short causal convolution; rnn_scan_*: the selective scan;
- * both for prompts and for single tokens) and layer normalization
- * (rnn_norm_*), each with its gradient.  Their section below says where their
- * conventions differ.
+ * both for prompts and for single tokens), of a linear attention block
+ * (rnn_attn_*: linear attention with a decay for each head, for prompts and for
+ * single tokens; rnn_rotary_*: norms of its queries and keys with the position
+ * rotation) and layer normalization (rnn_norm_*), each with its gradient.  Their
+ * section below says where their conventions differ.
  */
 #ifndef ONNX_RNN_MI355X_H
 #define ONNX_RNN_MI355X_H
@@ -86,8 +88,8 @@ typedef enum {
 } rnn_status;
 
 typedef enum { RNN_CELL_RNN = 0, RNN_CELL_GRU = 1, RNN_CELL_LSTM = 2 } rnn_cell;
-/* (BF16: the state space operators and layer normalization below; the
- * recurrent layers take F32 and F16.) */
+/* (BF16: the operators beside the recurrent layers, below; the recurrent layers
+ * take F32 and F16.) */
 typedef enum { RNN_DTYPE_F32 = 0, RNN_DTYPE_F16 = 1, RNN_DTYPE_BF16 = 2 } rnn_dtype;
 typedef enum { RNN_DIR_FORWARD = 0, RNN_DIR_REVERSE = 1, RNN_DIR_BIDIRECTIONAL = 2 } rnn_direction;
 
@@ -315,7 +317,8 @@ typedef struct {
 int rnn_read_run_status(const rnn_problem* problem, const void* state_scratch, void* stream, rnn_run_status* out);
 
 /* ---------------------------------------------------------------------------
- * Operators of a selective state space block, and layer normalization.
+ * Operators of selective state space and linear attention blocks, and layer
+ * normalization.
  *
  * Manner: as the recurrent layers -- a description is validated into an
  * immutable problem, scratch is the caller's, an encode call checks everything
@@ -561,8 +564,65 @@ int rnn_attn_encode(const rnn_attn* attn, const rnn_attn_operands* operands, voi
 int rnn_attn_encode_backward(const rnn_attn* attn, const rnn_attn_operands* operands,
                              const rnn_attn_gradients* gradients, void* scratch, void* stream);
 
+/* Norms of queries and keys for each head, with the position rotation in the
+ * same pass (what linear attention's Q and K go through):
+ *   n = x / sqrt(sum_i x_i^2 / size + epsilon) * scale   over the `size` elements of a head
+ * and of the first `rotary` of them each pair (n1, n2) becomes
+ *   (n1 * cos - n2 * sin, n2 * cos + n1 * sin)
+ * with the cosine and sine of the row's position and the pair, p = 0 to
+ * rotary/2 - 1, from the caller's tables: elements p and p + rotary/2, or 2p and
+ * 2p + 1 when interleaved.  Elements past `rotary` are not rotated.
+ * A row of a negative position is none: it is not read, its outputs are zero and
+ * it adds nothing to the gradients of the scales.  A position at or past the
+ * table's end, which cannot be refused from the host, makes the row's rotated
+ * elements (and their gradients) no numbers.  Q_out may be the very buffer of Q,
+ * with its row_stride, and K_out that of K. */
+typedef struct {
+  int32_t dtype;        /* rnn_dtype of Q, K, the scales, the outputs and row gradients */
+  int32_t interleaved;  /* 0 or 1 */
+  float epsilon;        /* >= 0, finite */
+  int64_t rows;         /* >= 0, at most 2^30 */
+  int64_t q_heads;      /* >= 1, at most 2^20 */
+  int64_t k_heads;      /* >= 0, at most 2^20 */
+  int64_t size;         /* 1 to 512 (above: RNN_ERR_UNSUPPORTED) */
+  int64_t rotary;       /* even, 0 (no rotation: no table, positions optional) to size */
+  int64_t table;        /* positions that the tables hold, >= 0 */
+} rnn_rotary_desc;
+
+typedef struct rnn_rotary rnn_rotary;
+
+typedef struct {
+  rnn_rows Q;            /* [q_heads * size] a row             required */
+  rnn_rows K;            /* [k_heads * size] a row             required with K_out, or a gradient of the keys */
+  rnn_tensor q_scale;    /* [size]                             optional (ones) */
+  rnn_tensor k_scale;    /* [size]                             optional (ones) */
+  rnn_tensor cos;        /* [table, rotary / 2] f32            required with a rotation */
+  rnn_tensor sin;        /* as cos */
+  rnn_tensor positions;  /* [rows] int32                       required with a rotation */
+  rnn_rows Q_out;        /* as Q                               optional output (forward only) */
+  rnn_rows K_out;        /* as K                               optional output (forward only) */
+} rnn_rotary_operands;
+
+typedef struct {
+  rnn_rows dQ_out;       /* as Q                               required */
+  rnn_rows dK_out;       /* as K                               required with a gradient of the keys */
+  rnn_rows dQ;           /* as Q                               optional outputs from here on */
+  rnn_rows dK;           /* as K */
+  rnn_tensor dq_scale;   /* [size] f32 */
+  rnn_tensor dk_scale;   /* [size] f32 */
+} rnn_rotary_gradients;
+
+int rnn_rotary_create(const rnn_rotary_desc* desc, rnn_rotary** out);
+void rnn_rotary_destroy(rnn_rotary* rotary);
+/* Scratch of rnn_rotary_encode (always 0) and of rnn_rotary_encode_backward;
+ * 256-byte aligned device memory. */
+int rnn_rotary_scratch_size(const rnn_rotary* rotary, size_t* forward_bytes, size_t* backward_bytes);
+int rnn_rotary_encode(const rnn_rotary* rotary, const rnn_rotary_operands* operands, void* scratch, void* stream);
+int rnn_rotary_encode_backward(const rnn_rotary* rotary, const rnn_rotary_operands* operands,
+                               const rnn_rotary_gradients* gradients, void* scratch, void* stream);
+
 /* Message of the last failed call on this thread ("" if none): the cell
- * (LSTM, GRU or RNN) or operator (conv, scan or layer norm) and the argument at fault, as the page's shape
+ * (LSTM, GRU or RNN) or operator (conv, scan, layer norm, linear attention or rotary norm) and the argument at fault, as the page's shape
  * exception names them ("Scratch").  The string is owned by the library and
  * valid until the thread's next call. */
 const char* rnn_last_error(void);

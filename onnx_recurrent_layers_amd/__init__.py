@@ -143,6 +143,22 @@ class rnn_attn_gradients(ctypes.Structure):
                 ("dG", rnn_rows), ("d_decay", rnn_tensor), ("d_initial_state", rnn_tensor)]
 
 
+class rnn_rotary_desc(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("epsilon", ctypes.c_float),
+                ("rows", ctypes.c_int64), ("q_heads", ctypes.c_int64), ("k_heads", ctypes.c_int64),
+                ("size", ctypes.c_int64), ("rotary", ctypes.c_int64), ("table", ctypes.c_int64)]
+
+
+class rnn_rotary_operands(ctypes.Structure):
+    _fields_ = [("Q", rnn_rows), ("K", rnn_rows), ("q_scale", rnn_tensor), ("k_scale", rnn_tensor), ("cos", rnn_tensor),
+                ("sin", rnn_tensor), ("positions", rnn_tensor), ("Q_out", rnn_rows), ("K_out", rnn_rows)]
+
+
+class rnn_rotary_gradients(ctypes.Structure):
+    _fields_ = [("dQ_out", rnn_rows), ("dK_out", rnn_rows), ("dQ", rnn_rows), ("dK", rnn_rows),
+                ("dq_scale", rnn_tensor), ("dk_scale", rnn_tensor)]
+
+
 # rnn_products: which arithmetic units carry a stage's products
 PRODUCTS = {0: "f32 vector ALU", 1: "f32 matrix cores", 2: "f16 matrix cores", 3: "bf16x3 matrix cores"}
 
@@ -187,7 +203,8 @@ def load_library(path: str = LIB_PATH):
     for op, desc, operands, gradients in (("conv", rnn_conv_desc, rnn_conv_operands, rnn_conv_gradients),
                                           ("scan", rnn_scan_desc, rnn_scan_operands, rnn_scan_gradients),
                                           ("norm", rnn_norm_desc, rnn_norm_operands, rnn_norm_gradients),
-                                          ("attn", rnn_attn_desc, rnn_attn_operands, rnn_attn_gradients)):
+                                          ("attn", rnn_attn_desc, rnn_attn_operands, rnn_attn_gradients),
+                                          ("rotary", rnn_rotary_desc, rnn_rotary_operands, rnn_rotary_gradients)):
         def declare(name, restype, *argtypes):
             f = getattr(lib, f"rnn_{op}_{name}")
             f.argtypes, f.restype = list(argtypes), restype
@@ -484,6 +501,28 @@ def rnn_attn_encode_backward(handle, operands: rnn_attn_operands, gradients: rnn
                                                    stream_ptr or None))
 
 
+def rnn_rotary_create(desc: rnn_rotary_desc) -> ctypes.c_void_p:
+    return _create("rnn_rotary_create", desc)
+
+
+def rnn_rotary_destroy(handle) -> None:
+    load_library().rnn_rotary_destroy(handle)
+
+
+def rnn_rotary_scratch_size(handle):
+    return _scratch("rnn_rotary_scratch_size", handle)
+
+
+def rnn_rotary_encode(handle, operands: rnn_rotary_operands, scratch_ptr: int = 0, stream_ptr: int = 0) -> None:
+    _check(load_library().rnn_rotary_encode(handle, operands, scratch_ptr or None, stream_ptr or None))
+
+
+def rnn_rotary_encode_backward(handle, operands: rnn_rotary_operands, gradients: rnn_rotary_gradients,
+                               scratch_ptr: int = 0, stream_ptr: int = 0) -> None:
+    _check(load_library().rnn_rotary_encode_backward(handle, operands, gradients, scratch_ptr or None,
+                                                     stream_ptr or None))
+
+
 class _Operator:
     """One created problem of the operators below plus its scratch (made by the
     first call, forward and backward, on that call's stream), for repeated
@@ -754,6 +793,37 @@ class LinearAttention(_Operator):
             return {"Q": k, "K": k, "V": v, "G": g, "decay": head, "sequence_lens": ((batch,), torch.int32, False),
                     "initial_state": state, "Y": v, "final_state": state, "dY": v, "d_final_state": state, "dQ": k,
                     "dK": k, "dV": v, "dG": g, "d_decay": head, "d_initial_state": state}
+
+        self._open(desc, device, shapes)
+
+
+class RotaryNorm(_Operator):
+    """Norms of queries and keys for each head with the position rotation in the
+    same pass (``rnn_rotary_*``), and its gradient.  Q is [rows, q_heads * size],
+    K [rows, k_heads * size]; cos and sin are [table, rotary / 2] and f32,
+    positions [rows] and int32, a negative one marking a row that is none.
+    ``rotary`` (default: ``size``) elements of each head are rotated."""
+
+    op, who = "rotary", "rotary norm"
+    _operands, _gradients = rnn_rotary_operands, rnn_rotary_gradients
+    operand_names = tuple(n for n, _ in rnn_rotary_operands._fields_)
+    input_names = operand_names[:-2]
+    gradient_names = tuple(n for n, _ in rnn_rotary_gradients._fields_)
+
+    def __init__(self, dtype: str, rows: int, q_heads: int, k_heads: int, size: int, table: int,
+                 rotary: Optional[int] = None, interleaved: bool = False, epsilon: float = 1e-6, device: str = "cuda"):
+        self.dtype = dtype
+        rotary = size if rotary is None else rotary
+        desc = rnn_rotary_desc(DTYPES[dtype], int(interleaved), float(epsilon), int(rows), int(q_heads), int(k_heads),
+                               int(size), int(rotary), int(table))
+
+        def shapes(torch, dt):
+            q, k = ((rows, q_heads * size), dt, True), ((rows, k_heads * size), dt, True)
+            scale, grad = ((size,), dt, False), ((size,), torch.float32, False)
+            angles = ((table, rotary // 2), torch.float32, False)
+            return {"Q": q, "K": k, "q_scale": scale, "k_scale": scale, "cos": angles, "sin": angles,
+                    "positions": ((rows,), torch.int32, False), "Q_out": q, "K_out": k, "dQ_out": q, "dK_out": k,
+                    "dQ": q, "dK": k, "dq_scale": grad, "dk_scale": grad}
 
         self._open(desc, device, shapes)
 

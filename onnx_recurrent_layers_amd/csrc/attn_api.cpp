@@ -1,5 +1,5 @@
-// attn_api.cpp -- the C ABI of linear attention: validation, scratch sizing,
-// the walks of a call.  Every check runs in 64-bit checked arithmetic before
+// attn_api.cpp -- the C ABI of linear attention and of the norms and rotations
+// of its queries and keys: validation, scratch sizing, the launches of a call.  Every check runs in 64-bit checked arithmetic before
 // anything is enqueued; messages name operator and argument.
 #include <cmath>
 #include <new>
@@ -16,9 +16,16 @@ struct rnn_attn {
   size_t backward_bytes;
 };
 
+struct rnn_rotary {
+  rnn_rotary_desc d;
+  int es;
+  int64_t parts;          // workgroups of the gradient
+  size_t backward_bytes;
+};
+
 namespace {
 
-const char kAttn[] = "linear attention";
+const char kAttn[] = "linear attention", kRotary[] = "rotary norm";
 
 // The scratch regions of the gradient, in the order that they are taken.
 struct AttnScratch {
@@ -215,4 +222,167 @@ extern "C" int rnn_attn_encode_backward(const rnn_attn* attn, const rnn_attn_ope
   if (!ddecay) return RNN_OK;
   const ColSumArgs cs{f(at.decay), int(d.batch), d.heads, ddecay, nullptr, int(d.heads), 1};
   return attn_launch("sums", launch_colsum(cs, s));
+}
+
+// ---------------------------------------------------------------- rotary norm
+
+namespace {
+
+// How a launch lies over rows and heads: the lanes of a head, and the waves of a
+// row, more than one where rows alone do not fill the chip.
+void rotary_lay(const rnn_rotary& p, bool vec, RotaryArgs& a) {
+  const rnn_rotary_desc& d = p.d;
+  const int v = vec ? 16 / p.es : 1;
+  a.vec = vec;
+  a.units = int(d.rotary / 2 / v + ceil_div(d.size - d.rotary, 2 * v));
+  a.lph = 1;
+  while (a.lph < 64 && a.lph < a.units) a.lph *= 2;
+  const int64_t heads = d.q_heads + d.k_heads, rounds = ceil_div(heads, 64 / a.lph);
+  a.splits = int(d.rows >= 4096 ? 1 : std::min<int64_t>(rounds, ceil_div(4096, std::max<int64_t>(d.rows, 1))));
+  a.take = int(ceil_div(rounds, a.splits) * (64 / a.lph));
+  a.splits = int(ceil_div(heads, a.take));
+}
+
+// The operands both directions read.
+void rotary_inputs(const rnn_rotary& p, const rnn_rotary_operands& o, bool keys, Tensors& t, RotaryArgs& a) {
+  const rnn_rotary_desc& d = p.d;
+  const bool any = d.rows > 0, turned = any && d.rotary > 0;
+  a.x[0] = t.rows(o.Q, p.es, d.q_heads * d.size, d.rows, "Q", any);
+  a.x[1] = t.rows(o.K, p.es, d.k_heads * d.size, d.rows, "K", any && keys);
+  a.scale[0] = t.tensor(o.q_scale, p.es, "q_scale", false);
+  a.scale[1] = t.tensor(o.k_scale, p.es, "k_scale", false);
+  a.cos = reinterpret_cast<const float*>(t.tensor(o.cos, 4, "cos", turned));
+  a.sin = reinterpret_cast<const float*>(t.tensor(o.sin, 4, "sin", turned));
+  a.positions = reinterpret_cast<const int32_t*>(t.tensor(o.positions, 4, "positions", turned));
+  a.rows = d.rows;
+  a.heads[0] = int(d.q_heads), a.heads[1] = int(d.k_heads);
+  a.size = int(d.size);
+  a.rotary = int(d.rotary), a.half = int(d.rotary / 2);
+  a.table = int(d.table);
+  a.interleaved = d.interleaved;
+  a.eps = d.epsilon;
+}
+
+bool rotary_vec(const rnn_rotary& p, const RotaryArgs& a) {
+  const int v = 2 * 16 / p.es;
+  bool ok = p.d.size % v == 0 && p.d.rotary % v == 0 && aligned(a.cos, 16) && aligned(a.sin, 16);
+  for (int k = 0; k < 2; ++k)
+    ok = ok && aligned(a.x[k], 16, p.es) && aligned(a.out[k], 16, p.es) && aligned(a.dy[k], 16, p.es) && aligned(a.scale[k], 16);
+  return ok;
+}
+
+}  // namespace
+
+extern "C" int rnn_rotary_create(const rnn_rotary_desc* desc, rnn_rotary** out) {
+  set_error_of(RNN_OK, nullptr, nullptr);
+  if (out) *out = nullptr;
+  if (!desc) return fail(RNN_ERR_ARG, kRotary, "desc: NULL");
+  if (!out) return fail(RNN_ERR_ARG, kRotary, "out: NULL");
+  const rnn_rotary_desc& d = *desc;
+  if (d.dtype < RNN_DTYPE_F32 || d.dtype > RNN_DTYPE_BF16) return fail(RNN_ERR_ARG, kRotary, "dtype: unknown value %d", d.dtype);
+  if (d.interleaved != 0 && d.interleaved != 1) return fail(RNN_ERR_ARG, kRotary, "interleaved: must be 0 or 1");
+  if (!(d.epsilon >= 0.f) || std::isinf(d.epsilon)) return fail(RNN_ERR_ARG, kRotary, "epsilon: must be finite and not negative");
+  if (d.rows < 0) return fail(RNN_ERR_SHAPE, kRotary, "rows: negative (%lld)", (long long)d.rows);
+  if (d.q_heads < 1) return fail(RNN_ERR_SHAPE, kRotary, "q_heads: must be at least 1 (%lld)", (long long)d.q_heads);
+  if (d.k_heads < 0) return fail(RNN_ERR_SHAPE, kRotary, "k_heads: negative (%lld)", (long long)d.k_heads);
+  if (d.size < 1) return fail(RNN_ERR_SHAPE, kRotary, "size: must be at least 1 (%lld)", (long long)d.size);
+  if (d.rotary < 0 || d.rotary > d.size || d.rotary % 2)
+    return fail(RNN_ERR_SHAPE, kRotary, "rotary: even, 0 to size (%lld of %lld)", (long long)d.rotary, (long long)d.size);
+  if (d.table < 0) return fail(RNN_ERR_SHAPE, kRotary, "table: negative (%lld)", (long long)d.table);
+  if (d.size > kRotaryMaxSize) return fail(RNN_ERR_UNSUPPORTED, kRotary, "size: above %d", kRotaryMaxSize);
+  if (d.q_heads > (int64_t(1) << 20) || d.k_heads > (int64_t(1) << 20)) return fail(RNN_ERR_UNSUPPORTED, kRotary, "heads: above 2^20");
+  if (d.rows > (int64_t(1) << 30)) return fail(RNN_ERR_UNSUPPORTED, kRotary, "rows: above 2^30");
+  if (d.table > (int64_t(1) << 30)) return fail(RNN_ERR_UNSUPPORTED, kRotary, "table: above 2^30");
+  rnn_rotary p{};
+  p.d = d;
+  p.es = elem_size(d.dtype);
+  if (bytes_of({d.rows, std::max(d.q_heads, d.k_heads), d.size, p.es}) < 0) return fail(RNN_ERR_SHAPE, kRotary, "Q: size overflows");
+  RotaryArgs a{};
+  rotary_lay(p, false, a);
+  p.parts = std::max<int64_t>(1, std::min<int64_t>(1024, ceil_div(d.rows * a.splits, 4)));
+  Regions r;
+  r.take({p.parts, 2, d.size, 4});
+  p.backward_bytes = r.off;
+  rnn_rotary* q = new (std::nothrow) rnn_rotary(p);
+  if (!q) return fail(RNN_ERR_ARG, kRotary, "out of host memory");
+  *out = q;
+  return RNN_OK;
+}
+
+extern "C" void rnn_rotary_destroy(rnn_rotary* rotary) { delete rotary; }
+
+extern "C" int rnn_rotary_scratch_size(const rnn_rotary* rotary, size_t* forward_bytes, size_t* backward_bytes) {
+  set_error_of(RNN_OK, nullptr, nullptr);
+  if (!rotary) return fail(RNN_ERR_ARG, kRotary, "rotary: NULL");
+  if (forward_bytes) *forward_bytes = 0;
+  if (backward_bytes) *backward_bytes = rotary->backward_bytes;
+  return RNN_OK;
+}
+
+extern "C" int rnn_rotary_encode(const rnn_rotary* rotary, const rnn_rotary_operands* operands, void* scratch, void* stream) {
+  (void)scratch;
+  set_error_of(RNN_OK, nullptr, nullptr);
+  if (!rotary) return fail(RNN_ERR_ARG, kRotary, "rotary: NULL");
+  if (!operands) return fail(RNN_ERR_ARG, kRotary, "operands: NULL");
+  const rnn_rotary& p = *rotary;
+  const rnn_rotary_desc& d = p.d;
+  const rnn_rotary_operands& o = *operands;
+  Tensors t(kRotary);
+  RotaryArgs a{};
+  rotary_inputs(p, o, o.K_out.ptr != nullptr, t, a);
+  a.out[0] = t.rows(o.Q_out, p.es, d.q_heads * d.size, d.rows, "Q_out", false, true);
+  a.out[1] = t.rows(o.K_out, p.es, d.k_heads * d.size, d.rows, "K_out", false, true);
+  t.apart({{"Q", "Q_out"}, {"K", "K_out"}});
+  if (t.status != RNN_OK) return t.status;
+  for (int k = 0; k < 2; ++k)
+    if (a.out[k].p && a.out[k].p == a.x[k].p && a.out[k].rs != a.x[k].rs)
+      return fail(RNN_ERR_ARG, kRotary, "%s: the memory of its input at another row_stride", k ? "K_out" : "Q_out");
+  if (d.rows == 0 || (!a.out[0].p && !a.out[1].p)) return RNN_OK;
+  rotary_lay(p, rotary_vec(p, a), a);
+  const int64_t blocks = std::min<int64_t>(ceil_div(d.rows * a.splits, 4), int64_t(1) << 23);
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  OnDevice on(s);
+  if (hipError_t e = launch_rotary(a, d.dtype, blocks, s); e != hipSuccess)
+    return fail(RNN_ERR_HIP, kRotary, "launch: %s", hipGetErrorString(e));
+  return RNN_OK;
+}
+
+extern "C" int rnn_rotary_encode_backward(const rnn_rotary* rotary, const rnn_rotary_operands* operands,
+                                          const rnn_rotary_gradients* gradients, void* scratch, void* stream) {
+  set_error_of(RNN_OK, nullptr, nullptr);
+  if (!rotary) return fail(RNN_ERR_ARG, kRotary, "rotary: NULL");
+  if (!operands) return fail(RNN_ERR_ARG, kRotary, "operands: NULL");
+  if (!gradients) return fail(RNN_ERR_ARG, kRotary, "gradients: NULL");
+  const rnn_rotary& p = *rotary;
+  const rnn_rotary_desc& d = p.d;
+  const rnn_rotary_gradients& g = *gradients;
+  Tensors t(kRotary);
+  RotaryArgs a{};
+  const bool keys = d.k_heads > 0 && (g.dK_out.ptr || g.dK.ptr || g.dk_scale.ptr);
+  const bool any = d.rows > 0;
+  rotary_inputs(p, *operands, keys, t, a);
+  a.dy[0] = t.rows(g.dQ_out, p.es, d.q_heads * d.size, d.rows, "dQ_out", any);
+  a.dy[1] = t.rows(g.dK_out, p.es, d.k_heads * d.size, d.rows, "dK_out", any && keys);
+  a.out[0] = t.rows(g.dQ, p.es, d.q_heads * d.size, d.rows, "dQ", false, true);
+  a.out[1] = t.rows(g.dK, p.es, d.k_heads * d.size, d.rows, "dK", false, true);
+  float* dq = reinterpret_cast<float*>(t.tensor(g.dq_scale, 4, "dq_scale", false, true));
+  float* dk = reinterpret_cast<float*>(t.tensor(g.dk_scale, 4, "dk_scale", false, true));
+  t.apart();
+  if (t.status != RNN_OK) return t.status;
+  if (!a.out[0].p && !a.out[1].p && !dq && !dk) return RNN_OK;
+  if (int rc = check_scratch(kRotary, scratch, dq || dk ? p.backward_bytes : 0)) return rc;
+  if (!keys) a.x[1].p = nullptr;
+  if (!a.out[0].p && !dq) a.x[0].p = nullptr;
+  a.part = dq || dk ? static_cast<float*>(scratch) : nullptr;
+  rotary_lay(p, rotary_vec(p, a), a);
+  const int64_t blocks = a.part ? p.parts : std::max<int64_t>(1, std::min<int64_t>(ceil_div(d.rows * a.splits, 4), int64_t(1) << 23));
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  OnDevice on(s);
+  if (hipError_t e = launch_rotary_backward(a, d.dtype, blocks, s); e != hipSuccess)
+    return fail(RNN_ERR_HIP, kRotary, "launch: %s", hipGetErrorString(e));
+  if (!a.part) return RNN_OK;
+  const ColSumArgs cs{a.part, int(p.parts), 2 * d.size, dq, dk, int(d.size), 1};
+  if (hipError_t e = launch_colsum(cs, s); e != hipSuccess)
+    return fail(RNN_ERR_HIP, kRotary, "sums launch: %s", hipGetErrorString(e));
+  return RNN_OK;
 }

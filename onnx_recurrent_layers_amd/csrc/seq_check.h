@@ -6,6 +6,7 @@
 #include <algorithm>
 #include <cstdarg>
 #include <cstdio>
+#include <cstring>
 #include <initializer_list>
 
 #include "seq_ops.h"
@@ -108,7 +109,7 @@ class Tensors {
     for (int i = 0; i < n_ && status == RNN_OK; ++i)
       for (int j = 0; j < i && status == RNN_OK; ++j)
         if (seen_[i].p == seen_[j].p && (seen_[i].output || seen_[j].output) &&
-            std::none_of(pairs.begin(), pairs.end(), [&](const Pair& p) { return seen_[i].name == p.b && seen_[j].name == p.a; }))
+            std::none_of(pairs.begin(), pairs.end(), [&](const Pair& p) { return !std::strcmp(seen_[i].name, p.b) && !std::strcmp(seen_[j].name, p.a); }))
           status = fail(RNN_ERR_ARG, who_, "%s: the same memory as %s", seen_[i].name, seen_[j].name);
   }
 
@@ -183,7 +184,7 @@ inline SeqGeom geometry(int64_t seq, int64_t batch, int layout, int direction, c
   return g;
 }
 
-// Names that may be one buffer (compared by address).
+// Names that may be one buffer.
 inline constexpr char kInitial[] = "initial_state", kFinal[] = "final_state";
 
 }  // namespace rnnhip

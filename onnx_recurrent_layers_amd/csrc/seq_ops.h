@@ -1,6 +1,7 @@
 // seq_ops.h -- arguments and launchers of the state space operators (short
 // causal convolution, selective scan), of layer normalization and of linear
-// attention, between their C ABI (seq_api.cpp, attn_api.cpp) and their kernels.
+// attention and its position rotation, between their C ABI (seq_api.cpp,
+// attn_api.cpp) and their kernels.
 // Internal.
 #pragma once
 
@@ -172,6 +173,22 @@ struct HeadSumArgs {
   Rows out;
 };
 
+// Norms and rotations of a row's heads, queries [0] and keys [1].
+struct RotaryArgs {
+  int64_t rows;
+  int32_t heads[2], size;
+  int32_t rotary, half, table, interleaved;   // elements rotated, pairs, positions of the table
+  float eps;
+  Rows x[2], out[2], dy[2];   // out: the outputs, backward the gradients of x
+  const char* scale[2];
+  const float *cos, *sin;
+  const int32_t* positions;
+  float* part;                // backward: [workgroups][2][size], or NULL
+  int32_t vec, units, lph;    // 16-byte accesses; pieces of a head, lanes that share them
+  int32_t splits, take;       // waves of a row, heads that each takes
+};
+
+constexpr int kRotaryMaxSize = 512;
 constexpr int kAttnMaxSize = 256;   // of a head's keys and values
 constexpr int kAttnCols = 64;       // columns of v and out that a workgroup takes
 
@@ -215,6 +232,8 @@ hipError_t launch_norm_backward(const NormArgs& a, int dtype, hipStream_t s);
 hipError_t launch_attn_steps(const AttnArgs& a, int dtype, hipStream_t s);
 hipError_t launch_attn_decay(const AttnDecayArgs& a, hipStream_t s);
 hipError_t launch_head_sum(const HeadSumArgs& a, int dtype, hipStream_t s);
+hipError_t launch_rotary(const RotaryArgs& a, int dtype, int64_t blocks, hipStream_t s);
+hipError_t launch_rotary_backward(const RotaryArgs& a, int dtype, int64_t blocks, hipStream_t s);
 hipError_t launch_colsum(const ColSumArgs& a, hipStream_t s);
 
 // From api.cpp: the thread's error message, "who: text".
