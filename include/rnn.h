@@ -54,6 +54,9 @@
  *                                   n steps (rounded up to whole tiles; above
  *                                   the length: one chunk), read by
  *                                   rnn_scan_create
+ *       RNN_ATTN_PIECE=n            linear attention's time axis in pieces of n
+ *                                   steps (rounded up to 64s; above the length:
+ *                                   one piece), read by rnn_attn_create
  *
  * Beside the recurrent layers: the operators of a selective state space block
  * (rnn_conv_*: the short causal convolution; rnn_scan_*: the selective scan;

@@ -2,18 +2,27 @@
 // of its queries and keys: validation, scratch sizing, the launches of a call.  Every check runs in 64-bit checked arithmetic before
 // anything is enqueued; messages name operator and argument.
 #include <cmath>
+#include <cstdlib>
 #include <new>
 
+#include "attn_ops.h"
 #include "seq_check.h"
 
 using namespace rnnhip;
 
+// The time axis of a call in pieces.
+struct AttnPlan {
+  int piece, pieces;
+};
+
 struct rnn_attn {
   rnn_attn_desc d;
   int es;
-  int per;                // heads of a group
+  int per;                    // heads of a group
   int key_cols, value_cols;   // workgroups along a head's keys and values
-  size_t backward_bytes;
+  bool tokens;                // step after step
+  AttnPlan f, b, bd;          // forward; the gradient without and with the decays'
+  size_t forward_bytes, backward_bytes;
 };
 
 struct rnn_rotary {
@@ -27,18 +36,46 @@ namespace {
 
 const char kAttn[] = "linear attention", kRotary[] = "rotary norm";
 
-// The scratch regions of the gradient, in the order that they are taken.
+// The pieces of a call whose walks have `blocks` workgroups a piece.  Where these
+// fill the chip by themselves one piece does; more cost a launch for the states
+// that they leave and one that joins them.  `most`: steps of a piece at most.
+AttnPlan attn_plan(const rnn_attn_desc& d, bool tokens, int64_t blocks, int64_t most) {
+  if (tokens) return {int(std::max<int64_t>(d.seq, 1)), 1};
+  const int64_t whole = ceil_div(d.seq, 64) * 64;
+  int64_t piece = whole;
+  if (blocks <= 256) piece = std::max<int64_t>(ceil_div(ceil_div(whole, ceil_div(512, std::max<int64_t>(blocks, 1))), 64) * 64, 128);
+  piece = std::min(std::min(piece, most), whole);
+  if (const char* e = std::getenv("RNN_ATTN_PIECE")) {
+    const int64_t c = std::atoll(e);
+    if (c > 0) piece = c >= whole ? whole : ceil_div(c, 64) * 64;
+  }
+  return {int(piece), int(ceil_div(d.seq, piece))};
+}
+
+// The scratch regions of the two directions, in the order that they are taken.
 struct AttnScratch {
-  size_t rows, cols, ends, decay, part;
+  size_t starts, totals, back_starts, back_totals, rows, cols, ends, decay, part;
 };
-bool attn_scratch(const rnn_attn& p, AttnScratch* at, size_t* total) {
+bool attn_scratch(const rnn_attn& p, bool backward, AttnScratch* at, size_t* total) {
   const rnn_attn_desc& d = p.d;
+  const int64_t pieces = backward ? std::max(p.b.pieces, p.bd.pieces) : p.f.pieces;
   Regions r;
-  at->rows = r.take({p.key_cols, d.batch, d.heads, d.seq, 4});
-  at->cols = r.take({p.key_cols, d.batch, d.heads, d.seq, 4});
-  at->ends = r.take({p.key_cols, d.batch, d.heads, 4});
-  at->decay = r.take({d.batch, d.heads, 4});
-  at->part = p.per > 1 ? r.take({d.seq, d.batch, d.heads, d.key, 4}) : r.off;
+  *at = AttnScratch{};
+  if (pieces > 1) {
+    at->starts = r.take({d.batch, d.heads, pieces, d.key, d.value, 4});
+    at->totals = r.take({d.batch, d.heads, pieces, 4});
+  }
+  if (backward) {
+    if (pieces > 1) {
+      at->back_starts = r.take({d.batch, d.heads, pieces, d.key, d.value, 4});
+      at->back_totals = r.take({d.batch, d.heads, pieces, 4});
+    }
+    at->rows = r.take({p.key_cols, d.batch, d.heads, d.seq, 4});
+    at->cols = r.take({p.key_cols, d.batch, d.heads, d.seq, 4});
+    at->ends = r.take({p.key_cols, d.batch, d.heads, p.bd.pieces, 4});
+    at->decay = r.take({d.batch, d.heads, p.bd.pieces, 4});
+    if (p.per > 1) at->part = r.take({d.seq, d.batch, d.heads, d.key, 4});
+  }
   *total = r.off;
   return r.ok;
 }
@@ -66,8 +103,28 @@ AttnInputs attn_inputs(const rnn_attn& p, const rnn_attn_operands& o, Tensors& t
   return in;
 }
 
+// One walk of all pieces.
+hipError_t attn_walk(const rnn_attn& p, const AttnArgs& a, bool local, hipStream_t s) {
+  if (p.tokens) return launch_attn_steps(a, p.d.dtype, s);
+  return p.d.dtype == RNN_DTYPE_F32   ? launch_attn_chunks_f32(a, local, s)
+         : p.d.dtype == RNN_DTYPE_F16 ? launch_attn_chunks_f16(a, local, s)
+                                      : launch_attn_chunks_bf16(a, local, s);
+}
+
 int attn_launch(const char* what, hipError_t e) {
   return e == hipSuccess ? RNN_OK : fail(RNN_ERR_HIP, kAttn, "%s launch: %s", what, hipGetErrorString(e));
+}
+
+// The states that the pieces of a walk begin with, from `init`.
+int attn_starts(const rnn_attn& p, const AttnArgs& a, hipStream_t s) {
+  if (a.pieces == 1) return RNN_OK;
+  AttnArgs w = a;
+  w.K = int(p.d.key), w.V = int(p.d.value);
+  w.sk = int(p.d.value), w.sv = 1;
+  w.dots = w.ends = nullptr;
+  if (int rc = attn_launch("pieces", attn_walk(p, w, true, s))) return rc;
+  const AttnJoinArgs j{a.pieces, a.back, p.d.batch * p.d.heads, p.d.key * p.d.value, a.starts, a.totals, a.init};
+  return attn_launch("join", launch_attn_join(j, s));
 }
 
 }  // namespace
@@ -95,10 +152,19 @@ extern "C" int rnn_attn_create(const rnn_attn_desc* desc, rnn_attn** out) {
   if (bytes_of({d.seq, d.batch, d.heads, d.key, p.es}) < 0) return fail(RNN_ERR_SHAPE, kAttn, "Q: size overflows");
   if (bytes_of({d.seq, d.batch, d.heads, d.value, p.es}) < 0) return fail(RNN_ERR_SHAPE, kAttn, "V: size overflows");
   if (bytes_of({d.batch, d.heads, d.key, d.value, 4}) < 0) return fail(RNN_ERR_SHAPE, kAttn, "initial_state: size overflows");
-  if (bytes_of({d.batch, d.heads, std::max(p.key_cols, p.value_cols), 256}) > kMaxThreads)
+  const int64_t heads = d.batch * d.heads, blocks = heads * std::max(p.key_cols, p.value_cols);   // (below 2^57)
+  p.tokens = d.seq <= kAttnSteps;
+  p.f = attn_plan(d, p.tokens, heads * p.value_cols, d.seq + 64);
+  p.b = attn_plan(d, p.tokens, heads * std::min(p.key_cols, p.value_cols), d.seq + 64);
+  // (the decays' gradient is summed back from a piece's end: pieces of 512 steps
+  // keep what the sums lose small next to it)
+  p.bd = attn_plan(d, p.tokens, heads * std::min(p.key_cols, p.value_cols), 512);
+  const int64_t pieces = std::max(std::max(p.f.pieces, p.b.pieces), p.bd.pieces);
+  if (bytes_of({blocks, pieces, 256}) < 0 || blocks * pieces * 256 > kMaxThreads || heads * ceil_div(d.key * d.value, 256) * 256 > kMaxThreads)
     return fail(RNN_ERR_UNSUPPORTED, kAttn, "batch x heads: too large for one launch");
   AttnScratch at;
-  if (!attn_scratch(p, &at, &p.backward_bytes)) return fail(RNN_ERR_SHAPE, kAttn, "scratch: size overflows");
+  if (!attn_scratch(p, false, &at, &p.forward_bytes) || !attn_scratch(p, true, &at, &p.backward_bytes))
+    return fail(RNN_ERR_SHAPE, kAttn, "scratch: size overflows");
   rnn_attn* q = new (std::nothrow) rnn_attn(p);
   if (!q) return fail(RNN_ERR_ARG, kAttn, "out of host memory");
   *out = q;
@@ -110,13 +176,12 @@ extern "C" void rnn_attn_destroy(rnn_attn* attn) { delete attn; }
 extern "C" int rnn_attn_scratch_size(const rnn_attn* attn, size_t* forward_bytes, size_t* backward_bytes) {
   set_error_of(RNN_OK, nullptr, nullptr);
   if (!attn) return fail(RNN_ERR_ARG, kAttn, "attn: NULL");
-  if (forward_bytes) *forward_bytes = 0;
+  if (forward_bytes) *forward_bytes = attn->forward_bytes;
   if (backward_bytes) *backward_bytes = attn->backward_bytes;
   return RNN_OK;
 }
 
 extern "C" int rnn_attn_encode(const rnn_attn* attn, const rnn_attn_operands* operands, void* scratch, void* stream) {
-  (void)scratch;
   set_error_of(RNN_OK, nullptr, nullptr);
   if (!attn) return fail(RNN_ERR_ARG, kAttn, "attn: NULL");
   if (!operands) return fail(RNN_ERR_ARG, kAttn, "operands: NULL");
@@ -135,9 +200,17 @@ extern "C" int rnn_attn_encode(const rnn_attn* attn, const rnn_attn_operands* op
   a.K = int(d.key), a.V = int(d.value);
   a.sk = int(d.value), a.sv = 1;
   a.in_scale = 1.f, a.out_scale = d.scale;
+  a.piece = p.f.piece, a.pieces = p.f.pieces;
+  if (int rc = check_scratch(kAttn, scratch, p.forward_bytes)) return rc;
+  AttnScratch at;
+  size_t total;
+  attn_scratch(p, false, &at, &total);
+  a.starts = reinterpret_cast<float*>(static_cast<char*>(scratch) + at.starts);
+  a.totals = reinterpret_cast<float*>(static_cast<char*>(scratch) + at.totals);
   hipStream_t s = static_cast<hipStream_t>(stream);
   OnDevice on(s);
-  return attn_launch("forward", launch_attn_steps(a, d.dtype, s));
+  if (int rc = attn_starts(p, a, s)) return rc;
+  return attn_launch("forward", attn_walk(p, a, false, s));
 }
 
 extern "C" int rnn_attn_encode_backward(const rnn_attn* attn, const rnn_attn_operands* operands,
@@ -168,10 +241,27 @@ extern "C" int rnn_attn_encode_backward(const rnn_attn* attn, const rnn_attn_ope
   if (int rc = check_scratch(kAttn, scratch, p.backward_bytes)) return rc;
   AttnScratch at;
   size_t total;
-  attn_scratch(p, &at, &total);
+  attn_scratch(p, true, &at, &total);
   auto f = [&](size_t off) { return reinterpret_cast<float*>(static_cast<char*>(scratch) + off); };
   hipStream_t s = static_cast<hipStream_t>(stream);
   OnDevice on(s);
+  const AttnPlan& plan = decays ? p.bd : p.b;
+  a.piece = plan.piece, a.pieces = plan.pieces;
+  // forward in time from the initial state, back from the final one's gradient
+  AttnArgs fore = a, back = a;
+  fore.in_scale = 1.f, fore.out_scale = d.scale;
+  fore.init = in.init;
+  fore.b = in.K, fore.v = in.V;
+  fore.starts = f(at.starts), fore.totals = f(at.totals);
+  back.back = 1;
+  back.in_scale = d.scale, back.out_scale = 1.f;
+  back.init = dfin;
+  back.b = in.Q, back.v = dY;
+  back.starts = f(at.back_starts), back.totals = f(at.back_totals);
+  if (dQ.p || decays)
+    if (int rc = attn_starts(p, fore, s)) return rc;
+  if (dK.p || dV.p || dinit || decays)
+    if (int rc = attn_starts(p, back, s)) return rc;
 
   // dQ and dK: of each head by itself, summed over a group's heads
   auto shared = [&](const char* what, AttnArgs w, const Rows& out, const HeadRows& dot, float* dots) -> int {
@@ -182,45 +272,42 @@ extern "C" int rnn_attn_encode_backward(const rnn_attn* attn, const rnn_attn_ope
     w.out_f32 = sum;
     w.dot = dot;
     w.dots = decays ? dots : nullptr;
-    if (int rc = attn_launch(what, launch_attn_steps(w, d.dtype, s))) return rc;
+    if (int rc = attn_launch(what, attn_walk(p, w, false, s))) return rc;
     if (!sum) return RNN_OK;
     const HeadSumArgs hs{f(at.part), rows, int(d.heads), p.per, int(d.key), out};
     return attn_launch("sum", launch_head_sum(hs, d.dtype, s));
   };
+  const bool ends = decays && (dfin || a.pieces > 1);
   if (dQ.p || decays) {
-    AttnArgs w = a;
+    AttnArgs w = fore;
     w.a = dY, w.b = in.V, w.v = in.K;
-    w.init = in.init;
-    w.in_scale = 1.f, w.out_scale = d.scale;
-    if (decays && dfin) {
+    if (ends) {
       w.other = dfin;
+      w.others = a.pieces > 1 ? back.starts : nullptr;
       w.ends = f(at.ends);
     }
     if (int rc = shared("dQ", w, dQ, in.Q, f(at.rows))) return rc;
   }
-  a.back = 1;
-  a.in_scale = d.scale, a.out_scale = 1.f;
-  a.init = dfin;
   if (dK.p || decays) {
-    AttnArgs w = a;
+    AttnArgs w = back;
     w.a = in.V, w.b = dY, w.v = in.Q;
     if (int rc = shared("dK", w, dK, in.K, f(at.cols))) return rc;
   }
   if (dV.p || dinit) {
-    AttnArgs w = a;
+    AttnArgs w = back;
     w.a = in.K, w.b = in.Q, w.v = dY;
     w.K = int(d.key), w.V = int(d.value);
     w.sk = int(d.value), w.sv = 1;
     w.out = head_rows(dV, 1);
     w.fin = dinit;
-    if (int rc = attn_launch("dV", launch_attn_steps(w, d.dtype, s))) return rc;
+    if (int rc = attn_launch("dV", attn_walk(p, w, false, s))) return rc;
   }
   if (!decays) return RNN_OK;
-  const AttnDecayArgs da{a.geo, a.H, p.key_cols, p.key_cols, f(at.rows), f(at.cols), dfin ? f(at.ends) : nullptr, a.G, a.decay, dG,
+  const AttnDecayArgs da{a.geo, a.H, p.key_cols, a.piece, a.pieces, f(at.rows), f(at.cols), ends ? f(at.ends) : nullptr, a.G, a.decay, dG,
                          ddecay ? f(at.decay) : nullptr};
   if (int rc = attn_launch("decay", launch_attn_decay(da, s))) return rc;
   if (!ddecay) return RNN_OK;
-  const ColSumArgs cs{f(at.decay), int(d.batch), d.heads, ddecay, nullptr, int(d.heads), 1};
+  const ColSumArgs cs{f(at.decay), int(d.batch) * a.pieces, d.heads, ddecay, nullptr, int(d.heads), 1};
   return attn_launch("sums", launch_colsum(cs, s));
 }
 

@@ -2,6 +2,7 @@
 // their rows, decays, states.  Internal.
 #pragma once
 
+#include "attn_ops.h"
 #include "seq_device.h"
 
 namespace rnnhip {

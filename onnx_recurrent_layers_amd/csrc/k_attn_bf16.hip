@@ -1,0 +1,8 @@
+// k_attn_bf16.hip -- linear attention over chunks, bf16 tensors (attn_chunk.h).
+#include "attn_chunk.h"
+
+namespace rnnhip {
+
+hipError_t launch_attn_chunks_bf16(const AttnArgs& a, bool local, hipStream_t s) { return attn_chunks<bf16_t>(a, local, s); }
+
+}  // namespace rnnhip

@@ -1,0 +1,8 @@
+// k_attn_f32.hip -- linear attention over chunks, f32 tensors (attn_chunk.h).
+#include "attn_chunk.h"
+
+namespace rnnhip {
+
+hipError_t launch_attn_chunks_f32(const AttnArgs& a, bool local, hipStream_t s) { return attn_chunks<float>(a, local, s); }
+
+}  // namespace rnnhip

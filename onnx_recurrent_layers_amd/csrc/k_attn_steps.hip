@@ -121,25 +121,42 @@ __global__ __launch_bounds__(256) void attn_steps_kernel(AttnArgs a) {
       if (c0 + (t & 63) < a.V) r.put(dead_row(a.geo, b, s), c0 + (t & 63), 0.f);
 }
 
-// A row's steps of a head, 256 at a time from the last: the sum of what is left
-// of each step's pairs with earlier steps less those with later ones.  64-bit
-// sums, since over a long row the two nearly cancel.
+// An element of a head's states a thread, through the pieces in the walk's order.
+__global__ __launch_bounds__(256) void attn_join_kernel(AttnJoinArgs a) {
+  const int64_t per = (a.size + 255) / 256, bh = int64_t(blockIdx.x) / per, i = (int64_t(blockIdx.x) - bh * per) * 256 + threadIdx.x;
+  if (i >= a.size) return;
+  float* p = a.starts + bh * a.pieces * a.size + i;
+  float v = a.init ? a.init[bh * a.size + i] : 0.f;
+  for (int k = 0; k < a.pieces; ++k) {
+    const int at = a.back ? a.pieces - 1 - k : k;
+    const float local = k + 1 < a.pieces ? p[at * a.size] : 0.f;
+    p[at * a.size] = v;
+    if (k + 1 < a.pieces) v = __builtin_fmaf(v, a.totals[bh * a.pieces + at], local);
+  }
+}
+
+// A piece's steps of a head, 256 at a time from the last: the sum of what is left
+// of each step's pairs with earlier steps less those with later ones, whose
+// whole is at hand again at each piece's end.  64-bit sums, since the two
+// nearly cancel.
 __global__ __launch_bounds__(256) void attn_decay_kernel(AttnDecayArgs a) {
   __shared__ double part[4];
-  const int t = int(threadIdx.x), b = int(blockIdx.x) / a.H, h = int(blockIdx.x) - b * a.H;
-  const int L = geo_len(a.geo, b), w = t >> 6;
+  const int t = int(threadIdx.x), w = t >> 6;
+  const int64_t head = int64_t(a.geo.B) * a.H, bh = int64_t(blockIdx.x) / a.pieces;
+  const int piece = int(int64_t(blockIdx.x) - bh * a.pieces), b = int(bh / a.H), h = int(bh - int64_t(b) * a.H);
+  const int L = geo_len(a.geo, b);
+  const int64_t lo64 = int64_t(piece) * a.piece;
+  const int lo = int(min(lo64, int64_t(a.geo.S))), end = int(min(lo64 + a.piece, int64_t(a.geo.S))), hi = min(end, L);
   const StepRows r = step_rows(a.geo, b, L);
-  const int64_t head = int64_t(a.geo.B) * a.H, n = head * a.geo.S, at = int64_t(blockIdx.x) * a.geo.S;
+  const int64_t n = head * a.geo.S, at = bh * a.geo.S;
   double after = 0., total = 0.;   // the gradient just after the block's steps; a thread's part of its sum
-  if (a.ends)
-    for (int k = 0; k < a.row_slices; ++k) after += a.ends[k * head + blockIdx.x];
-  for (int s1 = L; s1 > 0; s1 -= 256) {
+  if (a.ends && hi > lo)
+    for (int k = 0; k < a.slices; ++k) after += a.ends[(k * head + bh) * a.pieces + piece];
+  for (int s1 = hi; s1 > lo; s1 -= 256) {
     const int s = s1 - 1 - t;   // thread 0: the last step
     double x = 0.;
-    if (s >= 0) {
-      for (int k = 0; k < a.row_slices; ++k) x += a.rows[k * n + at + s];
-      for (int k = 0; k < a.col_slices; ++k) x -= a.cols[k * n + at + s];
-    }
+    if (s >= lo)
+      for (int k = 0; k < a.slices; ++k) x += double(a.rows[k * n + at + s]) - double(a.cols[k * n + at + s]);
 #pragma unroll
     for (int m = 1; m < 64; m *= 2) {
       const double o = __shfl_up(x, m, 64);
@@ -153,7 +170,7 @@ __global__ __launch_bounds__(256) void attn_decay_kernel(AttnDecayArgs a) {
       if (k < w) before += part[k];
       after += part[k];
     }
-    if (s >= 0) {
+    if (s >= lo) {
       const int64_t row = r.base + s * r.step;
       float g = a.G.p ? reinterpret_cast<const float*>(a.G.p)[row * a.G.rs + h] : 0.f;
       if (a.decay) g += a.decay[h];
@@ -163,14 +180,14 @@ __global__ __launch_bounds__(256) void attn_decay_kernel(AttnDecayArgs a) {
     }
   }
   if (a.dG.p)
-    for (int s = L + t; s < a.geo.S; s += 256) reinterpret_cast<float*>(a.dG.p)[dead_row(a.geo, b, s) * a.dG.rs + h] = 0.f;
+    for (int s = max(lo, L) + t; s < end; s += 256) reinterpret_cast<float*>(a.dG.p)[dead_row(a.geo, b, s) * a.dG.rs + h] = 0.f;
   if (!a.part) return;
 #pragma unroll
   for (int m = 1; m < 64; m *= 2) total += __shfl_xor(total, m, 64);
   __syncthreads();
   if ((t & 63) == 0) part[w] = total;
   __syncthreads();
-  if (t == 0) a.part[blockIdx.x] = float(((part[0] + part[1]) + part[2]) + part[3]);
+  if (t == 0) a.part[(int64_t(b) * a.pieces + piece) * a.H + h] = float(((part[0] + part[1]) + part[2]) + part[3]);
 }
 
 template <typename T>
@@ -208,7 +225,13 @@ hipError_t launch_attn_steps(const AttnArgs& a, int dtype, hipStream_t s) {
   return dtype == RNN_DTYPE_F32 ? steps<float>(a, s) : dtype == RNN_DTYPE_F16 ? steps<f16_t>(a, s) : steps<bf16_t>(a, s);
 }
 
-hipError_t launch_attn_decay(const AttnDecayArgs& a, hipStream_t s) { return go(attn_decay_kernel, int64_t(a.geo.B) * a.H, 256, a, s); }
+hipError_t launch_attn_join(const AttnJoinArgs& a, hipStream_t s) {
+  return go(attn_join_kernel, a.heads * ((a.size + 255) / 256), 256, a, s);
+}
+
+hipError_t launch_attn_decay(const AttnDecayArgs& a, hipStream_t s) {
+  return go(attn_decay_kernel, int64_t(a.geo.B) * a.H * a.pieces, 256, a, s);
+}
 
 hipError_t launch_head_sum(const HeadSumArgs& a, int dtype, hipStream_t s) {
   const int64_t all = (a.rows * (a.H / a.per) * a.K + 255) / 256, blocks = all < 1 << 20 ? all : 1 << 20;

@@ -13,6 +13,7 @@
 // of a row at a time: what a lane loads of the table of cosines and sines, and of
 // scale, then serves all heads that it takes of the row, which keeps the table
 // (as many bytes a head as the head itself) out of the way.
+#include "attn_ops.h"
 #include "seq_device.h"
 
 namespace rnnhip {

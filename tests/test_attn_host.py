@@ -93,6 +93,29 @@ def test_nothing_asked_for_is_nothing_done(handle):
     rl.rnn_attn_destroy(h)
 
 
+def test_scratch_sizes(monkeypatch):
+    def up(n):
+        return (n + 255) // 256 * 256
+
+    def sizes(**kw):
+        h = rl.rnn_attn_create(desc(**kw))
+        try:
+            return rl.rnn_attn_scratch_size(h)
+        finally:
+            rl.rnn_attn_destroy(h)
+
+    monkeypatch.delenv("RNN_ATTN_PIECE", raising=False)
+    # tokens: each step's two sums and each row's product and sum; for shared queries a row of every head
+    rows, one = up(3 * 6 * 4 * 4), up(3 * 6 * 4)
+    assert sizes(seq=4) == (0, 2 * rows + 2 * one + up(4 * 3 * 6 * 4 * 4))
+    assert sizes(seq=4, groups=6) == (0, 2 * rows + 2 * one)
+    monkeypatch.setenv("RNN_ATTN_PIECE", "100")    # of 128 steps: two
+    starts = up(3 * 6 * 2 * 4 * 8 * 4) + up(3 * 6 * 2 * 4)
+    assert sizes(seq=200, groups=6) == (starts, 2 * starts + 2 * up(3 * 6 * 200 * 4) + 2 * up(3 * 6 * 2 * 4))
+    monkeypatch.setenv("RNN_ATTN_PIECE", "1000")
+    assert sizes(seq=200, groups=6) == (0, 2 * up(3 * 6 * 200 * 4) + 2 * up(3 * 6 * 4))
+
+
 def test_binding_refuses_tensors():
     op = rl.LinearAttention(dtype="f16", seq=4, batch=3, heads=6, groups=2, key=5, value=7, device="cuda:0")
     op._index = -1     # CPU tensors stand for the device's: nothing is launched

@@ -274,3 +274,42 @@ def test_graphs_and_streams(s):
         for a, c in ((f, f2), (g, g2)):
             for n in a:
                 assert torch.equal(a[n], c[n]), (seed, n)
+
+
+@pytest.mark.parametrize("dtype", ref.TYPES)
+@pytest.mark.parametrize("name", ["Q", "K", "V", "G"])
+@pytest.mark.parametrize("bad", [float("inf"), float("nan")])
+def test_values_that_are_not_finite(dtype, name, bad):
+    """A step's infinity or NaN spoils what depends on it and nothing else: no earlier step, no other head or column."""
+    if name == "G" and bad > 0:
+        bad = float("nan")
+    b, s, h, k, v, at = 2, 200, 2, 32, 40, 70
+    t = values(dtype, b, s, h, h, k, v)
+    t[name][0, at, 1] = bad     # of head 0; of G head 1
+    op = rl.LinearAttention(dtype=dtype, seq=s, batch=b, heads=h, key=k, value=v)
+    to = types(dtype)
+    d = {n: x.to(to[n]).cuda() for n, x in t.items()}
+    y, fin = torch.empty(b, s, h * v, dtype=to["Y"], device="cuda"), torch.empty(b, h, k, v, device="cuda")
+    op.encode({**{n: d[n] for n in ("Q", "K", "V", "G", "decay", "initial_state")}, "Y": y, "final_state": fin})
+    torch.cuda.synchronize()
+    want = reference(t, dtype, h, h, 1.0, None, False, False)
+    clean = reference({**t, name: values(dtype, b, s, h, h, k, v)[name]}, dtype, h, h, 1.0, None, False, False)
+    for got, n in ((y, "Y"), (fin, "final_state")):
+        value, bound = want[n]
+        ok = value.isfinite()
+        assert torch.equal(got.cpu().isfinite(), ok), n
+        got = torch.where(ok, got.cpu().double(), torch.zeros_like(value))
+        att.close(got, torch.where(ok, value, torch.zeros_like(value)), torch.where(ok, clean[n][1], torch.zeros_like(value)),
+                  dtype if n == "Y" else "f32", n)
+    one = y.view(b, s, h, v)
+    assert one[0, :at].isfinite().all() and one[1].isfinite().all() and one[0, :, 0 if name == "G" else 1].isfinite().all()
+
+
+@pytest.mark.parametrize("dtype", ref.TYPES)
+@pytest.mark.parametrize("piece", [64, 128, 1000])
+def test_pieces(dtype, piece, monkeypatch):
+    monkeypatch.setenv("RNN_ATTN_PIECE", str(piece))
+    for s, lens, reverse in ((64, None, False), (65, [65, 64], True), (300, [300, 129], False), (300, [128, 0], True)):
+        attn_case(dtype, 2, s, 2, 1, 48, 72, lens=lens, reverse=reverse, device="cuda")
+    attn_case(dtype, 1, 400, 2, 2, 16, 16, gate=40.0, device="cuda")
+    attn_case(dtype, 1, 400, 2, 2, 130, 130, device="cuda")
