@@ -176,13 +176,21 @@ __device__ __forceinline__ Scale wave_scale(float m) {
 
 __device__ __forceinline__ bool finite(float x) { return __builtin_fabsf(x) < __builtin_inff(); }
 
+// The value, unknown to the compiler from here on: conditions on it are made where
+// they are used.  (Kept from the kernel's start to its end, masks of 64 lanes for
+// each row of a state fill the scalar registers.)
+__device__ __forceinline__ int afresh(int x) {
+  asm volatile("" : "+v"(x));
+  return x;
+}
+
 enum { kAttnLocal, kAttnWalk, kAttnDots };
 
 // KT: 32-wide pieces of a and b.  MODE: the state that a piece of the time axis
 // leaves from a zero one; the outputs; these with what the decays' gradient
 // needs.  VEC: rows in aligned 16-byte pieces.
 template <typename T, int KT, int MODE, bool VEC>
-__global__ __launch_bounds__(256) void attn_chunk_kernel(AttnArgs a) {
+__global__ __launch_bounds__(256, 2) void attn_chunk_kernel(AttnArgs a) {
   typedef Mma<T> M;
   typedef typename M::Op Op;
   constexpr bool WALK = MODE != kAttnLocal, DOTS = MODE == kAttnDots;
@@ -209,36 +217,52 @@ __global__ __launch_bounds__(256) void attn_chunk_kernel(AttnArgs a) {
   const int64_t KV = int64_t(a.K) * a.V;
   const float scale = a.in_scale * a.out_scale;
 
-  // a chunk's rows, in registers until the one before is done with
+  // a chunk's rows, in registers until the one before is done with.  A thread's
+  // rows of a tensor are RK (RV) apart; past the last one it repeats that, and
+  // what it got is made zero on the way to shared memory.
   typedef Pack<T, M::Vec> Piece;
+  constexpr int RK = 256 / CK, RV = 256 / CV;
+  const int tk = t / CK, ck = t % CK * M::Vec, tv = t / CV, cv = t % CV * M::Vec;
+  const int64_t way = a.back ? -r.r.step : r.r.step, top = n > 0 ? r.row(0) : 0;
+  struct Walker {   // a thread's pieces of one tensor, a chunk's first row first
+    const T *p, *last;
+    int64_t rs;
+  };
+  auto walker = [&](const HeadRows& x, int size, int row, int c) {
+    const int64_t rs = way * x.rs;
+    const T* p = reinterpret_cast<const T*>(x.p) + top * x.rs + (h / x.per) * int64_t(size) + (c < size ? c : 0);
+    return Walker{p + row * rs, p + max(n - 1, 0) * rs, rs};
+  };
+  Walker wa = WALK ? walker(a.a, a.K, tk, ck) : Walker{}, wb = walker(a.b, a.K, tk, ck), wv = walker(a.v, a.V, tv, c0 + cv);
   Piece ra[WALK ? NK : 1], rb[NK], rv[NV];
-  float rg = 0.f;
-  auto piece_of = [&](const HeadRows& x, int size, int u, int c) {
+  auto load = [&](const Walker& x, int u, int i, int by, int size, int c) {
+    const T* at = u + i * by < n ? x.p + i * by * x.rs : x.last;
     Piece p = {};
-    if (u >= n || c >= size) return p;
-    const T* at = reinterpret_cast<const T*>(x.p) + r.row(u) * x.rs + (h / x.per) * int64_t(size) + c;
     if constexpr (VEC) {
       p = *reinterpret_cast<const Piece*>(at);
     } else {
 #pragma unroll
-      for (int i = 0; i < M::Vec; ++i)
-        if (c + i < size) p.v[i] = at[i];
+      for (int k = 0; k < M::Vec; ++k)
+        if (c + k < size) p.v[k] = at[k];
     }
     return p;
   };
+  float rg = 0.f;
   auto fetch = [&](int u0) {
 #pragma unroll
     for (int i = 0; i < NK; ++i) {
-      const int id = i * 256 + t;
-      if constexpr (WALK) ra[i] = piece_of(a.a, a.K, u0 + id / CK, id % CK * M::Vec);
-      rb[i] = piece_of(a.b, a.K, u0 + id / CK, id % CK * M::Vec);
+      if constexpr (WALK) ra[i] = load(wa, u0 + tk, i, RK, a.K, ck);
+      rb[i] = load(wb, u0 + tk, i, RK, a.K, ck);
     }
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int id = i * 256 + t;
-      rv[i] = piece_of(a.v, a.V, u0 + id / CV, c0 + id % CV * M::Vec);
-    }
+    for (int i = 0; i < NV; ++i) rv[i] = load(wv, u0 + tv, i, RV, a.V, c0 + cv);
     rg = lane < TC && u0 + lane < n ? r.log_decay(u0 + lane) : 0.f;
+    wa.p += TC * wa.rs;
+    wb.p += TC * wb.rs;
+    wv.p += TC * wv.rs;
+  };
+  auto keep = [&](Piece& p, bool is) {
+    if (!is) p = Piece{};
   };
   // lane i: the sums of log decays (to base 2) up to step i
   double csum = 0., ctotal = 0.;
@@ -259,17 +283,33 @@ __global__ __launch_bounds__(256) void attn_chunk_kernel(AttnArgs a) {
   const bool col = cw + q < a.V;
   const float* start = !WALK ? nullptr : a.pieces > 1 ? a.starts + (int64_t(bh) * a.pieces + piece) * KV : a.init ? a.init + bh * KV : nullptr;
   auto state_at = [&](int k, int i) { return int64_t(16 * k + 4 * g + i) * a.sk + int64_t(cw + q) * a.sv; };
-  auto has = [&](int k, int i) { return col && 16 * k + 4 * g + i < a.K; };
+  // rows that there are among 4 g + (0..3) on (none without a column): for k, i those below
+  auto rows_of = [&] { return afresh(col ? a.K - 4 * g : 0); };
   if (n > 0) fetch(0);
 #pragma unroll
-  for (int k = 0; k < 2 * KT; ++k)
+  for (int k = 0; k < 2 * KT; ++k) S[k] = f32x4{0.f, 0.f, 0.f, 0.f};
+  if (start) {   // (past the last row or column: some other, made zero)
+    const float* at = start + int64_t(col ? cw + q : 0) * a.sv;
+    const int rows = rows_of();
 #pragma unroll
-    for (int i = 0; i < 4; ++i) S[k][i] = start && has(k, i) ? start[state_at(k, i)] : 0.f;
+    for (int k = 0; k < 2 * KT; ++k)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) S[k][i] = at[min(16 * k + 4 * g + i, a.K - 1) * a.sk];
+#pragma unroll
+    for (int k = 0; k < 2 * KT; ++k)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) S[k][i] = 16 * k + i < rows ? S[k][i] : 0.f;
+  }
   if constexpr (WALK) {   // scores above the diagonal that a product reads
     for (int i = t; i < NP * TC * PP; i += 256) sp[0][0][i] = T(0.f);
   }
   sums();
   double all = 0.;   // of the piece
+  // this lane's first element of a chunk's outputs, and of the rows that they are multiplied with
+  const int64_t ors = way * a.out.rs, drs = way * a.dot.rs;
+  int64_t po = 0, pd = 0;
+  if constexpr (WALK) po = top * a.out.rs + (h / a.out.per) * int64_t(a.V) + cw + 4 * g + q * ors;
+  if constexpr (DOTS) pd = top * a.dot.rs + (h / a.dot.per) * int64_t(a.V) + cw + 4 * g + q * drs;
 
   // The steps of the chunk one by one, from shared memory.
   auto one_by_one = [&](int u0, int steps) {
@@ -277,12 +317,13 @@ __global__ __launch_bounds__(256) void attn_chunk_kernel(AttnArgs a) {
       const float dec = __builtin_amdgcn_exp2f(slog[u]);
       const float v = float(sv[u][16 * w + q]);
       float off = 0.f, y = 0.f;
+      const int rows = afresh(a.K - 4 * g);
 #pragma unroll
       for (int k = 0; k < 2 * KT; ++k)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int d = 16 * k + 4 * g + i;
-          if (d < a.K) {
+          if (16 * k + i < rows) {
             const float kb = float(sb[u][d]) * a.in_scale;
             S[k][i] *= dec;
             if constexpr (WALK) off = __builtin_fmaf(float(sa[u][d]), S[k][i], off);
@@ -313,17 +354,22 @@ __global__ __launch_bounds__(256) void attn_chunk_kernel(AttnArgs a) {
 
   for (int u0 = 0; u0 < n; u0 += TC) {
     __syncthreads();   // all are done with the chunk before
+    if (u0 + TC > n || a.K < 32 * KT || c0 + kAttnCols > a.V) {
+#pragma unroll
+      for (int i = 0; i < NK; ++i) {
+        if constexpr (WALK) keep(ra[i], u0 + tk + i * RK < n && ck < a.K);
+        keep(rb[i], u0 + tk + i * RK < n && ck < a.K);
+      }
+#pragma unroll
+      for (int i = 0; i < NV; ++i) keep(rv[i], u0 + tv + i * RV < n && c0 + cv < a.V);
+    }
 #pragma unroll
     for (int i = 0; i < NK; ++i) {
-      const int id = i * 256 + t;
-      if constexpr (WALK) *reinterpret_cast<Piece*>(&sa[id / CK][id % CK * M::Vec]) = ra[i];
-      *reinterpret_cast<Piece*>(&sb[id / CK][id % CK * M::Vec]) = rb[i];
+      if constexpr (WALK) *reinterpret_cast<Piece*>(&sa[tk + i * RK][ck]) = ra[i];
+      *reinterpret_cast<Piece*>(&sb[tk + i * RK][ck]) = rb[i];
     }
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int id = i * 256 + t;
-      *reinterpret_cast<Piece*>(&sv[id / CV][id % CV * M::Vec]) = rv[i];
-    }
+    for (int i = 0; i < NV; ++i) *reinterpret_cast<Piece*>(&sv[tv + i * RV][cv]) = rv[i];
     if (t < TC) {
       shi[t] = float(csum);
       slo[t] = float(csum - double(float(csum)));
@@ -446,7 +492,7 @@ __global__ __launch_bounds__(256) void attn_chunk_kernel(AttnArgs a) {
           const int u = 16 * i + q, c = cw + 4 * g;
           float d[4] = {};
           if (u < steps) {
-            const T* at = reinterpret_cast<const T*>(a.dot.p) + r.row(u0 + u) * a.dot.rs + (h / a.dot.per) * int64_t(a.V) + c;
+            const T* at = reinterpret_cast<const T*>(a.dot.p) + pd + i * 16 * drs;
             if (VEC && c < a.V) {
               const Pack<T, 4> x = *reinterpret_cast<const Pack<T, 4>*>(at);
 #pragma unroll
@@ -467,17 +513,18 @@ __global__ __launch_bounds__(256) void attn_chunk_kernel(AttnArgs a) {
           }
         }
       }
+      float zero = 0.f;   // (not so once anything is not finite)
 #pragma unroll
       for (int i = 0; i < IT; ++i)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) fine = fine && finite(y[i][k]);
-      fine = __builtin_amdgcn_ballot_w64(!fine) == 0;
+        for (int k = 0; k < 4; ++k) zero = __builtin_fmaf(y[i][k], 0.f, zero);
+      fine = __builtin_amdgcn_ballot_w64(zero != 0.f) == 0;
       if (fine) {
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
           const int u = 16 * i + q, c = cw + 4 * g;
           if (a.out.p && u < steps && c < a.V) {
-            const int64_t at = r.row(u0 + u) * a.out.rs + (h / a.out.per) * int64_t(a.V) + c;
+            const int64_t at = po + i * 16 * ors;
             if (a.out_f32) {
               float* o = reinterpret_cast<float*>(a.out.p) + at;
 #pragma unroll
@@ -543,6 +590,8 @@ __global__ __launch_bounds__(256) void attn_chunk_kernel(AttnArgs a) {
       }
     }
     if (u0 + TC < n) sums();
+    po += TC * ors;
+    pd += TC * drs;
   }
   if constexpr (!WALK) {
     // (what the products make of values that are not finite, the steps decide)
@@ -557,30 +606,33 @@ __global__ __launch_bounds__(256) void attn_chunk_kernel(AttnArgs a) {
       for (int u = 0; u < n; ++u) {
         const int64_t row = r.row(u);
         const float dec = __builtin_amdgcn_exp2f(r.log_decay(u) * kLog2e), v = col ? r.get(a.v, a.V, row, cw + q) : 0.f;
+        const int rows = afresh(a.K - 4 * g);
 #pragma unroll
         for (int k = 0; k < 2 * KT; ++k)
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            if (16 * k + 4 * g + i < a.K) S[k][i] = __builtin_fmaf(r.get(a.b, a.K, row, 16 * k + 4 * g + i) * a.in_scale, v, S[k][i] * dec);
+            if (16 * k + i < rows) S[k][i] = __builtin_fmaf(r.get(a.b, a.K, row, 16 * k + 4 * g + i) * a.in_scale, v, S[k][i] * dec);
       }
     }
     float* to = a.starts + (int64_t(bh) * a.pieces + piece) * KV;
+    const int rows = rows_of();
 #pragma unroll
     for (int k = 0; k < 2 * KT; ++k)
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        if (has(k, i)) to[state_at(k, i)] = S[k][i];
+        if (16 * k + i < rows) to[state_at(k, i)] = S[k][i];
     if (t == 0 && slice == 0) a.totals[int64_t(bh) * a.pieces + piece] = __builtin_amdgcn_exp2f(float(all));
     return;
   }
   if (a.fin && (a.back ? piece == 0 : lo < L ? hi == L : piece == 0 && L == 0)) {
     const float by = a.back && L > 0 ? __builtin_amdgcn_exp2f(r.first_decay() * kLog2e) : 1.f;
     float* to = a.fin + bh * KV;
+    const int rows = rows_of();
 #pragma unroll
     for (int k = 0; k < 2 * KT; ++k)
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        if (has(k, i)) to[state_at(k, i)] = S[k][i] * by;
+        if (16 * k + i < rows) to[state_at(k, i)] = S[k][i] * by;
   }
   if constexpr (DOTS) {
     __syncthreads();
@@ -588,12 +640,12 @@ __global__ __launch_bounds__(256) void attn_chunk_kernel(AttnArgs a) {
     if (a.ends) {   // the state after the piece by the gradient of the one before the next
       float d = 0.f;
       const float* other = a.others ? a.others + (int64_t(bh) * a.pieces + piece) * KV : a.other ? a.other + bh * KV : nullptr;
-      if (other)
+      const int rows = other ? rows_of() : 0;
 #pragma unroll
-        for (int k = 0; k < 2 * KT; ++k)
+      for (int k = 0; k < 2 * KT; ++k)
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (has(k, i)) d = __builtin_fmaf(S[k][i], other[state_at(k, i)], d);
+        for (int i = 0; i < 4; ++i)
+          if (16 * k + i < rows) d = __builtin_fmaf(S[k][i], other[state_at(k, i)], d);
 #pragma unroll
       for (int m = 1; m < 64; m *= 2) d += __shfl_xor(d, m, 64);
       __syncthreads();
