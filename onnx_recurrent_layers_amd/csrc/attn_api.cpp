@@ -43,7 +43,7 @@ AttnPlan attn_plan(const rnn_attn_desc& d, bool tokens, int64_t blocks, int64_t 
   if (tokens) return {int(std::max<int64_t>(d.seq, 1)), 1};
   const int64_t whole = ceil_div(d.seq, 64) * 64;
   int64_t piece = whole;
-  if (blocks <= 256) piece = std::max<int64_t>(ceil_div(ceil_div(whole, ceil_div(512, std::max<int64_t>(blocks, 1))), 64) * 64, 128);
+  if (blocks <= 128) piece = std::max<int64_t>(ceil_div(ceil_div(whole, ceil_div(256, std::max<int64_t>(blocks, 1))), 64) * 64, 128);
   piece = std::min(std::min(piece, most), whole);
   if (const char* e = std::getenv("RNN_ATTN_PIECE")) {
     const int64_t c = std::atoll(e);
@@ -147,20 +147,20 @@ extern "C" int rnn_attn_create(const rnn_attn_desc* desc, rnn_attn** out) {
   p.d = d;
   p.es = elem_size(d.dtype);
   p.per = int(d.heads / d.groups);
+  p.tokens = d.seq <= kAttnSteps;
   p.key_cols = int(ceil_div(d.key, kAttnCols));
   p.value_cols = int(ceil_div(d.value, kAttnCols));
   if (bytes_of({d.seq, d.batch, d.heads, d.key, p.es}) < 0) return fail(RNN_ERR_SHAPE, kAttn, "Q: size overflows");
   if (bytes_of({d.seq, d.batch, d.heads, d.value, p.es}) < 0) return fail(RNN_ERR_SHAPE, kAttn, "V: size overflows");
   if (bytes_of({d.batch, d.heads, d.key, d.value, 4}) < 0) return fail(RNN_ERR_SHAPE, kAttn, "initial_state: size overflows");
   const int64_t heads = d.batch * d.heads, blocks = heads * std::max(p.key_cols, p.value_cols);   // (below 2^57)
-  p.tokens = d.seq <= kAttnSteps;
   p.f = attn_plan(d, p.tokens, heads * p.value_cols, d.seq + 64);
   p.b = attn_plan(d, p.tokens, heads * std::min(p.key_cols, p.value_cols), d.seq + 64);
   // (the decays' gradient is summed back from a piece's end: pieces of 512 steps
   // keep what the sums lose small next to it)
   p.bd = attn_plan(d, p.tokens, heads * std::min(p.key_cols, p.value_cols), 512);
   const int64_t pieces = std::max(std::max(p.f.pieces, p.b.pieces), p.bd.pieces);
-  if (bytes_of({blocks, pieces, 256}) < 0 || blocks * pieces * 256 > kMaxThreads || heads * ceil_div(d.key * d.value, 256) * 256 > kMaxThreads)
+  if (bytes_of({blocks, pieces, 512}) < 0 || blocks * pieces * 512 > kMaxThreads || heads * ceil_div(d.key * d.value, 256) * 256 > kMaxThreads)
     return fail(RNN_ERR_UNSUPPORTED, kAttn, "batch x heads: too large for one launch");
   AttnScratch at;
   if (!attn_scratch(p, false, &at, &p.forward_bytes) || !attn_scratch(p, true, &at, &p.backward_bytes))

@@ -115,6 +115,23 @@ __device__ __forceinline__ typename Mma<T>::Op op_column(const T* base, int stri
   }
 }
 
+// Two values as 16 bits each, and what that leaves of them.
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t take_pair(f32x2& x, bf16_t) {
+  const uint32_t k = __builtin_bit_cast(uint32_t, __builtin_convertvector(x, bf16x2));
+  x[0] -= __builtin_bit_cast(float, k << 16);
+  x[1] -= __builtin_bit_cast(float, k & 0xffff0000u);
+  return k;
+}
+__device__ __forceinline__ uint32_t take_pair(f32x2& x, f16_t) {
+  const f16x2 k = __builtin_convertvector(x, f16x2);
+  x[0] = __builtin_fmaf(float(k[0]), -1.f, x[0]);
+  x[1] = __builtin_fmaf(float(k[1]), -1.f, x[1]);
+  return __builtin_bit_cast(uint32_t, k);
+}
+
 // N parts of eight values of 32 bits.
 template <typename T, int N>
 struct Parts {
@@ -126,16 +143,16 @@ __device__ __forceinline__ Parts<T, N> op_parts(const float (&x)[8]) {
   if constexpr (sizeof(T) == 4) {
     r.p[0] = {f32x4{x[0], x[1], x[2], x[3]}, f32x4{x[4], x[5], x[6], x[7]}};
   } else {
-    float left[8];
+    typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+    u32x4 k[N];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) left[i] = x[i];
+    for (int i = 0; i < 4; ++i) {
+      f32x2 left = {x[2 * i], x[2 * i + 1]};
 #pragma unroll
-    for (int n = 0; n < N; ++n)
+      for (int n = 0; n < N; ++n) k[n][i] = take_pair(left, T());
+    }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        r.p[n][i] = T(left[i]);
-        if (n + 1 < N) left[i] -= float(T(left[i]));
-      }
+    for (int n = 0; n < N; ++n) r.p[n] = __builtin_bit_cast(typename Mma<T>::Op, k[n]);
   }
   return r;
 }
@@ -174,6 +191,24 @@ __device__ __forceinline__ Scale wave_scale(float m) {
   return {__builtin_bit_cast(float, (267 - e) << 23), __builtin_bit_cast(float, (e - 13) << 23)};
 }
 
+// A sum over the lanes up to each one, without shared memory.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double lanes_before(double x) {
+  const uint64_t k = __builtin_bit_cast(uint64_t, x);
+  const uint32_t lo = __builtin_amdgcn_update_dpp(0, int(uint32_t(k)), CTRL, ROWS, 0xf, false);
+  const uint32_t hi = __builtin_amdgcn_update_dpp(0, int(uint32_t(k >> 32)), CTRL, ROWS, 0xf, false);
+  return __builtin_bit_cast(double, uint64_t(hi) << 32 | lo);
+}
+__device__ __forceinline__ double lanes_up_to(double x) {
+  x += lanes_before<0x111, 0xf>(x);   // by 1, 2, 4, 8 within sixteen
+  x += lanes_before<0x112, 0xf>(x);
+  x += lanes_before<0x114, 0xf>(x);
+  x += lanes_before<0x118, 0xf>(x);
+  x += lanes_before<0x142, 0xa>(x);   // the last of the sixteen before
+  x += lanes_before<0x143, 0xc>(x);   // and of the half before
+  return x;
+}
+
 __device__ __forceinline__ bool finite(float x) { return __builtin_fabsf(x) < __builtin_inff(); }
 
 // The value, unknown to the compiler from here on: conditions on it are made where
@@ -184,138 +219,337 @@ __device__ __forceinline__ int afresh(int x) {
   return x;
 }
 
+// Reads of shared memory above stay above: they are under way while the products
+// below are made.  (Left to itself the compiler asks for an operand right before
+// its use, and every product waits for one.)
+__device__ __forceinline__ void asked() { __builtin_amdgcn_sched_barrier(0); }
+
 enum { kAttnLocal, kAttnWalk, kAttnDots };
 
 // KT: 32-wide pieces of a and b.  MODE: the state that a piece of the time axis
 // leaves from a zero one; the outputs; these with what the decays' gradient
 // needs.  VEC: rows in aligned 16-byte pieces.
 template <typename T, int KT, int MODE, bool VEC>
-__global__ __launch_bounds__(256, 2) void attn_chunk_kernel(AttnArgs a) {
+__global__ __launch_bounds__(512, 2) void attn_chunk_kernel(AttnArgs a) {
   typedef Mma<T> M;
   typedef typename M::Op Op;
   constexpr bool WALK = MODE != kAttnLocal, DOTS = MODE == kAttnDots;
-  constexpr int TC = sizeof(T) == 4 && KT == 8 ? 32 : 64, IT = TC / 16, ST = TC / 32;   // steps of a chunk, in 16s and 32s
-  constexpr int KP = 32 * KT + M::Pad, VP = kAttnCols + M::Pad, PP = TC + M::Pad;
+  constexpr int TC = KT * int(sizeof(T)) >= 16 ? 32 : 64, IT = TC / 16, ST = TC / 32;    // steps of a chunk, in 16s and 32s
+  constexpr int COLS = kAttnCols;                                                        // of a workgroup
+  constexpr int KP = 32 * KT + M::Pad, VP = COLS + M::Pad, PP = 32 + M::Pad, PB = ST == 2 ? 6 : 2;
   constexpr int NP = DOTS ? M::Fine : M::Coarse, NU = M::Fine;
-  constexpr int CK = 32 * KT / M::Vec, CV = kAttnCols / M::Vec;                          // 16-byte pieces of a row
-  constexpr int NK = TC * CK / 256, NV = TC * CV / 256;                                  // of a thread
-  __shared__ alignas(16) T sa[WALK ? TC : 1][KP];
-  __shared__ alignas(16) T sb[TC][KP];
-  __shared__ alignas(16) T sv[TC][VP];
-  __shared__ alignas(16) T sp[WALK ? NP : 1][WALK ? TC : 1][PP];
-  __shared__ alignas(16) float shi[TC], slo[TC], ssince[TC], sleft[TC], slog[TC], sdiag[TC], sback[IT], red[4][TC];
-  const int t = int(threadIdx.x), lane = t & 63, w = __builtin_amdgcn_readfirstlane(t >> 6), q = lane & 15, g = lane >> 4;
-  const int slices = (a.V + kAttnCols - 1) / kAttnCols, pieces = WALK ? a.pieces : a.pieces - 1;
-  const int slice = int(blockIdx.x) % slices, bp = int(blockIdx.x) / slices, bh = bp / pieces;
+  constexpr int CK = 32 * KT / M::Vec, CV = COLS / M::Vec;                               // 16-byte pieces of a row
+  constexpr int RK = 256 / CK, RV = 256 / CV;                                            // rows that the threads take at once
+  constexpr int NK = (TC + RK - 1) / RK, NV = (TC + RV - 1) / RV;                        // pieces of a thread
+  constexpr int AHEAD = sizeof(T) == 4 && KT >= 4 ? 1 : 2;   // (wide rows of f32 fill the registers)
+  // two chunks' rows, sums and scores
+  __shared__ alignas(16) T sa[2][WALK ? TC : 1][KP];
+  __shared__ alignas(16) T sb[2][TC][KP];
+  __shared__ alignas(16) T sv[2][TC][VP];
+  // scores, 16 steps by 32: those of the first 32 steps for all, those of the next for the last 32
+  __shared__ alignas(16) T sp[2][WALK ? NP : 1][WALK ? PB : 1][16][PP];
+  __shared__ alignas(16) float shi[2][TC], slo[2][TC], ssince[2][TC], sleft[2][TC], slog[2][TC], sdiag[2][TC], sback[2][8], stotal[2], red[4][TC];
+  const int w = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
+  int t = int(threadIdx.x), lane = t & 63, q = lane & 15, g = lane >> 4;
+  const int slices = (a.V + COLS - 1) / COLS, pieces = WALK ? a.pieces : a.pieces - 1;
+  // a die's workgroups (they go to eight in turn) are neighbours: a head's slices share its a and b there
+  const int per_die = int(gridDim.x) / 8, rest = int(gridDim.x) % 8, die = int(blockIdx.x) % 8;
+  const int block = die * per_die + min(die, rest) + int(blockIdx.x) / 8;
+  const int slice = block % slices, bp = block / slices, bh = bp / pieces;
   const int piece = bp - bh * pieces + (!WALK && a.back ? 1 : 0);
   const int b = bh / a.H, h = bh - b * a.H;
   const int L = geo_len(a.geo, b);
   const int64_t lo64 = int64_t(piece) * a.piece;
   const int lo = int(min(lo64, int64_t(a.geo.S))), end = int(min(lo64 + a.piece, int64_t(a.geo.S))), hi = min(end, L), n = max(hi - lo, 0);
   const AttnSteps<T> r(a, b, h, L, lo, hi);
-  const int c0 = slice * kAttnCols, cw = c0 + 16 * w;   // columns of the workgroup, of the wave
+  const int c0 = slice * COLS;
   const int64_t KV = int64_t(a.K) * a.V;
-  const float scale = a.in_scale * a.out_scale;
-
-  // a chunk's rows, in registers until the one before is done with.  A thread's
-  // rows of a tensor are RK (RV) apart; past the last one it repeats that, and
-  // what it got is made zero on the way to shared memory.
-  typedef Pack<T, M::Vec> Piece;
-  constexpr int RK = 256 / CK, RV = 256 / CV;
-  const int tk = t / CK, ck = t % CK * M::Vec, tv = t / CV, cv = t % CV * M::Vec;
   const int64_t way = a.back ? -r.r.step : r.r.step, top = n > 0 ? r.row(0) : 0;
-  struct Walker {   // a thread's pieces of one tensor, a chunk's first row first
-    const T *p, *last;
-    int64_t rs;
-  };
-  auto walker = [&](const HeadRows& x, int size, int row, int c) {
-    const int64_t rs = way * x.rs;
-    const T* p = reinterpret_cast<const T*>(x.p) + top * x.rs + (h / x.per) * int64_t(size) + (c < size ? c : 0);
-    return Walker{p + row * rs, p + max(n - 1, 0) * rs, rs};
-  };
-  Walker wa = WALK ? walker(a.a, a.K, tk, ck) : Walker{}, wb = walker(a.b, a.K, tk, ck), wv = walker(a.v, a.V, tv, c0 + cv);
-  Piece ra[WALK ? NK : 1], rb[NK], rv[NV];
-  auto load = [&](const Walker& x, int u, int i, int by, int size, int c) {
-    const T* at = u + i * by < n ? x.p + i * by * x.rs : x.last;
-    Piece p = {};
-    if constexpr (VEC) {
-      p = *reinterpret_cast<const Piece*>(at);
-    } else {
-#pragma unroll
-      for (int k = 0; k < M::Vec; ++k)
-        if (c + k < size) p.v[k] = at[k];
-    }
-    return p;
-  };
-  float rg = 0.f;
-  auto fetch = [&](int u0) {
-#pragma unroll
-    for (int i = 0; i < NK; ++i) {
-      if constexpr (WALK) ra[i] = load(wa, u0 + tk, i, RK, a.K, ck);
-      rb[i] = load(wb, u0 + tk, i, RK, a.K, ck);
-    }
-#pragma unroll
-    for (int i = 0; i < NV; ++i) rv[i] = load(wv, u0 + tv, i, RV, a.V, c0 + cv);
-    rg = lane < TC && u0 + lane < n ? r.log_decay(u0 + lane) : 0.f;
-    wa.p += TC * wa.rs;
-    wb.p += TC * wb.rs;
-    wv.p += TC * wv.rs;
-  };
-  auto keep = [&](Piece& p, bool is) {
-    if (!is) p = Piece{};
-  };
-  // lane i: the sums of log decays (to base 2) up to step i
-  double csum = 0., ctotal = 0.;
-  float clog = 0.f;
-  auto sums = [&] {
-    clog = rg * kLog2e;
-    csum = double(rg) * 1.4426950408889634;
-#pragma unroll
-    for (int m = 1; m < 64; m *= 2) {
-      const double o = __shfl_up(csum, m, 64);
-      if (lane >= m) csum += o;
-    }
-    ctotal = __shfl(csum, 63, 64);
-  };
+  const bool down = way < 0;   // (the rows of later steps lie below: in one of a reverse layer and a walk back)
+  // the place of step u of a chunk among its rows from the lowest
+  auto place = [&](int u) { return down ? TC - 1 - u : u; };
+  const int chunks = (n + TC - 1) / TC;
 
-  // rows 16 k + 4 g + (0..3) of the state, column cw + q
+  if (w >= 4) {
+    // ---- rows into shared memory, and the scores
+    t -= 256;
+    // The rows of AHEAD chunks, in registers until their place is free (with one
+    // chunk's the loads come late).  A thread's rows of a tensor are RK (RV) apart;
+    // past the last one it repeats that, and what it got is made zero on the way to
+    // shared memory.  VEC: a chunk's lowest row is
+    // at a uniform address, a thread's own at an offset of 32 bits.
+    typedef Pack<T, M::Vec> Piece;
+    int tk, ck, tv, cv;
+    auto places = [&] {   // (made in each chunk: kept, they take more registers than there are)
+      t = afresh(t);
+      lane = t & 63, q = lane & 15, g = lane >> 4;
+      tk = t / CK, ck = t % CK * M::Vec, tv = t / CV, cv = t % CV * M::Vec;
+    };
+    struct Walker {
+      const T* p;     // of the head, the chunk's lowest row (VEC), or its first
+      int64_t rs;     // elements from a step to the next
+    };
+    auto walker = [&](const HeadRows& x, int size) {
+      const int64_t rs = way * x.rs;
+      const T* p = reinterpret_cast<const T*>(x.p) + top * x.rs + (h / x.per) * int64_t(size);
+      return Walker{p + (VEC && down ? (TC - 1) * rs : 0), rs};
+    };
+    Walker wa = WALK ? walker(a.a, a.K) : Walker{}, wb = walker(a.b, a.K), wv = walker(a.v, a.V);
+    struct Rows {
+      Piece a[WALK ? NK : 1], b[NK], v[NV];
+    } x[AHEAD];
+    auto load = [&](const Walker& from, int u, int left, int size, int c) {
+      u = min(u, left);
+      Piece p = {};
+      if constexpr (VEC) {
+        const uint32_t stride = uint32_t(down ? -from.rs : from.rs) * sizeof(T);
+        p = *reinterpret_cast<const Piece*>(reinterpret_cast<const char*>(from.p) + (uint32_t(place(u)) * stride + uint32_t(c < size ? c : 0) * uint32_t(sizeof(T))));
+      } else {
+#pragma unroll
+        for (int k = 0; k < M::Vec; ++k)
+          if (c + k < size) p.v[k] = from.p[u * from.rs + c + k];
+      }
+      return p;
+    };
+    // b and v of the steps from u0 on, and a
+    auto fetch_bv = [&](int u0, Rows& x) {
+      const int left = min(n - 1 - u0, TC - 1);   // (threads past a chunk's pieces repeat the last, too)
+#pragma unroll
+      for (int i = 0; i < NK; ++i) x.b[i] = load(wb, tk + i * RK, left, a.K, ck);
+#pragma unroll
+      for (int i = 0; i < NV; ++i) x.v[i] = load(wv, tv + i * RV, left, a.V, c0 + cv);
+      wb.p += TC * wb.rs;
+      wv.p += TC * wv.rs;
+    };
+    auto fetch_a = [&](int u0, Rows& x) {
+      if constexpr (WALK) {
+        const int left = min(n - 1 - u0, TC - 1);
+#pragma unroll
+        for (int i = 0; i < NK; ++i) x.a[i] = load(wa, tk + i * RK, left, a.K, ck);
+        wa.p += TC * wa.rs;
+      }
+    };
+    auto keep = [&](Piece& p, bool is) {
+      if (!is) p = Piece{};
+    };
+    // The last wave, lane i: the sums of log decays (to base 2) up to step i of the
+    // chunk to come, asked for a chunk earlier.
+    const bool sums_here = w == 7;
+    double all = 0.;   // of the piece
+    float rg = 0.f, clog = 0.f, chi = 0.f, clo = 0.f, csince = 0.f, cleft = 0.f, ctotal = 0.f;
+    auto later = [&](int u) { return r.step(u) + (a.back ? 1 : 0); };   // (AttnSteps::log_decay)
+    auto ask = [&](int u0) {
+      if (a.G.p) rg = r.raw_decay(min(later(min(u0 + lane, n - 1)), L - 1));
+    };
+    auto sums = [&](int u0) {
+      const bool is = lane < TC && u0 + lane < n && later(u0 + lane) < L;
+      const float x = is ? attn_log_decay(rg + r.fixed) : 0.f;
+      clog = x * kLog2e;
+      const double sum = lanes_up_to(double(x) * 1.4426950408889634);
+      const uint64_t k = __builtin_bit_cast(uint64_t, sum);
+      const double whole = __builtin_bit_cast(double, uint64_t(uint32_t(__builtin_amdgcn_readlane(int(k >> 32), 63))) << 32 | uint32_t(__builtin_amdgcn_readlane(int(uint32_t(k)), 63)));
+      chi = float(sum);
+      clo = float(sum - double(chi));
+      csince = __builtin_amdgcn_exp2f(chi) * a.out_scale;
+      cleft = __builtin_amdgcn_exp2f(float(whole - sum)) * a.in_scale;
+      ctotal = __builtin_amdgcn_exp2f(float(whole));
+      all += whole;
+    };
+    // what was fetched, of the steps from u0 on, and b and v of AHEAD chunks later asked for
+    auto put_rows = [&](int u0, int at, Rows& x) {
+      if (u0 + TC > n || a.K < 32 * KT || c0 + COLS > a.V) {
+#pragma unroll
+        for (int i = 0; i < NK; ++i) {
+          if constexpr (WALK) keep(x.a[i], u0 + tk + i * RK < n && ck < a.K);
+          keep(x.b[i], u0 + tk + i * RK < n && ck < a.K);
+        }
+#pragma unroll
+        for (int i = 0; i < NV; ++i) keep(x.v[i], u0 + tv + i * RV < n && c0 + cv < a.V);
+      }
+#pragma unroll
+      for (int i = 0; i < NK; ++i) {
+        if (TC % RK && tk + i * RK >= TC) break;   // (more threads than pieces)
+        if constexpr (WALK) *reinterpret_cast<Piece*>(&sa[at][tk + i * RK][ck]) = x.a[i];
+        *reinterpret_cast<Piece*>(&sb[at][tk + i * RK][ck]) = x.b[i];
+      }
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        if (TC % RV && tv + i * RV >= TC) break;
+        *reinterpret_cast<Piece*>(&sv[at][tv + i * RV][cv]) = x.v[i];
+      }
+      if (sums_here && lane < TC) {
+        shi[at][lane] = chi;
+        slo[at][lane] = clo;
+        ssince[at][lane] = csince;
+        sleft[at][lane] = cleft;
+        slog[at][lane] = clog;
+        stotal[at] = ctotal;
+      }
+      if (u0 + AHEAD * TC < n) fetch_bv(u0 + AHEAD * TC, x);
+    };
+    // when the scores are made: the rest of those loads, and the next chunk's sums
+    // (loads are spread over a chunk's time: they come no faster than the memory has
+    // them)
+    auto prepare = [&](int u0, Rows& x) {
+      if (u0 < n && sums_here) {
+        sums(u0);
+        ask(u0 + TC);
+      }
+      if (u0 + (AHEAD - 1) * TC < n) fetch_a(u0 + (AHEAD - 1) * TC, x);
+    };
+    // The scores of a block: of steps 16 it + q (a lane's) by those of one half of
+    // the chunk, zero past step 16 it + q.
+    const float scale = a.in_scale * a.out_scale;
+    auto scores = [&](int at, int it, int half) {
+      const int i = 16 * it + q, j0 = 32 * half, block = it + (half ? 2 : 0);
+      Op fa[KT], fb[2][KT];
+      f32x4 hj[2], lj[2];
+#pragma unroll
+      for (int k = 0; k < KT; ++k) fa[k] = op_run<T>(&sa[at][i][32 * k + 8 * g]);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+#pragma unroll
+        for (int k = 0; k < KT; ++k) fb[j][k] = op_run<T>(&sb[at][j0 + 16 * j + q][32 * k + 8 * g]);
+        hj[j] = *reinterpret_cast<const f32x4*>(&shi[at][j0 + 16 * j + 4 * g]);
+        lj[j] = *reinterpret_cast<const f32x4*>(&slo[at][j0 + 16 * j + 4 * g]);
+      }
+      const float hi_i = shi[at][i], lo_i = slo[at][i];
+      asked();
+      f32x4 c[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+      for (int k = 0; k < KT; ++k)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) c[j] = M::mul(fb[j][k], fa[k], c[j]);
+      float p[2][4], most = 0.f, own = 0.f;
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int to = i - (j0 + 16 * j + 4 * g + k);   // steps from one to the other
+          const float x = c[j][k] * (scale * __builtin_amdgcn_exp2f((hi_i - hj[j][k]) + (lo_i - lj[j][k])));
+          if (DOTS) own = to == 0 ? c[j][k] * scale : own;
+          p[j][k] = to >= (DOTS ? 1 : 0) ? x : 0.f;
+          if constexpr (M::Scaled) most = fmaxf(most, __builtin_fabsf(p[j][k]));
+        }
+      Scale sc{1.f, 1.f};
+      if constexpr (M::Scaled) {
+        sc = wave_scale(most);
+        if (lane == 0) sback[at][block] = sc.back;
+      }
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        T* to = &sp[at][0][block][q][16 * j + 4 * g];
+        if constexpr (sizeof(T) == 4) {
+          *reinterpret_cast<f32x4*>(to) = f32x4{p[j][0], p[j][1], p[j][2], p[j][3]};
+        } else {
+          f32x2 left[2] = {{p[j][0] * sc.by, p[j][1] * sc.by}, {p[j][2] * sc.by, p[j][3] * sc.by}};
+#pragma unroll
+          for (int m = 0; m < NP; ++m) {
+            uint2 x;
+            x.x = take_pair(left[0], T());
+            x.y = take_pair(left[1], T());
+            *reinterpret_cast<uint2*>(to + m * (PB * 16 * PP)) = x;
+          }
+        }
+      }
+      // (a step's own score: where its sixteen is among the block's, of four lanes the one that has it)
+      if (DOTS && it / 2 == half && (q >> 2) == g) sdiag[at][i] = own;
+    };
+    // A wave's blocks (steps, half): 3 0 and 0 0; 1 0; 2 0 and 2 1; 3 1.
+    auto all_scores = [&](int at) {
+      const int x = w - 4;
+      if constexpr (ST == 1) {
+        if (x < 2) scores(at, x, 0);
+      } else {
+        scores(at, x == 0 ? 3 : x, x == 3 ? 1 : 0);
+        if ((x & 1) == 0) scores(at, x, x / 2);
+      }
+    };
+    auto put_dots = [&](int u0) {
+      if (t >= TC || u0 + t >= n) return;
+      a.dots[((int64_t(slice) * a.geo.B + b) * a.H + h) * a.geo.S + r.step(u0 + t)] = ((red[0][t] + red[1][t]) + red[2][t]) + red[3][t];
+    };
+
+    places();
+    if (n > 0) {
+      if (sums_here) ask(0);
+      fetch_bv(0, x[0]);
+      fetch_a(0, x[0]);
+      if (AHEAD == 2 && n > TC) {
+        fetch_bv(TC, x[AHEAD - 1]);
+        fetch_a(TC, x[AHEAD - 1]);
+      }
+      if (sums_here) {
+        sums(0);
+        ask(TC);
+      }
+      put_rows(0, 0, x[0]);
+    }
+    __syncthreads();
+    if (WALK && n > 0) all_scores(0);
+    prepare(TC, x[0]);
+    if constexpr (WALK) __syncthreads();
+    auto next = [&](int u0, auto AT) {   // the chunk from u0 on, while the one before is walked
+      constexpr int at = decltype(AT)::value;
+      places();
+      if (DOTS && u0 > TC) put_dots(u0 - 2 * TC);
+      if (u0 < n) put_rows(u0, at, x[at % AHEAD]);
+      if constexpr (WALK) {
+        __syncthreads();
+        if (u0 < n) all_scores(at);
+      }
+      prepare(u0 + TC, x[at % AHEAD]);
+      __syncthreads();
+    };
+    for (int c = 0; c < chunks; c += 2) {
+      next((c + 1) * TC, std::integral_constant<int, 1>{});
+      if (c + 1 < chunks) next((c + 2) * TC, std::integral_constant<int, 0>{});
+    }
+    if (DOTS && chunks > 0) put_dots((chunks - 1) * TC);
+    if (!WALK && sums_here && lane == 0 && slice == 0) a.totals[int64_t(bh) * a.pieces + piece] = __builtin_amdgcn_exp2f(float(all));
+    if constexpr (DOTS)
+      if (a.ends) {
+        __syncthreads();
+        __syncthreads();
+      }
+    return;
+  }
+
+  // ---- the state and the outputs: rows 16 k + 4 g + (0..3), column c0 + 16 w + q
   f32x4 S[2 * KT];
-  const bool col = cw + q < a.V;
-  const float* start = !WALK ? nullptr : a.pieces > 1 ? a.starts + (int64_t(bh) * a.pieces + piece) * KV : a.init ? a.init + bh * KV : nullptr;
-  auto state_at = [&](int k, int i) { return int64_t(16 * k + 4 * g + i) * a.sk + int64_t(cw + q) * a.sv; };
+  const int cw = 16 * w, column = c0 + cw + q;
+  auto state_at = [&](int k, int i) { return int64_t(16 * k + 4 * g + i) * a.sk + int64_t(column) * a.sv; };
   // rows that there are among 4 g + (0..3) on (none without a column): for k, i those below
-  auto rows_of = [&] { return afresh(col ? a.K - 4 * g : 0); };
-  if (n > 0) fetch(0);
+  auto rows_of = [&] { return afresh(column < a.V ? a.K - 4 * g : 0); };
+  {
+    const float* start = !WALK ? nullptr : a.pieces > 1 ? a.starts + (int64_t(bh) * a.pieces + piece) * KV : a.init ? a.init + bh * KV : nullptr;
 #pragma unroll
-  for (int k = 0; k < 2 * KT; ++k) S[k] = f32x4{0.f, 0.f, 0.f, 0.f};
-  if (start) {   // (past the last row or column: some other, made zero)
-    const float* at = start + int64_t(col ? cw + q : 0) * a.sv;
-    const int rows = rows_of();
+    for (int k = 0; k < 2 * KT; ++k) S[k] = f32x4{0.f, 0.f, 0.f, 0.f};
+    if (start) {   // (past the last row or column: some other, made zero)
+      const float* from = start + int64_t(min(column, a.V - 1)) * a.sv;
+      const int rows = rows_of();
 #pragma unroll
-    for (int k = 0; k < 2 * KT; ++k)
+      for (int k = 0; k < 2 * KT; ++k)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) S[k][i] = at[min(16 * k + 4 * g + i, a.K - 1) * a.sk];
+        for (int i = 0; i < 4; ++i) S[k][i] = from[min(16 * k + 4 * g + i, a.K - 1) * a.sk];
 #pragma unroll
-    for (int k = 0; k < 2 * KT; ++k)
+      for (int k = 0; k < 2 * KT; ++k)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) S[k][i] = 16 * k + i < rows ? S[k][i] : 0.f;
+        for (int i = 0; i < 4; ++i) S[k][i] = 16 * k + i < rows ? S[k][i] : 0.f;
+    }
   }
-  if constexpr (WALK) {   // scores above the diagonal that a product reads
-    for (int i = t; i < NP * TC * PP; i += 256) sp[0][0][i] = T(0.f);
-  }
-  sums();
-  double all = 0.;   // of the piece
-  // this lane's first element of a chunk's outputs, and of the rows that they are multiplied with
+  // a chunk's outputs, and the rows that they are multiplied with
   const int64_t ors = way * a.out.rs, drs = way * a.dot.rs;
-  int64_t po = 0, pd = 0;
-  if constexpr (WALK) po = top * a.out.rs + (h / a.out.per) * int64_t(a.V) + cw + 4 * g + q * ors;
-  if constexpr (DOTS) pd = top * a.dot.rs + (h / a.dot.per) * int64_t(a.V) + cw + 4 * g + q * drs;
+  const int oes = a.out_f32 ? 4 : int(sizeof(T));
+  char* po = a.out.p ? a.out.p + (top * a.out.rs + (h / a.out.per) * int64_t(a.V) + (VEC && down ? (TC - 1) * ors : 0)) * oes : nullptr;
+  const T* pd = DOTS ? reinterpret_cast<const T*>(a.dot.p) + top * a.dot.rs + (h / a.dot.per) * int64_t(a.V) + (VEC && down ? (TC - 1) * drs : 0) : nullptr;
 
   // The steps of the chunk one by one, from shared memory.
-  auto one_by_one = [&](int u0, int steps) {
+  auto one_by_one = [&](int u0, int steps, int at) {
     for (int u = 0; u < steps; ++u) {
-      const float dec = __builtin_amdgcn_exp2f(slog[u]);
-      const float v = float(sv[u][16 * w + q]);
+      const float dec = __builtin_amdgcn_exp2f(slog[at][u]);
+      const int64_t row = r.row(u0 + u);
+      const float v = float(sv[at][u][cw + q]);
       float off = 0.f, y = 0.f;
       const int rows = afresh(a.K - 4 * g);
 #pragma unroll
@@ -324,125 +558,41 @@ __global__ __launch_bounds__(256, 2) void attn_chunk_kernel(AttnArgs a) {
         for (int i = 0; i < 4; ++i) {
           const int d = 16 * k + 4 * g + i;
           if (16 * k + i < rows) {
-            const float kb = float(sb[u][d]) * a.in_scale;
             S[k][i] *= dec;
-            if constexpr (WALK) off = __builtin_fmaf(float(sa[u][d]), S[k][i], off);
-            S[k][i] = __builtin_fmaf(kb, v, S[k][i]);
-            if constexpr (WALK) y = __builtin_fmaf(float(sa[u][d]), S[k][i], y);
+            if constexpr (WALK) off = __builtin_fmaf(float(sa[at][u][d]), S[k][i], off);
+            S[k][i] = __builtin_fmaf(float(sb[at][u][d]) * a.in_scale, v, S[k][i]);
+            if constexpr (WALK) y = __builtin_fmaf(float(sa[at][u][d]), S[k][i], y);
           }
         }
-      if constexpr (WALK) {
-        y += __shfl_xor(y, 16, 64);
-        y += __shfl_xor(y, 32, 64);
-        const int64_t row = r.row(u0 + u);
-        if (g == 0 && col) r.put(row, cw + q, y * a.out_scale);
-        if constexpr (DOTS) {
-          off += __shfl_xor(off, 16, 64);
-          off += __shfl_xor(off, 32, 64);
-          off = col ? off * a.out_scale * r.get(a.dot, a.V, row, cw + q) : 0.f;
+      y += __shfl_xor(y, 16, 64);
+      y += __shfl_xor(y, 32, 64);
+      if (g == 0 && column < a.V) r.put(row, column, y * a.out_scale);
+      if constexpr (DOTS) {
+        off += __shfl_xor(off, 16, 64);
+        off += __shfl_xor(off, 32, 64);
+        float dot = column < a.V ? off * a.out_scale * r.get(a.dot, a.V, row, column) : 0.f;
 #pragma unroll
-          for (int m = 1; m < 16; m *= 2) off += __shfl_xor(off, m, 64);
-          if (lane == 0) red[w][u] = off;
-        }
+        for (int m = 1; m < 16; m *= 2) dot += __shfl_xor(dot, m, 64);
+        if (lane == 0) red[w][u] = dot;
       }
     }
   };
-  auto put_dots = [&](int u0) {
-    if (t < TC && u0 + t < n)
-      a.dots[((int64_t(slice) * a.geo.B + b) * a.H + h) * a.geo.S + r.step(u0 + t)] = ((red[0][t] + red[1][t]) + red[2][t]) + red[3][t];
-  };
 
-  for (int u0 = 0; u0 < n; u0 += TC) {
-    __syncthreads();   // all are done with the chunk before
-    if (u0 + TC > n || a.K < 32 * KT || c0 + kAttnCols > a.V) {
-#pragma unroll
-      for (int i = 0; i < NK; ++i) {
-        if constexpr (WALK) keep(ra[i], u0 + tk + i * RK < n && ck < a.K);
-        keep(rb[i], u0 + tk + i * RK < n && ck < a.K);
-      }
-#pragma unroll
-      for (int i = 0; i < NV; ++i) keep(rv[i], u0 + tv + i * RV < n && c0 + cv < a.V);
-    }
-#pragma unroll
-    for (int i = 0; i < NK; ++i) {
-      if constexpr (WALK) *reinterpret_cast<Piece*>(&sa[tk + i * RK][ck]) = ra[i];
-      *reinterpret_cast<Piece*>(&sb[tk + i * RK][ck]) = rb[i];
-    }
-#pragma unroll
-    for (int i = 0; i < NV; ++i) *reinterpret_cast<Piece*>(&sv[tv + i * RV][cv]) = rv[i];
-    if (t < TC) {
-      shi[t] = float(csum);
-      slo[t] = float(csum - double(float(csum)));
-      ssince[t] = __builtin_amdgcn_exp2f(float(csum)) * a.out_scale;
-      sleft[t] = __builtin_amdgcn_exp2f(float(ctotal - csum)) * a.in_scale;
-      slog[t] = clog;
-    }
-    const float total = __builtin_amdgcn_exp2f(float(ctotal));
-    all += ctotal;
-    if (DOTS && u0 > 0) put_dots(u0 - TC);
-    __syncthreads();
-    const int steps = min(n - u0, TC);
-    if (u0 + TC < n) fetch(u0 + TC);
-
-    bool fine = true;
-    if constexpr (WALK) {
-      // the scores of steps 16 w to 16 w + 15 (this lane's: 16 w + q) by those up to them
-      if (w < IT) {
-        Op fa[KT];
-#pragma unroll
-        for (int k = 0; k < KT; ++k) fa[k] = op_run<T>(&sa[16 * w + q][32 * k + 8 * g]);
-        const int i = 16 * w + q;
-        const float hi_i = shi[i], lo_i = slo[i];
-        float p[IT][4], most = 0.f;
-#pragma unroll
-        for (int j = 0; j < IT; ++j) {
-          if (j > w) break;
-          f32x4 c = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int k = 0; k < KT; ++k) c = M::mul(op_run<T>(&sb[16 * j + q][32 * k + 8 * g]), fa[k], c);
-          const f32x4 hj = *reinterpret_cast<const f32x4*>(&shi[16 * j + 4 * g]), lj = *reinterpret_cast<const f32x4*>(&slo[16 * j + 4 * g]);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int at = 16 * j + 4 * g + k;
-            const float x = c[k] * scale * __builtin_amdgcn_exp2f((hi_i - hj[k]) + (lo_i - lj[k]));
-            if (DOTS && at == i) sdiag[i] = c[k] * scale;
-            p[j][k] = (DOTS ? at < i : at <= i) ? x : 0.f;
-            if (M::Scaled) most = fmaxf(most, __builtin_fabsf(p[j][k]));
-          }
-        }
-        Scale sc{1.f, 1.f};
-        if constexpr (M::Scaled) {
-          sc = wave_scale(most);
-          if (lane == 0) sback[w] = sc.back;
-        }
-#pragma unroll
-        for (int j = 0; j < IT; ++j) {
-          if (j > w) break;
-          float left[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) left[k] = p[j][k] * sc.by;
-#pragma unroll
-          for (int m = 0; m < NP; ++m) {
-            Pack<T, 4> x;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              x.v[k] = T(left[k]);
-              left[k] -= float(x.v[k]);
-            }
-            *reinterpret_cast<Pack<T, 4>*>(&sp[m][i][16 * j + 4 * g]) = x;
-          }
-        }
-      }
-      __syncthreads();
-    }
+  __syncthreads();
+  if constexpr (WALK) __syncthreads();
+  for (int chunk = 0; chunk < chunks; ++chunk) {
+    const int u0 = chunk * TC, at = chunk & 1, steps = min(n - u0, TC);
+    t = afresh(t);
+    lane = t & 63, q = lane & 15, g = lane >> 4;
     // v by steps: this lane's column, eight steps of each 32
     Op fv[ST];
 #pragma unroll
-    for (int s = 0; s < ST; ++s) fv[s] = op_column<T>(&sv[0][0], VP, 32 * s + 8 * g, 16 * w, q);
+    for (int s = 0; s < ST; ++s) fv[s] = op_column<T>(&sv[at][0][0], VP, 32 * s + 8 * g, cw, q);
 
+    // outputs of step 16 i + q, columns c0 + cw + 4 g + (0..3): the state's part, then the chunk's
+    f32x4 y[IT];
+    bool fine = true;
     if constexpr (WALK) {
-      // outputs of step 16 i + q, columns cw + 4 g + (0..3): the state's part, then the chunk's
-      f32x4 y[IT];
 #pragma unroll
       for (int i = 0; i < IT; ++i) y[i] = f32x4{0.f, 0.f, 0.f, 0.f};
       Scale ss{1.f, 1.f};
@@ -454,63 +604,84 @@ __global__ __launch_bounds__(256, 2) void attn_chunk_kernel(AttnArgs a) {
           for (int i = 0; i < 4; ++i) most = fmaxf(most, __builtin_fabsf(S[k][i]));
         ss = wave_scale(most);
       }
+      Op fa[2][IT];
+      auto read_a = [&](int k) {
+#pragma unroll
+        for (int i = 0; i < IT; ++i) fa[k & 1][i] = op_runs<T>(&sa[at][16 * i + q][32 * k + 4 * g], &sa[at][16 * i + q][32 * k + 16 + 4 * g]);
+      };
+      constexpr int BL = ST == 2 ? 6 : 2;   // blocks of scores: i = 0 1 2 2 3 3, s = 0 0 0 1 0 1
+      Parts<T, NP> fp[3];
+      float since[IT];
+      auto read_p = [&](int m) {
+        const int i = m < 2 ? m : (m - 2) / 2 + 2, s = m < 2 ? 0 : m & 1;
+#pragma unroll
+        for (int x = 0; x < NP; ++x) fp[m % 3].p[x] = op_run<T>(&sp[at][x][s ? i + 2 : i][q][8 * g]);
+      };
+      read_a(0);
 #pragma unroll
       for (int k = 0; k < KT; ++k) {
+        if (k + 1 < KT) {
+          read_a(k + 1);
+        } else {
+          read_p(0);
+          read_p(1);
+#pragma unroll
+          for (int i = 0; i < IT; ++i) since[i] = ssince[at][16 * i + q];
+        }
+        asked();
         float x[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[i] = S[2 * k + i / 4][i % 4] * ss.by;
         const Parts<T, NP> fs = op_parts<T, NP>(x);
 #pragma unroll
-        for (int i = 0; i < IT; ++i)
-          y[i] = mul_parts<T, NP>(fs, op_runs<T>(&sa[16 * i + q][32 * k + 4 * g], &sa[16 * i + q][32 * k + 16 + 4 * g]), y[i]);
+        for (int m = NP - 1; m >= 0; --m)
+#pragma unroll
+          for (int i = 0; i < IT; ++i) y[i] = M::mul(fs.p[m], fa[k & 1][i], y[i]);
       }
 #pragma unroll
-      for (int i = 0; i < IT; ++i) {
-        const float by = ssince[16 * i + q] * ss.back;
-        y[i] *= by;
-        f32x4 c = M::Scaled ? f32x4{0.f, 0.f, 0.f, 0.f} : y[i];
-#pragma unroll
-        for (int s = 0; s < ST; ++s) {
-          if (16 * i + 15 < 32 * s) break;
-          Parts<T, NP> fp;
-#pragma unroll
-          for (int m = 0; m < NP; ++m) fp.p[m] = op_run<T>(&sp[m][16 * i + q][32 * s + 8 * g]);
-          c = mul_parts<T, NP>(fv[s], fp, c);
-        }
+      for (int m = 0; m < BL; ++m) {
+        const int i = m < 2 ? m : (m - 2) / 2 + 2, s = m < 2 ? 0 : m & 1;
+        if (m + 2 < BL) read_p(m + 2);
+        asked();
+        if (s == 0) y[i] *= since[i] * ss.back;
         if constexpr (M::Scaled) {
-          const float back = sback[i];
+          const f32x4 c = mul_parts<T, NP>(fv[s], fp[m % 3], f32x4{0.f, 0.f, 0.f, 0.f});
+          const float back = sback[at][s ? i + 2 : i];
 #pragma unroll
           for (int k = 0; k < 4; ++k) y[i][k] = __builtin_fmaf(c[k], back, y[i][k]);
         } else {
-          y[i] = c;
+          y[i] = mul_parts<T, NP>(fv[s], fp[m % 3], y[i]);
         }
       }
-      float dots[IT];
+      __syncthreads();   // (the next chunk's rows are there)
       if constexpr (DOTS) {
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
-          const int u = 16 * i + q, c = cw + 4 * g;
+          const int u = 16 * i + q, c = c0 + cw + 4 * g;
+          const float by = sdiag[at][u];
           float d[4] = {};
           if (u < steps) {
-            const T* at = reinterpret_cast<const T*>(a.dot.p) + pd + i * 16 * drs;
-            if (VEC && c < a.V) {
-              const Pack<T, 4> x = *reinterpret_cast<const Pack<T, 4>*>(at);
+            if constexpr (VEC) {
+              const uint32_t off = uint32_t(place(u)) * uint32_t(down ? -drs : drs) + uint32_t(c < a.V ? c : 0);
+              const Pack<T, 4> x = *reinterpret_cast<const Pack<T, 4>*>(reinterpret_cast<const char*>(pd) + off * uint32_t(sizeof(T)));
 #pragma unroll
               for (int k = 0; k < 4; ++k) d[k] = float(x.v[k]);
             } else {
 #pragma unroll
               for (int k = 0; k < 4; ++k)
-                if (c + k < a.V) d[k] = float(at[k]);
+                if (c + k < a.V) d[k] = float(pd[u * drs + c + k]);
             }
           }
-          const Pack<T, 4> own = *reinterpret_cast<const Pack<T, 4>*>(&sv[u][16 * w + 4 * g]);
-          const float by = sdiag[u];
-          dots[i] = 0.f;
+          const Pack<T, 4> own = *reinterpret_cast<const Pack<T, 4>*>(&sv[at][u][cw + 4 * g]);
+          float dot = 0.f;
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            if (c + k < a.V) dots[i] = __builtin_fmaf(y[i][k], d[k], dots[i]);
+            if (c + k < a.V) dot = __builtin_fmaf(y[i][k], d[k], dot);
             y[i][k] = __builtin_fmaf(by, float(own.v[k]), y[i][k]);
           }
+          dot += __shfl_xor(dot, 16, 64);
+          dot += __shfl_xor(dot, 32, 64);
+          if (g == 0) red[w][u] = dot;
         }
       }
       float zero = 0.f;   // (not so once anything is not finite)
@@ -519,52 +690,59 @@ __global__ __launch_bounds__(256, 2) void attn_chunk_kernel(AttnArgs a) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) zero = __builtin_fmaf(y[i][k], 0.f, zero);
       fine = __builtin_amdgcn_ballot_w64(zero != 0.f) == 0;
-      if (fine) {
+    }
+    if (__builtin_expect(fine, 1)) {
+      // the state after the chunk; the outputs on their way between
+      const float total = stotal[at];
+      f32x4 left[2 * ST];
+#pragma unroll
+      for (int s = 0; s < ST; ++s)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) left[2 * s + i] = *reinterpret_cast<const f32x4*>(&sleft[at][32 * s + 8 * g + 4 * i]);
+      Op fb[2][2][ST];   // of two sixteens of rows, while the two before are multiplied
+      auto read_b = [&](int k) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int s = 0; s < ST; ++s) fb[k & 1][j][s] = op_column<T>(&sb[at][0][0], KP, 32 * s + 8 * g, 32 * k + 16 * j, q);
+      };
+      read_b(0);
+      asked();
+      if constexpr (WALK) {
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
-          const int u = 16 * i + q, c = cw + 4 * g;
-          if (a.out.p && u < steps && c < a.V) {
-            const int64_t at = po + i * 16 * ors;
-            if (a.out_f32) {
-              float* o = reinterpret_cast<float*>(a.out.p) + at;
+          const int u = 16 * i + q, c = c0 + cw + 4 * g;
+          if (po && u < steps && c < a.V) {
+            if constexpr (VEC) {   // (whole pieces of four columns)
+              char* to = po + (uint32_t(place(u)) * uint32_t(down ? -ors : ors) + uint32_t(c)) * uint32_t(oes);
+              if (a.out_f32) {
+                *reinterpret_cast<f32x4*>(to) = y[i];
+              } else {
+                Pack<T, 4> x;
 #pragma unroll
-              for (int k = 0; k < 4; ++k)
-                if (c + k < a.V) o[k] = y[i][k];
-            } else if (VEC) {
-              Pack<T, 4> x;
-#pragma unroll
-              for (int k = 0; k < 4; ++k) x.v[k] = T(y[i][k]);
-              *reinterpret_cast<Pack<T, 4>*>(reinterpret_cast<T*>(a.out.p) + at) = x;
+                for (int k = 0; k < 4; ++k) x.v[k] = T(y[i][k]);
+                *reinterpret_cast<Pack<T, 4>*>(to) = x;
+              }
             } else {
-              T* o = reinterpret_cast<T*>(a.out.p) + at;
 #pragma unroll
               for (int k = 0; k < 4; ++k)
-                if (c + k < a.V) o[k] = T(y[i][k]);
+                if (c + k < a.V) {
+                  char* to = po + (u * ors + c + k) * oes;
+                  if (a.out_f32) *reinterpret_cast<float*>(to) = y[i][k];
+                  else *reinterpret_cast<T*>(to) = T(y[i][k]);
+                }
             }
           }
-          if constexpr (DOTS) {
-            dots[i] += __shfl_xor(dots[i], 16, 64);
-            dots[i] += __shfl_xor(dots[i], 32, 64);
-            if (g == 0) red[w][u] = dots[i];
-          }
         }
-      } else {
-        one_by_one(u0, steps);
       }
-    }
-    if (fine) {
-      // the state after the chunk
-      float x[ST][8];
-      float most = 0.f;
+      float x[ST][8], most = 0.f;
 #pragma unroll
-      for (int s = 0; s < ST; ++s) {
-        const f32x4 l0 = *reinterpret_cast<const f32x4*>(&sleft[32 * s + 8 * g]), l1 = *reinterpret_cast<const f32x4*>(&sleft[32 * s + 8 * g + 4]);
+      for (int s = 0; s < ST; ++s)
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          x[s][i] = float(fv[s][i]) * (i < 4 ? l0[i] : l1[i - 4]);
+          x[s][i] = float(fv[s][i]) * left[2 * s + i / 4][i % 4];
           if (M::Scaled) most = fmaxf(most, __builtin_fabsf(x[s][i]));
         }
-      }
       Scale sc{1.f, 1.f};
       if constexpr (M::Scaled) {
         sc = wave_scale(most);
@@ -577,21 +755,34 @@ __global__ __launch_bounds__(256, 2) void attn_chunk_kernel(AttnArgs a) {
 #pragma unroll
       for (int s = 0; s < ST; ++s) fx[s] = op_parts<T, NU>(x[s]);
 #pragma unroll
-      for (int k = 0; k < 2 * KT; ++k) {
-        f32x4 c = M::Scaled ? f32x4{0.f, 0.f, 0.f, 0.f} : S[k] * total;
+      for (int k = 0; k < KT; ++k) {
+        if (k + 1 < KT) read_b(k + 1);
+        asked();
+        f32x4 c[2];
 #pragma unroll
-        for (int s = 0; s < ST; ++s) c = mul_parts<T, NU>(op_column<T>(&sb[0][0], KP, 32 * s + 8 * g, 16 * k, q), fx[s], c);
-        if constexpr (M::Scaled) {
+        for (int j = 0; j < 2; ++j) c[j] = M::Scaled ? f32x4{0.f, 0.f, 0.f, 0.f} : S[2 * k + j] * total;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) S[k][i] = __builtin_fmaf(S[k][i], total, c[i] * sc.back);
-        } else {
-          S[k] = c;
+        for (int s = 0; s < ST; ++s)
+#pragma unroll
+          for (int m = NU - 1; m >= 0; --m)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) c[j] = M::mul(fb[k & 1][j][s], fx[s].p[m], c[j]);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          if constexpr (M::Scaled) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) S[2 * k + j][i] = __builtin_fmaf(S[2 * k + j][i], total, c[j][i] * sc.back);
+          } else {
+            S[2 * k + j] = c[j];
+          }
         }
       }
+    } else {
+      one_by_one(u0, steps, at);
     }
-    if (u0 + TC < n) sums();
-    po += TC * ors;
-    pd += TC * drs;
+    if (po) po += TC * ors * oes;
+    if constexpr (DOTS) pd += TC * drs;
+    __syncthreads();   // (the next chunk's scores are there, this one's rows are done with)
   }
   if constexpr (!WALK) {
     // (what the products make of values that are not finite, the steps decide)
@@ -605,7 +796,7 @@ __global__ __launch_bounds__(256, 2) void attn_chunk_kernel(AttnArgs a) {
       for (int k = 0; k < 2 * KT; ++k) S[k] = f32x4{0.f, 0.f, 0.f, 0.f};
       for (int u = 0; u < n; ++u) {
         const int64_t row = r.row(u);
-        const float dec = __builtin_amdgcn_exp2f(r.log_decay(u) * kLog2e), v = col ? r.get(a.v, a.V, row, cw + q) : 0.f;
+        const float dec = __builtin_amdgcn_exp2f(r.log_decay(u) * kLog2e), v = column < a.V ? r.get(a.v, a.V, row, column) : 0.f;
         const int rows = afresh(a.K - 4 * g);
 #pragma unroll
         for (int k = 0; k < 2 * KT; ++k)
@@ -621,7 +812,6 @@ __global__ __launch_bounds__(256, 2) void attn_chunk_kernel(AttnArgs a) {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         if (16 * k + i < rows) to[state_at(k, i)] = S[k][i];
-    if (t == 0 && slice == 0) a.totals[int64_t(bh) * a.pieces + piece] = __builtin_amdgcn_exp2f(float(all));
     return;
   }
   if (a.fin && (a.back ? piece == 0 : lo < L ? hi == L : piece == 0 && L == 0)) {
@@ -634,9 +824,7 @@ __global__ __launch_bounds__(256, 2) void attn_chunk_kernel(AttnArgs a) {
       for (int i = 0; i < 4; ++i)
         if (16 * k + i < rows) to[state_at(k, i)] = S[k][i] * by;
   }
-  if constexpr (DOTS) {
-    __syncthreads();
-    if (n > 0) put_dots((n - 1) / TC * TC);
+  if constexpr (DOTS)
     if (a.ends) {   // the state after the piece by the gradient of the one before the next
       float d = 0.f;
       const float* other = a.others ? a.others + (int64_t(bh) * a.pieces + piece) * KV : a.other ? a.other + bh * KV : nullptr;
@@ -648,14 +836,13 @@ __global__ __launch_bounds__(256, 2) void attn_chunk_kernel(AttnArgs a) {
           if (16 * k + i < rows) d = __builtin_fmaf(S[k][i], other[state_at(k, i)], d);
 #pragma unroll
       for (int m = 1; m < 64; m *= 2) d += __shfl_xor(d, m, 64);
-      __syncthreads();
+      __syncthreads();   // (the last chunk's sums are read)
       if (lane == 0) red[w][0] = d;
       __syncthreads();
       const float by = hi > 0 && hi < L ? __builtin_amdgcn_exp2f(r.log_decay_at(hi) * kLog2e) : 1.f;
       if (t == 0)
         a.ends[(int64_t(slice) * a.geo.B * a.H + bh) * a.pieces + piece] = by * (((red[0][0] + red[1][0]) + red[2][0]) + red[3][0]);
     }
-  }
   // steps that the row does not take
   if (a.out.p)
     for (int s = max(lo, L) + w; s < end; s += 4)
@@ -665,20 +852,21 @@ __global__ __launch_bounds__(256, 2) void attn_chunk_kernel(AttnArgs a) {
 template <typename T, int MODE, bool VEC>
 hipError_t attn_chunks_of(const AttnArgs& a, hipStream_t s) {
   const int64_t blocks = int64_t(a.geo.B) * a.H * ((a.V + kAttnCols - 1) / kAttnCols) * (MODE == kAttnLocal ? a.pieces - 1 : a.pieces);
-  if (a.K <= 32) return go(attn_chunk_kernel<T, 1, MODE, VEC>, blocks, 256, a, s);
-  if (a.K <= 64) return go(attn_chunk_kernel<T, 2, MODE, VEC>, blocks, 256, a, s);
-  if (a.K <= 128) return go(attn_chunk_kernel<T, 4, MODE, VEC>, blocks, 256, a, s);
-  return go(attn_chunk_kernel<T, 8, MODE, VEC>, blocks, 256, a, s);
+  if (a.K <= 32) return go(attn_chunk_kernel<T, 1, MODE, VEC>, blocks, 512, a, s);
+  if (a.K <= 64) return go(attn_chunk_kernel<T, 2, MODE, VEC>, blocks, 512, a, s);
+  if (a.K <= 128) return go(attn_chunk_kernel<T, 4, MODE, VEC>, blocks, 512, a, s);
+  return go(attn_chunk_kernel<T, 8, MODE, VEC>, blocks, 512, a, s);
 }
 
 template <typename T>
 hipError_t attn_chunks(const AttnArgs& a, bool local, hipStream_t s) {
-  const auto whole = [](const HeadRows& x, int size) {
-    return reinterpret_cast<uintptr_t>(x.p) % 16 == 0 && x.rs * sizeof(T) % 16 == 0 && size * sizeof(T) % 16 == 0;
+  // rows in whole aligned pieces, a chunk's within 2^31 bytes (2^25 a step)
+  const auto whole = [&](const HeadRows& x, int size, size_t es) {
+    return reinterpret_cast<uintptr_t>(x.p) % 16 == 0 && x.rs * es % 16 == 0 && size * sizeof(T) % 16 == 0 &&
+           x.rs * es <= (size_t(1) << 25) / (a.geo.layout ? 1 : a.geo.B);
   };
-  // (outputs of 32 bits are stored one by one)
-  const bool vec = whole(a.b, a.K) && whole(a.v, a.V) && (local || whole(a.a, a.K)) && (!a.dots || whole(a.dot, a.V)) &&
-                   (local || !a.out.p || a.out_f32 || whole(a.out, a.V));
+  const bool vec = whole(a.b, a.K, sizeof(T)) && whole(a.v, a.V, sizeof(T)) && (local || whole(a.a, a.K, sizeof(T))) &&
+                   (!a.dots || whole(a.dot, a.V, sizeof(T))) && (local || !a.out.p || whole(a.out, a.V, a.out_f32 ? 4 : sizeof(T)));
   if (local) return vec ? attn_chunks_of<T, kAttnLocal, true>(a, s) : attn_chunks_of<T, kAttnLocal, false>(a, s);
   if (a.dots) return vec ? attn_chunks_of<T, kAttnDots, true>(a, s) : attn_chunks_of<T, kAttnDots, false>(a, s);
   return vec ? attn_chunks_of<T, kAttnWalk, true>(a, s) : attn_chunks_of<T, kAttnWalk, false>(a, s);

@@ -25,10 +25,10 @@ struct AttnSteps {
       : a(a), h(h), L(L), lo(lo), hi(hi), r(step_rows(a.geo, b, L)), fixed(a.decay ? a.decay[h] : 0.f) {}
   __device__ __forceinline__ int step(int u) const { return a.back ? hi - 1 - u : lo + u; }
   __device__ __forceinline__ int64_t row(int u) const { return r.base + step(u) * r.step; }
-  __device__ __forceinline__ float log_decay_at(int s) const {
-    const float g = a.G.p ? reinterpret_cast<const float*>(a.G.p)[(r.base + s * r.step) * a.G.rs + h] : 0.f;
-    return attn_log_decay(g + fixed);
+  __device__ __forceinline__ float raw_decay(int s) const {
+    return reinterpret_cast<const float*>(a.G.p)[(r.base + s * r.step) * a.G.rs + h];
   }
+  __device__ __forceinline__ float log_decay_at(int s) const { return attn_log_decay((a.G.p ? raw_decay(s) : 0.f) + fixed); }
   // From the step before in the walk's order: the later one's of the two, and
   // none before the last step of all.
   __device__ __forceinline__ float log_decay(int u) const {
