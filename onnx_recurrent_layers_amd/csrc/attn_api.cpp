@@ -156,9 +156,11 @@ extern "C" int rnn_attn_create(const rnn_attn_desc* desc, rnn_attn** out) {
   const int64_t heads = d.batch * d.heads, blocks = heads * std::max(p.key_cols, p.value_cols);   // (below 2^57)
   p.f = attn_plan(d, p.tokens, heads * p.value_cols, d.seq + 64);
   p.b = attn_plan(d, p.tokens, heads * std::min(p.key_cols, p.value_cols), d.seq + 64);
-  // (the decays' gradient is summed back from a piece's end: pieces of 512 steps
-  // keep what the sums lose small next to it)
-  p.bd = attn_plan(d, p.tokens, heads * std::min(p.key_cols, p.value_cols), 512);
+  // (the decays' gradient is summed back from a piece's end, and what the sums lose
+  // grows with it: 2 x 2048 steps, 8 heads of 128 x 128, bf16, dG off by 3.3e-7 of its
+  // norm with pieces of 256, 8.1e-7 of 1024, 1.3e-6 of 2048; f32, d_decay 6.2e-7,
+  // 1.3e-6, 3.1e-6)
+  p.bd = attn_plan(d, p.tokens, heads * std::min(p.key_cols, p.value_cols), 1024);
   const int64_t pieces = std::max(std::max(p.f.pieces, p.b.pieces), p.bd.pieces);
   if (bytes_of({blocks, pieces, 512}) < 0 || blocks * pieces * 512 > kMaxThreads || heads * ceil_div(d.key * d.value, 256) * 256 > kMaxThreads)
     return fail(RNN_ERR_UNSUPPORTED, kAttn, "batch x heads: too large for one launch");

@@ -44,13 +44,17 @@ typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
 typedef short i16x4 __attribute__((ext_vector_type(4)));
 
 // Operands of a 32-deep product, 8 values a lane: Coarse parts of a score or a
-// state, Fine ones of what is summed on.
+// state, Fine ones of what is summed on.  Values between rows in shared memory, 16
+// bits (clocks that a wave's read takes the memory, measured): b's and the scores'
+// rows, read 16 bytes a lane, a multiple of 32 and 16 (4; with 8: 8; 32), a's,
+// read in runs of 8 bytes, and 4 (4; with 8: 8, with 16: 16), v's, and b's too, by
+// the transposing reads, and 8 or 16 (4; none: 16).
 template <typename T>
 struct Mma;
 
 template <>
 struct Mma<bf16_t> {
-  static constexpr int Coarse = 2, Fine = 3, Vec = 8, Pad = 8;
+  static constexpr int Coarse = 2, Fine = 3, Vec = 8, PadA = 4, PadB = 16, PadV = 8;
   static constexpr bool Scaled = false;
   typedef bf16x8 Op;
   typedef bf16x4 Half;
@@ -61,7 +65,7 @@ struct Mma<bf16_t> {
 };
 template <>
 struct Mma<f16_t> {
-  static constexpr int Coarse = 2, Fine = 2, Vec = 8, Pad = 8;
+  static constexpr int Coarse = 2, Fine = 2, Vec = 8, PadA = 4, PadB = 16, PadV = 8;
   static constexpr bool Scaled = true;
   typedef f16x8 Op;
   typedef f16x4 Half;
@@ -76,7 +80,7 @@ struct f32x8 {
 };
 template <>
 struct Mma<float> {
-  static constexpr int Coarse = 1, Fine = 1, Vec = 4, Pad = 4;
+  static constexpr int Coarse = 1, Fine = 1, Vec = 4, PadA = 4, PadB = 4, PadV = 4;
   static constexpr bool Scaled = false;
   typedef f32x8 Op;
   static __device__ __forceinline__ f32x4 mul(const Op& a, const Op& b, f32x4 c) {
@@ -224,6 +228,18 @@ __device__ __forceinline__ int afresh(int x) {
 // its use, and every product waits for one.)
 __device__ __forceinline__ void asked() { __builtin_amdgcn_sched_barrier(0); }
 
+// The instructions up to the next such mark in the order of N times one product and
+// V vector instructions (a product takes the matrix unit four times as long as
+// its issue: the vector instructions between cost nothing).
+template <int N, int V>
+__device__ __forceinline__ void between_products() {
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+    __builtin_amdgcn_sched_group_barrier(0x2, V, 0);
+  }
+}
+
 enum { kAttnLocal, kAttnWalk, kAttnDots };
 
 // KT: 32-wide pieces of a and b.  MODE: the state that a piece of the time axis
@@ -236,21 +252,21 @@ __global__ __launch_bounds__(512, 2) void attn_chunk_kernel(AttnArgs a) {
   constexpr bool WALK = MODE != kAttnLocal, DOTS = MODE == kAttnDots;
   constexpr int TC = KT * int(sizeof(T)) >= 16 ? 32 : 64, IT = TC / 16, ST = TC / 32;    // steps of a chunk, in 16s and 32s
   constexpr int COLS = kAttnCols;                                                        // of a workgroup
-  constexpr int KP = 32 * KT + M::Pad, VP = COLS + M::Pad, PP = 32 + M::Pad, PB = ST == 2 ? 6 : 2;
+  constexpr int KA = 32 * KT + M::PadA, KB = 32 * KT + M::PadB, VP = COLS + M::PadV, PP = 32 + M::PadB, PB = ST == 2 ? 6 : 2;
   constexpr int NP = DOTS ? M::Fine : M::Coarse, NU = M::Fine;
   constexpr int CK = 32 * KT / M::Vec, CV = COLS / M::Vec;                               // 16-byte pieces of a row
   constexpr int RK = 256 / CK, RV = 256 / CV;                                            // rows that the threads take at once
   constexpr int NK = (TC + RK - 1) / RK, NV = (TC + RV - 1) / RV;                        // pieces of a thread
   constexpr int AHEAD = sizeof(T) == 4 && KT >= 4 ? 1 : 2;   // (wide rows of f32 fill the registers)
   // two chunks' rows, sums and scores
-  __shared__ alignas(16) T sa[2][WALK ? TC : 1][KP];
-  __shared__ alignas(16) T sb[2][TC][KP];
+  __shared__ alignas(16) T sa[2][WALK ? TC : 1][KA];
+  __shared__ alignas(16) T sb[2][TC][KB];
   __shared__ alignas(16) T sv[2][TC][VP];
   // scores, 16 steps by 32: those of the first 32 steps for all, those of the next for the last 32
   __shared__ alignas(16) T sp[2][WALK ? NP : 1][WALK ? PB : 1][16][PP];
   __shared__ alignas(16) float shi[2][TC], slo[2][TC], ssince[2][TC], sleft[2][TC], slog[2][TC], sdiag[2][TC], sback[2][8], stotal[2], red[4][TC];
   const int w = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
-  int t = int(threadIdx.x), lane = t & 63, q = lane & 15, g = lane >> 4;
+  const int t = int(threadIdx.x) & 255, lane = t & 63, q = lane & 15, g = lane >> 4;
   const int slices = (a.V + COLS - 1) / COLS, pieces = WALK ? a.pieces : a.pieces - 1;
   // a die's workgroups (they go to eight in turn) are neighbours: a head's slices share its a and b there
   const int per_die = int(gridDim.x) / 8, rest = int(gridDim.x) % 8, die = int(blockIdx.x) % 8;
@@ -272,19 +288,14 @@ __global__ __launch_bounds__(512, 2) void attn_chunk_kernel(AttnArgs a) {
 
   if (w >= 4) {
     // ---- rows into shared memory, and the scores
-    t -= 256;
+    __builtin_amdgcn_s_setprio(1);   // (they are few instructions that all waves wait for)
     // The rows of AHEAD chunks, in registers until their place is free (with one
     // chunk's the loads come late).  A thread's rows of a tensor are RK (RV) apart;
     // past the last one it repeats that, and what it got is made zero on the way to
     // shared memory.  VEC: a chunk's lowest row is
     // at a uniform address, a thread's own at an offset of 32 bits.
     typedef Pack<T, M::Vec> Piece;
-    int tk, ck, tv, cv;
-    auto places = [&] {   // (made in each chunk: kept, they take more registers than there are)
-      t = afresh(t);
-      lane = t & 63, q = lane & 15, g = lane >> 4;
-      tk = t / CK, ck = t % CK * M::Vec, tv = t / CV, cv = t % CV * M::Vec;
-    };
+    const int tk = t / CK, ck = t % CK * M::Vec, tv = t / CV, cv = t % CV * M::Vec;
     struct Walker {
       const T* p;     // of the head, the chunk's lowest row (VEC), or its first
       int64_t rs;     // elements from a step to the next
@@ -355,6 +366,15 @@ __global__ __launch_bounds__(512, 2) void attn_chunk_kernel(AttnArgs a) {
       ctotal = __builtin_amdgcn_exp2f(float(whole));
       all += whole;
     };
+    // (a's rows of 16 bits begin at eight bytes)
+    auto put_a = [&](T* to, const Piece& p) {
+      if constexpr (sizeof(T) == 4) {
+        *reinterpret_cast<Piece*>(to) = p;
+      } else {
+        *reinterpret_cast<Pack<T, 4>*>(to) = Pack<T, 4>{{p.v[0], p.v[1], p.v[2], p.v[3]}};
+        *reinterpret_cast<Pack<T, 4>*>(to + 4) = Pack<T, 4>{{p.v[4], p.v[5], p.v[6], p.v[7]}};
+      }
+    };
     // what was fetched, of the steps from u0 on, and b and v of AHEAD chunks later asked for
     auto put_rows = [&](int u0, int at, Rows& x) {
       if (u0 + TC > n || a.K < 32 * KT || c0 + COLS > a.V) {
@@ -369,7 +389,7 @@ __global__ __launch_bounds__(512, 2) void attn_chunk_kernel(AttnArgs a) {
 #pragma unroll
       for (int i = 0; i < NK; ++i) {
         if (TC % RK && tk + i * RK >= TC) break;   // (more threads than pieces)
-        if constexpr (WALK) *reinterpret_cast<Piece*>(&sa[at][tk + i * RK][ck]) = x.a[i];
+        if constexpr (WALK) put_a(&sa[at][tk + i * RK][ck], x.a[i]);
         *reinterpret_cast<Piece*>(&sb[at][tk + i * RK][ck]) = x.b[i];
       }
 #pragma unroll
@@ -405,7 +425,7 @@ __global__ __launch_bounds__(512, 2) void attn_chunk_kernel(AttnArgs a) {
       Op fa[KT], fb[2][KT];
       f32x4 hj[2], lj[2];
 #pragma unroll
-      for (int k = 0; k < KT; ++k) fa[k] = op_run<T>(&sa[at][i][32 * k + 8 * g]);
+      for (int k = 0; k < KT; ++k) fa[k] = op_runs<T>(&sa[at][i][32 * k + 8 * g], &sa[at][i][32 * k + 8 * g + 4]);
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
 #pragma unroll
@@ -422,15 +442,25 @@ __global__ __launch_bounds__(512, 2) void attn_chunk_kernel(AttnArgs a) {
         for (int j = 0; j < 2; ++j) c[j] = M::mul(fb[j][k], fa[k], c[j]);
       float p[2][4], most = 0.f, own = 0.f;
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
+      for (int j = 0; j < 2; ++j) {
+        if (j0 + 16 * j > 16 * it) {   // (past the diagonal)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int to = i - (j0 + 16 * j + 4 * g + k);   // steps from one to the other
-          const float x = c[j][k] * (scale * __builtin_amdgcn_exp2f((hi_i - hj[j][k]) + (lo_i - lj[j][k])));
-          if (DOTS) own = to == 0 ? c[j][k] * scale : own;
-          p[j][k] = to >= (DOTS ? 1 : 0) ? x : 0.f;
-          if constexpr (M::Scaled) most = fmaxf(most, __builtin_fabsf(p[j][k]));
+          for (int k = 0; k < 4; ++k) p[j][k] = 0.f;
+        } else {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) p[j][k] = c[j][k] * (scale * __builtin_amdgcn_exp2f((hi_i - hj[j][k]) + (lo_i - lj[j][k])));
+          if (j0 + 16 * j == 16 * it)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int to = q - (4 * g + k);   // steps from one to the other
+              if (DOTS) own = to == 0 ? c[j][k] * scale : own;
+              p[j][k] = to >= (DOTS ? 1 : 0) ? p[j][k] : 0.f;
+            }
+          if constexpr (M::Scaled)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) most = fmaxf(most, __builtin_fabsf(p[j][k]));
         }
+      }
       Scale sc{1.f, 1.f};
       if constexpr (M::Scaled) {
         sc = wave_scale(most);
@@ -470,7 +500,6 @@ __global__ __launch_bounds__(512, 2) void attn_chunk_kernel(AttnArgs a) {
       a.dots[((int64_t(slice) * a.geo.B + b) * a.H + h) * a.geo.S + r.step(u0 + t)] = ((red[0][t] + red[1][t]) + red[2][t]) + red[3][t];
     };
 
-    places();
     if (n > 0) {
       if (sums_here) ask(0);
       fetch_bv(0, x[0]);
@@ -491,7 +520,6 @@ __global__ __launch_bounds__(512, 2) void attn_chunk_kernel(AttnArgs a) {
     if constexpr (WALK) __syncthreads();
     auto next = [&](int u0, auto AT) {   // the chunk from u0 on, while the one before is walked
       constexpr int at = decltype(AT)::value;
-      places();
       if (DOTS && u0 > TC) put_dots(u0 - 2 * TC);
       if (u0 < n) put_rows(u0, at, x[at % AHEAD]);
       if constexpr (WALK) {
@@ -582,8 +610,6 @@ __global__ __launch_bounds__(512, 2) void attn_chunk_kernel(AttnArgs a) {
   if constexpr (WALK) __syncthreads();
   for (int chunk = 0; chunk < chunks; ++chunk) {
     const int u0 = chunk * TC, at = chunk & 1, steps = min(n - u0, TC);
-    t = afresh(t);
-    lane = t & 63, q = lane & 15, g = lane >> 4;
     // v by steps: this lane's column, eight steps of each 32
     Op fv[ST];
 #pragma unroll
@@ -617,7 +643,14 @@ __global__ __launch_bounds__(512, 2) void attn_chunk_kernel(AttnArgs a) {
 #pragma unroll
         for (int x = 0; x < NP; ++x) fp[m % 3].p[x] = op_run<T>(&sp[at][x][s ? i + 2 : i][q][8 * g]);
       };
+      auto state_parts = [&](int k) {
+        float x[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = S[2 * k + i / 4][i % 4] * ss.by;
+        return op_parts<T, NP>(x);
+      };
       read_a(0);
+      Parts<T, NP> fs = state_parts(0);
 #pragma unroll
       for (int k = 0; k < KT; ++k) {
         if (k + 1 < KT) {
@@ -629,14 +662,13 @@ __global__ __launch_bounds__(512, 2) void attn_chunk_kernel(AttnArgs a) {
           for (int i = 0; i < IT; ++i) since[i] = ssince[at][16 * i + q];
         }
         asked();
-        float x[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = S[2 * k + i / 4][i % 4] * ss.by;
-        const Parts<T, NP> fs = op_parts<T, NP>(x);
 #pragma unroll
         for (int m = NP - 1; m >= 0; --m)
 #pragma unroll
           for (int i = 0; i < IT; ++i) y[i] = M::mul(fs.p[m], fa[k & 1][i], y[i]);
+        if (k + 1 < KT) fs = state_parts(k + 1);
+        if constexpr (sizeof(T) == 2) between_products<NP * IT, 3>();
+        asked();
       }
 #pragma unroll
       for (int m = 0; m < BL; ++m) {
@@ -699,12 +731,13 @@ __global__ __launch_bounds__(512, 2) void attn_chunk_kernel(AttnArgs a) {
       for (int s = 0; s < ST; ++s)
 #pragma unroll
         for (int i = 0; i < 2; ++i) left[2 * s + i] = *reinterpret_cast<const f32x4*>(&sleft[at][32 * s + 8 * g + 4 * i]);
-      Op fb[2][2][ST];   // of two sixteens of rows, while the two before are multiplied
+      constexpr int J = KT >= 4 && sizeof(T) == 2 ? 4 : 2;   // sixteens of rows multiplied at once
+      Op fb[2][J][ST];   // theirs, while those before are multiplied
       auto read_b = [&](int k) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+        for (int j = 0; j < J; ++j)
 #pragma unroll
-          for (int s = 0; s < ST; ++s) fb[k & 1][j][s] = op_column<T>(&sb[at][0][0], KP, 32 * s + 8 * g, 32 * k + 16 * j, q);
+          for (int s = 0; s < ST; ++s) fb[k & 1][j][s] = op_column<T>(&sb[at][0][0], KB, 32 * s + 8 * g, 16 * (J * k + j), q);
       };
       read_b(0);
       asked();
@@ -735,45 +768,50 @@ __global__ __launch_bounds__(512, 2) void attn_chunk_kernel(AttnArgs a) {
           }
         }
       }
-      float x[ST][8], most = 0.f;
-#pragma unroll
-      for (int s = 0; s < ST; ++s)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          x[s][i] = float(fv[s][i]) * left[2 * s + i / 4][i % 4];
-          if (M::Scaled) most = fmaxf(most, __builtin_fabsf(x[s][i]));
-        }
       Scale sc{1.f, 1.f};
+      auto value = [&](int s, int i) { return float(fv[s][i]) * left[2 * s + i / 4][i % 4]; };
       if constexpr (M::Scaled) {
+        float most = 0.f;
+#pragma unroll
+        for (int s = 0; s < ST; ++s)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) most = fmaxf(most, __builtin_fabsf(value(s, i)));
         sc = wave_scale(most);
-#pragma unroll
-        for (int s = 0; s < ST; ++s)
-#pragma unroll
-          for (int i = 0; i < 8; ++i) x[s][i] *= sc.by;
       }
+      auto value_parts = [&](int s) {
+        float x[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = value(s, i) * sc.by;
+        return op_parts<T, NU>(x);
+      };
       Parts<T, NU> fx[ST];
+      fx[0] = value_parts(0);
 #pragma unroll
-      for (int s = 0; s < ST; ++s) fx[s] = op_parts<T, NU>(x[s]);
-#pragma unroll
-      for (int k = 0; k < KT; ++k) {
-        if (k + 1 < KT) read_b(k + 1);
+      for (int k = 0; k < 2 * KT / J; ++k) {
+        if (k + 1 < 2 * KT / J) read_b(k + 1);
         asked();
-        f32x4 c[2];
+        f32x4 c[J];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) c[j] = M::Scaled ? f32x4{0.f, 0.f, 0.f, 0.f} : S[2 * k + j] * total;
+        for (int j = 0; j < J; ++j) c[j] = M::Scaled ? f32x4{0.f, 0.f, 0.f, 0.f} : S[J * k + j] * total;
 #pragma unroll
-        for (int s = 0; s < ST; ++s)
+        for (int s = 0; s < ST; ++s) {
 #pragma unroll
           for (int m = NU - 1; m >= 0; --m)
 #pragma unroll
-            for (int j = 0; j < 2; ++j) c[j] = M::mul(fb[k & 1][j][s], fx[s].p[m], c[j]);
+            for (int j = 0; j < J; ++j) c[j] = M::mul(fb[k & 1][j][s], fx[s].p[m], c[j]);
+          if (ST == 2 && s == 0 && k == 0) {
+            fx[ST - 1] = value_parts(ST - 1);
+            if constexpr (sizeof(T) == 2) between_products<NU * J, 4>();
+            asked();
+          }
+        }
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
+        for (int j = 0; j < J; ++j) {
           if constexpr (M::Scaled) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) S[2 * k + j][i] = __builtin_fmaf(S[2 * k + j][i], total, c[j][i] * sc.back);
+            for (int i = 0; i < 4; ++i) S[J * k + j][i] = __builtin_fmaf(S[J * k + j][i], total, c[j][i] * sc.back);
           } else {
-            S[2 * k + j] = c[j];
+            S[J * k + j] = c[j];
           }
         }
       }
