@@ -327,7 +327,7 @@ void rotary_lay(const rnn_rotary& p, bool vec, RotaryArgs& a) {
   a.lph = 1;
   while (a.lph < 64 && a.lph < a.units) a.lph *= 2;
   const int64_t heads = d.q_heads + d.k_heads, rounds = ceil_div(heads, 64 / a.lph);
-  a.splits = int(d.rows >= 4096 ? 1 : std::min<int64_t>(rounds, ceil_div(4096, std::max<int64_t>(d.rows, 1))));
+  a.splits = int(std::min<int64_t>(rounds, ceil_div(4 * kRotaryBlocks, std::max<int64_t>(d.rows, 1))));
   a.take = int(ceil_div(rounds, a.splits) * (64 / a.lph));
   a.splits = int(ceil_div(heads, a.take));
 }
@@ -388,7 +388,7 @@ extern "C" int rnn_rotary_create(const rnn_rotary_desc* desc, rnn_rotary** out) 
   if (bytes_of({d.rows, std::max(d.q_heads, d.k_heads), d.size, p.es}) < 0) return fail(RNN_ERR_SHAPE, kRotary, "Q: size overflows");
   RotaryArgs a{};
   rotary_lay(p, false, a);
-  p.parts = std::max<int64_t>(1, std::min<int64_t>(1024, ceil_div(d.rows * a.splits, 4)));
+  p.parts = std::max<int64_t>(1, std::min<int64_t>(kRotaryBlocks, ceil_div(d.rows * a.splits, 4)));
   Regions r;
   r.take({p.parts, 2, d.size, 4});
   p.backward_bytes = r.off;
@@ -427,8 +427,10 @@ extern "C" int rnn_rotary_encode(const rnn_rotary* rotary, const rnn_rotary_oper
     if (a.out[k].p && a.out[k].p == a.x[k].p && a.out[k].rs != a.x[k].rs)
       return fail(RNN_ERR_ARG, kRotary, "%s: the memory of its input at another row_stride", k ? "K_out" : "Q_out");
   if (d.rows == 0 || (!a.out[0].p && !a.out[1].p)) return RNN_OK;
+  for (int k = 0; k < 2; ++k)
+    if (!a.out[k].p) a.x[k].p = nullptr;
   rotary_lay(p, rotary_vec(p, a), a);
-  const int64_t blocks = std::min<int64_t>(ceil_div(d.rows * a.splits, 4), int64_t(1) << 23);
+  const int64_t blocks = std::min<int64_t>(ceil_div(d.rows * a.splits, 4), kRotaryBlocks);
   hipStream_t s = static_cast<hipStream_t>(stream);
   OnDevice on(s);
   if (hipError_t e = launch_rotary(a, d.dtype, blocks, s); e != hipSuccess)
@@ -464,7 +466,7 @@ extern "C" int rnn_rotary_encode_backward(const rnn_rotary* rotary, const rnn_ro
   if (!a.out[0].p && !dq) a.x[0].p = nullptr;
   a.part = dq || dk ? static_cast<float*>(scratch) : nullptr;
   rotary_lay(p, rotary_vec(p, a), a);
-  const int64_t blocks = a.part ? p.parts : std::max<int64_t>(1, std::min<int64_t>(ceil_div(d.rows * a.splits, 4), int64_t(1) << 23));
+  const int64_t blocks = a.part ? p.parts : std::max<int64_t>(1, std::min<int64_t>(ceil_div(d.rows * a.splits, 4), kRotaryBlocks));
   hipStream_t s = static_cast<hipStream_t>(stream);
   OnDevice on(s);
   if (hipError_t e = launch_rotary_backward(a, d.dtype, blocks, s); e != hipSuccess)

@@ -92,6 +92,7 @@ struct RotaryArgs {
 };
 
 constexpr int kRotaryMaxSize = 512;
+constexpr int64_t kRotaryBlocks = 512;   // workgroups of a launch at most
 constexpr int kAttnMaxSize = 256;   // of a head's keys and values
 constexpr int kAttnCols = 64;       // columns of v and out that a workgroup takes
 constexpr int kAttnSteps = 4;       // steps up to which a sequence is taken one by one
