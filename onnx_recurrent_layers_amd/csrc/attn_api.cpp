@@ -12,7 +12,7 @@ using namespace rnnhip;
 
 // The time axis of a call in pieces.
 struct AttnPlan {
-  int piece, pieces;
+  int piece, pieces, sub;
 };
 
 struct rnn_attn {
@@ -40,7 +40,7 @@ const char kAttn[] = "linear attention", kRotary[] = "rotary norm";
 // fill the chip by themselves one piece does; more cost a launch for the states
 // that they leave and one that joins them.  `most`: steps of a piece at most.
 AttnPlan attn_plan(const rnn_attn_desc& d, bool tokens, int64_t blocks, int64_t most) {
-  if (tokens) return {int(std::max<int64_t>(d.seq, 1)), 1};
+  if (tokens) return {int(std::max<int64_t>(d.seq, 1)), 1, 0};
   const int64_t whole = ceil_div(d.seq, 64) * 64;
   int64_t piece = whole;
   if (blocks <= 128) piece = std::max<int64_t>(ceil_div(ceil_div(whole, ceil_div(256, std::max<int64_t>(blocks, 1))), 64) * 64, 128);
@@ -49,7 +49,19 @@ AttnPlan attn_plan(const rnn_attn_desc& d, bool tokens, int64_t blocks, int64_t 
     const int64_t c = std::atoll(e);
     if (c > 0) piece = c >= whole ? whole : ceil_div(c, 64) * 64;
   }
-  return {int(piece), int(ceil_div(d.seq, piece))};
+  return {int(piece), int(ceil_div(d.seq, piece)), 0};
+}
+
+// Few pieces' walks join what the pieces before them leave by themselves, without a
+// launch, and then these are walked for their states in parts that fill the chip,
+// too.  (Two pieces of 1024 steps, 128 workgroups a piece, bf16: 63 us in two parts
+// each, 73 joined by a launch; eight of 512, 32 workgroups, f16: 50.3, 51.0.)
+int attn_sub(const AttnPlan& f, int64_t blocks) {
+  const int64_t before = f.pieces - 1;
+  if (before < 1 || before > kAttnParts) return 0;
+  int sub = 1;
+  while (2 * sub * before <= kAttnParts && 2 * sub * before * blocks <= 256 && f.piece % (128 * sub) == 0 && f.piece / (2 * sub) >= 128) sub *= 2;
+  return sub;
 }
 
 // The scratch regions of the two directions, in the order that they are taken.
@@ -58,7 +70,7 @@ struct AttnScratch {
 };
 bool attn_scratch(const rnn_attn& p, bool backward, AttnScratch* at, size_t* total) {
   const rnn_attn_desc& d = p.d;
-  const int64_t pieces = backward ? std::max(p.b.pieces, p.bd.pieces) : p.f.pieces;
+  const int64_t pieces = backward ? std::max(p.b.pieces, p.bd.pieces) : int64_t(p.f.pieces) * std::max(p.f.sub, 1);
   Regions r;
   *at = AttnScratch{};
   if (pieces > 1) {
@@ -123,6 +135,7 @@ int attn_starts(const rnn_attn& p, const AttnArgs& a, hipStream_t s) {
   w.sk = int(p.d.value), w.sv = 1;
   w.dots = w.ends = nullptr;
   if (int rc = attn_launch("pieces", attn_walk(p, w, true, s))) return rc;
+  if (a.sub) return RNN_OK;
   const AttnJoinArgs j{a.pieces, a.back, p.d.batch * p.d.heads, p.d.key * p.d.value, a.starts, a.totals, a.init};
   return attn_launch("join", launch_attn_join(j, s));
 }
@@ -155,6 +168,7 @@ extern "C" int rnn_attn_create(const rnn_attn_desc* desc, rnn_attn** out) {
   if (bytes_of({d.batch, d.heads, d.key, d.value, 4}) < 0) return fail(RNN_ERR_SHAPE, kAttn, "initial_state: size overflows");
   const int64_t heads = d.batch * d.heads, blocks = heads * std::max(p.key_cols, p.value_cols);   // (below 2^57)
   p.f = attn_plan(d, p.tokens, heads * p.value_cols, d.seq + 64);
+  p.f.sub = attn_sub(p.f, heads * p.value_cols);
   p.b = attn_plan(d, p.tokens, heads * std::min(p.key_cols, p.value_cols), d.seq + 64);
   // (the decays' gradient is summed back from a piece's end, and what the sums lose
   // grows with it: 2 x 2048 steps, 8 heads of 128 x 128, bf16, dG off by 3.3e-7 of its
@@ -203,6 +217,7 @@ extern "C" int rnn_attn_encode(const rnn_attn* attn, const rnn_attn_operands* op
   a.sk = int(d.value), a.sv = 1;
   a.in_scale = 1.f, a.out_scale = d.scale;
   a.piece = p.f.piece, a.pieces = p.f.pieces;
+  a.sub = a.init == a.fin ? 0 : p.f.sub;   // (the last piece's final state may be written before another walk begins)
   if (int rc = check_scratch(kAttn, scratch, p.forward_bytes)) return rc;
   AttnScratch at;
   size_t total;

@@ -161,12 +161,6 @@ __device__ __forceinline__ Parts<T, N> op_parts(const float (&x)[8]) {
   return r;
 }
 template <typename T, int N>
-__device__ __forceinline__ f32x4 mul_parts(const Parts<T, N>& a, const typename Mma<T>::Op& b, f32x4 c) {
-#pragma unroll
-  for (int n = N - 1; n >= 0; --n) c = Mma<T>::mul(a.p[n], b, c);
-  return c;
-}
-template <typename T, int N>
 __device__ __forceinline__ f32x4 mul_parts(const typename Mma<T>::Op& a, const Parts<T, N>& b, f32x4 c) {
 #pragma unroll
   for (int n = N - 1; n >= 0; --n) c = Mma<T>::mul(a, b.p[n], c);
@@ -267,16 +261,18 @@ __global__ __launch_bounds__(512, 2) void attn_chunk_kernel(AttnArgs a) {
   __shared__ alignas(16) float shi[2][TC], slo[2][TC], ssince[2][TC], sleft[2][TC], slog[2][TC], sdiag[2][TC], sback[2][8], stotal[2], red[4][TC];
   const int w = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
   const int t = int(threadIdx.x) & 255, lane = t & 63, q = lane & 15, g = lane >> 4;
-  const int slices = (a.V + COLS - 1) / COLS, pieces = WALK ? a.pieces : a.pieces - 1;
+  const int sub = a.sub ? a.sub : 1, parts = a.pieces * sub;   // (of a head; what is walked for its state)
+  const int slices = (a.V + COLS - 1) / COLS, pieces = WALK ? a.pieces : parts - sub;
   // a die's workgroups (they go to eight in turn) are neighbours: a head's slices share its a and b there
   const int per_die = int(gridDim.x) / 8, rest = int(gridDim.x) % 8, die = int(blockIdx.x) % 8;
   const int block = die * per_die + min(die, rest) + int(blockIdx.x) / 8;
   const int slice = block % slices, bp = block / slices, bh = bp / pieces;
-  const int piece = bp - bh * pieces + (!WALK && a.back ? 1 : 0);
+  const int piece = bp - bh * pieces + (!WALK && a.back ? sub : 0);
   const int b = bh / a.H, h = bh - b * a.H;
   const int L = geo_len(a.geo, b);
-  const int64_t lo64 = int64_t(piece) * a.piece;
-  const int lo = int(min(lo64, int64_t(a.geo.S))), end = int(min(lo64 + a.piece, int64_t(a.geo.S))), hi = min(end, L), n = max(hi - lo, 0);
+  const int size = WALK ? a.piece : a.piece / sub;
+  const int64_t lo64 = int64_t(piece) * size;
+  const int lo = int(min(lo64, int64_t(a.geo.S))), end = int(min(lo64 + size, int64_t(a.geo.S))), hi = min(end, L), n = max(hi - lo, 0);
   const AttnSteps<T> r(a, b, h, L, lo, hi);
   const int c0 = slice * COLS;
   const int64_t KV = int64_t(a.K) * a.V;
@@ -534,7 +530,7 @@ __global__ __launch_bounds__(512, 2) void attn_chunk_kernel(AttnArgs a) {
       if (c + 1 < chunks) next((c + 2) * TC, std::integral_constant<int, 0>{});
     }
     if (DOTS && chunks > 0) put_dots((chunks - 1) * TC);
-    if (!WALK && sums_here && lane == 0 && slice == 0) a.totals[int64_t(bh) * a.pieces + piece] = __builtin_amdgcn_exp2f(float(all));
+    if (!WALK && sums_here && lane == 0 && slice == 0) a.totals[int64_t(bh) * parts + piece] = __builtin_amdgcn_exp2f(float(all));
     if constexpr (DOTS)
       if (a.ends) {
         __syncthreads();
@@ -550,20 +546,32 @@ __global__ __launch_bounds__(512, 2) void attn_chunk_kernel(AttnArgs a) {
   // rows that there are among 4 g + (0..3) on (none without a column): for k, i those below
   auto rows_of = [&] { return afresh(column < a.V ? a.K - 4 * g : 0); };
   {
-    const float* start = !WALK ? nullptr : a.pieces > 1 ? a.starts + (int64_t(bh) * a.pieces + piece) * KV : a.init ? a.init + bh * KV : nullptr;
 #pragma unroll
     for (int k = 0; k < 2 * KT; ++k) S[k] = f32x4{0.f, 0.f, 0.f, 0.f};
-    if (start) {   // (past the last row or column: some other, made zero)
+    const int rows = rows_of();
+    auto add = [&](const float* start, float total) {   // (past the last row or column: some other, made zero)
       const float* from = start + int64_t(min(column, a.V - 1)) * a.sv;
-      const int rows = rows_of();
+      f32x4 x[2 * KT];
 #pragma unroll
       for (int k = 0; k < 2 * KT; ++k)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) S[k][i] = from[min(16 * k + 4 * g + i, a.K - 1) * a.sk];
+        for (int i = 0; i < 4; ++i) x[k][i] = from[min(16 * k + 4 * g + i, a.K - 1) * a.sk];
 #pragma unroll
       for (int k = 0; k < 2 * KT; ++k)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) S[k][i] = 16 * k + i < rows ? S[k][i] : 0.f;
+        for (int i = 0; i < 4; ++i) S[k][i] = 16 * k + i < rows ? __builtin_fmaf(S[k][i], total, x[k][i]) : 0.f;
+    };
+    if constexpr (WALK) {
+      if (a.pieces > 1 && a.sub == 0) {
+        add(a.starts + (int64_t(bh) * parts + piece) * KV, 1.f);
+      } else {
+        if (a.init) add(a.init + bh * KV, 1.f);
+        const int before = (a.back ? a.pieces - 1 - piece : piece) * a.sub;
+        for (int k = 0; k < before; ++k) {
+          const int64_t at = int64_t(bh) * parts + (a.back ? parts - 1 - k : k);
+          add(a.starts + at * KV, a.totals[at]);
+        }
+      }
     }
   }
   // a chunk's outputs, and the rows that they are multiplied with
@@ -843,7 +851,7 @@ __global__ __launch_bounds__(512, 2) void attn_chunk_kernel(AttnArgs a) {
             if (16 * k + i < rows) S[k][i] = __builtin_fmaf(r.get(a.b, a.K, row, 16 * k + 4 * g + i) * a.in_scale, v, S[k][i] * dec);
       }
     }
-    float* to = a.starts + (int64_t(bh) * a.pieces + piece) * KV;
+    float* to = a.starts + (int64_t(bh) * parts + piece) * KV;
     const int rows = rows_of();
 #pragma unroll
     for (int k = 0; k < 2 * KT; ++k)
@@ -889,7 +897,7 @@ __global__ __launch_bounds__(512, 2) void attn_chunk_kernel(AttnArgs a) {
 
 template <typename T, int MODE, bool VEC>
 hipError_t attn_chunks_of(const AttnArgs& a, hipStream_t s) {
-  const int64_t blocks = int64_t(a.geo.B) * a.H * ((a.V + kAttnCols - 1) / kAttnCols) * (MODE == kAttnLocal ? a.pieces - 1 : a.pieces);
+  const int64_t blocks = int64_t(a.geo.B) * a.H * ((a.V + kAttnCols - 1) / kAttnCols) * (MODE == kAttnLocal ? (a.pieces - 1) * (a.sub ? a.sub : 1) : a.pieces);
   if (a.K <= 32) return go(attn_chunk_kernel<T, 1, MODE, VEC>, blocks, 512, a, s);
   if (a.K <= 64) return go(attn_chunk_kernel<T, 2, MODE, VEC>, blocks, 512, a, s);
   if (a.K <= 128) return go(attn_chunk_kernel<T, 4, MODE, VEC>, blocks, 512, a, s);

@@ -36,7 +36,9 @@ struct AttnArgs {
   // The time axis in pieces, walked side by side, each of so many steps: the
   // states that they begin with (before: those that they leave from zero ones),
   // [B][H][pieces], and their decays.  (One piece: from init, and none of these.)
-  int32_t piece, pieces;
+  // `sub`: a walk begins from init and what the parts before its piece leave, `sub`
+  // parts a piece, [B][H][pieces][sub].
+  int32_t piece, pieces, sub;
   float *starts, *totals;
   float* fin;              // [B][H], or NULL; `back`: times the first step's decay
   // for the decays' gradient
@@ -95,6 +97,7 @@ constexpr int kRotaryMaxSize = 512;
 constexpr int64_t kRotaryBlocks = 512;   // workgroups of a launch at most
 constexpr int kAttnMaxSize = 256;   // of a head's keys and values
 constexpr int kAttnCols = 64;       // columns of v and out that a workgroup takes
+constexpr int kAttnParts = 8;      // parts before a piece that a walk joins by itself
 constexpr int kAttnSteps = 4;       // steps up to which a sequence is taken one by one
 
 hipError_t launch_attn_steps(const AttnArgs& a, int dtype, hipStream_t s);
