@@ -66,7 +66,7 @@ int attn_sub(const AttnPlan& f, int64_t blocks) {
 
 // The scratch regions of the two directions, in the order that they are taken.
 struct AttnScratch {
-  size_t starts, totals, back_starts, back_totals, rows, cols, ends, decay, part;
+  size_t starts, totals, back_starts, back_totals, rows, cols, ends, decay, part[2];
 };
 bool attn_scratch(const rnn_attn& p, bool backward, AttnScratch* at, size_t* total) {
   const rnn_attn_desc& d = p.d;
@@ -86,7 +86,8 @@ bool attn_scratch(const rnn_attn& p, bool backward, AttnScratch* at, size_t* tot
     at->cols = r.take({p.key_cols, d.batch, d.heads, d.seq, 4});
     at->ends = r.take({p.key_cols, d.batch, d.heads, p.bd.pieces, 4});
     at->decay = r.take({d.batch, d.heads, p.bd.pieces, 4});
-    if (p.per > 1) at->part = r.take({d.seq, d.batch, d.heads, d.key, 4});
+    if (p.per > 1)
+      for (size_t& part : at->part) part = r.take({d.seq, d.batch, d.heads, d.key, 4});
   }
   *total = r.off;
   return r.ok;
@@ -121,6 +122,13 @@ hipError_t attn_walk(const rnn_attn& p, const AttnArgs& a, bool local, hipStream
   return p.d.dtype == RNN_DTYPE_F32   ? launch_attn_chunks_f32(a, local, s)
          : p.d.dtype == RNN_DTYPE_F16 ? launch_attn_chunks_f16(a, local, s)
                                       : launch_attn_chunks_bf16(a, local, s);
+}
+
+// A few walks in one launch.
+hipError_t attn_walks(const rnn_attn& p, const AttnArgs* w, int n, hipStream_t s) {
+  return p.d.dtype == RNN_DTYPE_F32   ? launch_attn_walks_f32(w, n, s)
+         : p.d.dtype == RNN_DTYPE_F16 ? launch_attn_walks_f16(w, n, s)
+                                      : launch_attn_walks_bf16(w, n, s);
 }
 
 int attn_launch(const char* what, hipError_t e) {
@@ -281,18 +289,28 @@ extern "C" int rnn_attn_encode_backward(const rnn_attn* attn, const rnn_attn_ope
     if (int rc = attn_starts(p, back, s)) return rc;
 
   // dQ and dK: of each head by itself, summed over a group's heads
-  auto shared = [&](const char* what, AttnArgs w, const Rows& out, const HeadRows& dot, float* dots) -> int {
+  AttnArgs walks[3];
+  const char* names[3];
+  HeadSumArgs sums{};
+  sums.rows = rows, sums.H = int(d.heads), sums.per = p.per, sums.K = int(d.key);
+  int n = 0;
+  auto add = [&](const char* name, const AttnArgs& w) {
+    names[n] = name;
+    walks[n++] = w;
+  };
+  auto shared = [&](const char* name, AttnArgs w, const Rows& out, const HeadRows& dot, float* dots) {
     w.K = int(d.value), w.V = int(d.key);
     w.sk = 1, w.sv = int(d.value);
-    const bool sum = p.per > 1 && out.p;
-    w.out = sum ? HeadRows{reinterpret_cast<char*>(f(at.part)), d.heads * d.key, 1} : head_rows(out, 1);
-    w.out_f32 = sum;
+    w.out = head_rows(out, 1);
     w.dot = dot;
     w.dots = decays ? dots : nullptr;
-    if (int rc = attn_launch(what, attn_walk(p, w, false, s))) return rc;
-    if (!sum) return RNN_OK;
-    const HeadSumArgs hs{f(at.part), rows, int(d.heads), p.per, int(d.key), out};
-    return attn_launch("sum", launch_head_sum(hs, d.dtype, s));
+    if (p.per > 1 && out.p) {
+      sums.part[sums.n] = f(at.part[sums.n]);
+      w.out = HeadRows{reinterpret_cast<char*>(f(at.part[sums.n])), d.heads * d.key, 1};
+      w.out_f32 = 1;
+      sums.out[sums.n++] = out;
+    }
+    add(name, w);
   };
   const bool ends = decays && (dfin || a.pieces > 1);
   if (dQ.p || decays) {
@@ -303,12 +321,12 @@ extern "C" int rnn_attn_encode_backward(const rnn_attn* attn, const rnn_attn_ope
       w.others = a.pieces > 1 ? back.starts : nullptr;
       w.ends = f(at.ends);
     }
-    if (int rc = shared("dQ", w, dQ, in.Q, f(at.rows))) return rc;
+    shared("dQ", w, dQ, in.Q, f(at.rows));
   }
   if (dK.p || decays) {
     AttnArgs w = back;
     w.a = in.V, w.b = dY, w.v = in.Q;
-    if (int rc = shared("dK", w, dK, in.K, f(at.cols))) return rc;
+    shared("dK", w, dK, in.K, f(at.cols));
   }
   if (dV.p || dinit) {
     AttnArgs w = back;
@@ -317,8 +335,17 @@ extern "C" int rnn_attn_encode_backward(const rnn_attn* attn, const rnn_attn_ope
     w.sk = int(d.value), w.sv = 1;
     w.out = head_rows(dV, 1);
     w.fin = dinit;
-    if (int rc = attn_launch("dV", attn_walk(p, w, false, s))) return rc;
+    add("dV", w);
   }
+  // (a rule on the sizes alone: an output is the same whichever others are asked for)
+  if (!p.tokens && d.batch * d.heads * (2 * p.key_cols + p.value_cols) * a.pieces <= 256) {
+    if (int rc = attn_launch("gradient", attn_walks(p, walks, n, s))) return rc;
+  } else {
+    for (int k = 0; k < n; ++k)
+      if (int rc = attn_launch(names[k], attn_walk(p, walks[k], false, s))) return rc;
+  }
+  if (sums.n)
+    if (int rc = attn_launch("sum", launch_head_sum(sums, d.dtype, s))) return rc;
   if (!decays) return RNN_OK;
   const AttnDecayArgs da{a.geo, a.H, p.key_cols, a.piece, a.pieces, f(at.rows), f(at.cols), ends ? f(at.ends) : nullptr, a.G, a.decay, dG,
                          ddecay ? f(at.decay) : nullptr};

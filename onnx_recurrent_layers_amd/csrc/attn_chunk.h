@@ -234,16 +234,18 @@ __device__ __forceinline__ void between_products() {
   }
 }
 
-enum { kAttnLocal, kAttnWalk, kAttnDots };
+enum { kAttnLocal, kAttnWalk, kAttnDots, kAttnSome };
 
 // KT: 32-wide pieces of a and b.  MODE: the state that a piece of the time axis
 // leaves from a zero one; the outputs; these with what the decays' gradient
-// needs.  VEC: rows in aligned 16-byte pieces.
+// needs; these, of walks that have some of it.  VEC: rows in aligned 16-byte
+// pieces.
 template <typename T, int KT, int MODE, bool VEC>
-__global__ __launch_bounds__(512, 2) void attn_chunk_kernel(AttnArgs a) {
+__device__ __forceinline__ void attn_walk(const AttnArgs& a, int id, int blocks) {
   typedef Mma<T> M;
   typedef typename M::Op Op;
-  constexpr bool WALK = MODE != kAttnLocal, DOTS = MODE == kAttnDots;
+  constexpr bool WALK = MODE != kAttnLocal, DOTS = MODE >= kAttnDots;
+  const bool dots = MODE == kAttnDots || (MODE == kAttnSome && a.dots);
   constexpr int TC = KT * int(sizeof(T)) >= 16 ? 32 : 64, IT = TC / 16, ST = TC / 32;    // steps of a chunk, in 16s and 32s
   constexpr int COLS = kAttnCols;                                                        // of a workgroup
   constexpr int KA = 32 * KT + M::PadA, KB = 32 * KT + M::PadB, VP = COLS + M::PadV, PP = 32 + M::PadB, PB = ST == 2 ? 6 : 2;
@@ -264,8 +266,8 @@ __global__ __launch_bounds__(512, 2) void attn_chunk_kernel(AttnArgs a) {
   const int sub = a.sub ? a.sub : 1, parts = a.pieces * sub;   // (of a head; what is walked for its state)
   const int slices = (a.V + COLS - 1) / COLS, pieces = WALK ? a.pieces : parts - sub;
   // a die's workgroups (they go to eight in turn) are neighbours: a head's slices share its a and b there
-  const int per_die = int(gridDim.x) / 8, rest = int(gridDim.x) % 8, die = int(blockIdx.x) % 8;
-  const int block = die * per_die + min(die, rest) + int(blockIdx.x) / 8;
+  const int per_die = blocks / 8, rest = blocks % 8, die = id % 8;
+  const int block = die * per_die + min(die, rest) + id / 8;
   const int slice = block % slices, bp = block / slices, bh = bp / pieces;
   const int piece = bp - bh * pieces + (!WALK && a.back ? sub : 0);
   const int b = bh / a.H, h = bh - b * a.H;
@@ -492,7 +494,7 @@ __global__ __launch_bounds__(512, 2) void attn_chunk_kernel(AttnArgs a) {
       }
     };
     auto put_dots = [&](int u0) {
-      if (t >= TC || u0 + t >= n) return;
+      if (!dots || t >= TC || u0 + t >= n) return;
       a.dots[((int64_t(slice) * a.geo.B + b) * a.H + h) * a.geo.S + r.step(u0 + t)] = ((red[0][t] + red[1][t]) + red[2][t]) + red[3][t];
     };
 
@@ -578,7 +580,7 @@ __global__ __launch_bounds__(512, 2) void attn_chunk_kernel(AttnArgs a) {
   const int64_t ors = way * a.out.rs, drs = way * a.dot.rs;
   const int oes = a.out_f32 ? 4 : int(sizeof(T));
   char* po = a.out.p ? a.out.p + (top * a.out.rs + (h / a.out.per) * int64_t(a.V) + (VEC && down ? (TC - 1) * ors : 0)) * oes : nullptr;
-  const T* pd = DOTS ? reinterpret_cast<const T*>(a.dot.p) + top * a.dot.rs + (h / a.dot.per) * int64_t(a.V) + (VEC && down ? (TC - 1) * drs : 0) : nullptr;
+  const T* pd = dots ? reinterpret_cast<const T*>(a.dot.p) + top * a.dot.rs + (h / a.dot.per) * int64_t(a.V) + (VEC && down ? (TC - 1) * drs : 0) : nullptr;
 
   // The steps of the chunk one by one, from shared memory.
   auto one_by_one = [&](int u0, int steps, int at) {
@@ -606,7 +608,7 @@ __global__ __launch_bounds__(512, 2) void attn_chunk_kernel(AttnArgs a) {
       if constexpr (DOTS) {
         off += __shfl_xor(off, 16, 64);
         off += __shfl_xor(off, 32, 64);
-        float dot = column < a.V ? off * a.out_scale * r.get(a.dot, a.V, row, column) : 0.f;
+        float dot = dots && column < a.V ? off * a.out_scale * r.get(a.dot, a.V, row, column) : 0.f;
 #pragma unroll
         for (int m = 1; m < 16; m *= 2) dot += __shfl_xor(dot, m, 64);
         if (lane == 0) red[w][u] = dot;
@@ -618,6 +620,16 @@ __global__ __launch_bounds__(512, 2) void attn_chunk_kernel(AttnArgs a) {
   if constexpr (WALK) __syncthreads();
   for (int chunk = 0; chunk < chunks; ++chunk) {
     const int u0 = chunk * TC, at = chunk & 1, steps = min(n - u0, TC);
+    // the rows that the outputs are multiplied with, on their way until then
+    Pack<T, 4> dx[DOTS && VEC ? IT : 1];
+    if (DOTS && VEC && dots) {
+#pragma unroll
+      for (int i = 0; i < IT; ++i) {
+        const int c = c0 + cw + 4 * g;   // (past the last step: that one again)
+        const uint32_t off = uint32_t(place(min(16 * i + q, steps - 1))) * uint32_t(down ? -drs : drs) + uint32_t(c < a.V ? c : 0);
+        dx[i] = *reinterpret_cast<const Pack<T, 4>*>(reinterpret_cast<const char*>(pd) + off * uint32_t(sizeof(T)));
+      }
+    }
     // v by steps: this lane's column, eight steps of each 32
     Op fv[ST];
 #pragma unroll
@@ -700,16 +712,11 @@ __global__ __launch_bounds__(512, 2) void attn_chunk_kernel(AttnArgs a) {
           const int u = 16 * i + q, c = c0 + cw + 4 * g;
           const float by = sdiag[at][u];
           float d[4] = {};
-          if (u < steps) {
-            if constexpr (VEC) {
-              const uint32_t off = uint32_t(place(u)) * uint32_t(down ? -drs : drs) + uint32_t(c < a.V ? c : 0);
-              const Pack<T, 4> x = *reinterpret_cast<const Pack<T, 4>*>(reinterpret_cast<const char*>(pd) + off * uint32_t(sizeof(T)));
+          if (dots && u < steps) {
 #pragma unroll
-              for (int k = 0; k < 4; ++k) d[k] = float(x.v[k]);
-            } else {
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                if (c + k < a.V) d[k] = float(pd[u * drs + c + k]);
+            for (int k = 0; k < 4; ++k) {
+              if (VEC) d[k] = float(dx[i].v[k]);
+              else if (c + k < a.V) d[k] = float(pd[u * drs + c + k]);
             }
           }
           const Pack<T, 4> own = *reinterpret_cast<const Pack<T, 4>*>(&sv[at][u][cw + 4 * g]);
@@ -827,7 +834,7 @@ __global__ __launch_bounds__(512, 2) void attn_chunk_kernel(AttnArgs a) {
       one_by_one(u0, steps, at);
     }
     if (po) po += TC * ors * oes;
-    if constexpr (DOTS) pd += TC * drs;
+    if (dots) pd += TC * drs;
     __syncthreads();   // (the next chunk's scores are there, this one's rows are done with)
   }
   if constexpr (!WALK) {
@@ -895,6 +902,20 @@ __global__ __launch_bounds__(512, 2) void attn_chunk_kernel(AttnArgs a) {
       if (c0 + lane < a.V) r.put(dead_row(a.geo, b, s), c0 + lane, 0.f);
 }
 
+template <typename T, int KT, int MODE, bool VEC>
+__global__ __launch_bounds__(512, 2) void attn_chunk_kernel(AttnArgs a) {
+  attn_walk<T, KT, MODE, VEC>(a, int(blockIdx.x), int(gridDim.x));
+}
+
+// Walks that do not fill the chip by themselves, side by side.
+template <typename T, int KT, bool VEC>
+__global__ __launch_bounds__(512, 2) void attn_walks_kernel(AttnWalks) {
+  // (read where they lie: a copy of which one is chosen by index goes by memory)
+  const AttnWalks& s = *(const AttnWalks*)__builtin_amdgcn_kernarg_segment_ptr();
+  const int id = int(blockIdx.x), k = (id >= s.first[1]) + (id >= s.first[2]);
+  attn_walk<T, KT, kAttnSome, VEC>(s.w[k], id - s.first[k], s.first[k + 1] - s.first[k]);
+}
+
 template <typename T, int MODE, bool VEC>
 hipError_t attn_chunks_of(const AttnArgs& a, hipStream_t s) {
   const int64_t blocks = int64_t(a.geo.B) * a.H * ((a.V + kAttnCols - 1) / kAttnCols) * (MODE == kAttnLocal ? (a.pieces - 1) * (a.sub ? a.sub : 1) : a.pieces);
@@ -904,18 +925,47 @@ hipError_t attn_chunks_of(const AttnArgs& a, hipStream_t s) {
   return go(attn_chunk_kernel<T, 8, MODE, VEC>, blocks, 512, a, s);
 }
 
+// Rows in whole aligned pieces, a chunk's within 2^31 bytes (2^25 a step).
 template <typename T>
-hipError_t attn_chunks(const AttnArgs& a, bool local, hipStream_t s) {
-  // rows in whole aligned pieces, a chunk's within 2^31 bytes (2^25 a step)
+bool attn_whole(const AttnArgs& a, bool local) {
   const auto whole = [&](const HeadRows& x, int size, size_t es) {
     return reinterpret_cast<uintptr_t>(x.p) % 16 == 0 && x.rs * es % 16 == 0 && size * sizeof(T) % 16 == 0 &&
            x.rs * es <= (size_t(1) << 25) / (a.geo.layout ? 1 : a.geo.B);
   };
-  const bool vec = whole(a.b, a.K, sizeof(T)) && whole(a.v, a.V, sizeof(T)) && (local || whole(a.a, a.K, sizeof(T))) &&
-                   (!a.dots || whole(a.dot, a.V, sizeof(T))) && (local || !a.out.p || whole(a.out, a.V, a.out_f32 ? 4 : sizeof(T)));
+  return whole(a.b, a.K, sizeof(T)) && whole(a.v, a.V, sizeof(T)) && (local || whole(a.a, a.K, sizeof(T))) &&
+         (!a.dots || whole(a.dot, a.V, sizeof(T))) && (local || !a.out.p || whole(a.out, a.V, a.out_f32 ? 4 : sizeof(T)));
+}
+
+template <typename T>
+hipError_t attn_chunks(const AttnArgs& a, bool local, hipStream_t s) {
+  const bool vec = attn_whole<T>(a, local);
   if (local) return vec ? attn_chunks_of<T, kAttnLocal, true>(a, s) : attn_chunks_of<T, kAttnLocal, false>(a, s);
   if (a.dots) return vec ? attn_chunks_of<T, kAttnDots, true>(a, s) : attn_chunks_of<T, kAttnDots, false>(a, s);
   return vec ? attn_chunks_of<T, kAttnWalk, true>(a, s) : attn_chunks_of<T, kAttnWalk, false>(a, s);
+}
+
+template <typename T, bool VEC>
+hipError_t attn_walks_of(const AttnWalks& w, int K, hipStream_t s) {
+  const int64_t blocks = w.first[3];
+  if (K <= 32) return go(attn_walks_kernel<T, 1, VEC>, blocks, 512, w, s);
+  if (K <= 64) return go(attn_walks_kernel<T, 2, VEC>, blocks, 512, w, s);
+  if (K <= 128) return go(attn_walks_kernel<T, 4, VEC>, blocks, 512, w, s);
+  return go(attn_walks_kernel<T, 8, VEC>, blocks, 512, w, s);
+}
+
+template <typename T>
+hipError_t attn_walks(const AttnArgs* w, int n, hipStream_t s) {
+  AttnWalks all{};
+  bool vec = true;
+  int K = 0;
+  for (int k = 0; k < n; ++k) {
+    const AttnArgs& a = all.w[k] = w[k];
+    all.first[k + 1] = all.first[k] + a.geo.B * a.H * ((a.V + kAttnCols - 1) / kAttnCols) * a.pieces;
+    vec = vec && attn_whole<T>(a, false);
+    K = std::max(K, a.K);
+  }
+  for (int k = n; k < 3; ++k) all.first[k + 1] = all.first[k];
+  return vec ? attn_walks_of<T, true>(all, K, s) : attn_walks_of<T, false>(all, K, s);
 }
 
 }  // namespace

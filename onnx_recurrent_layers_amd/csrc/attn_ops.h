@@ -49,6 +49,12 @@ struct AttnArgs {
   float* ends;             // [slices][B][H][pieces], or NULL
 };
 
+// Up to three walks in one launch, walk k's workgroups from first[k] on.
+struct AttnWalks {
+  AttnArgs w[3];
+  int32_t first[4];
+};
+
 // The states that pieces begin with, in their place: from those that they leave
 // from a zero one.
 struct AttnJoinArgs {
@@ -70,12 +76,13 @@ struct AttnDecayArgs {
   float* part;                       // [B][pieces][H] sums over a piece's steps, or NULL
 };
 
-// out[row][g * K + k] = the sum over a group's heads of part[row][h][k].
+// out[i][row][g * K + k] = the sum over a group's heads of part[i][row][h][k], for
+// n tensors, one or two.
 struct HeadSumArgs {
-  const float* part;
+  const float* part[2];
   int64_t rows;
-  int32_t H, per, K;
-  Rows out;
+  int32_t n, H, per, K;
+  Rows out[2];
 };
 
 // Norms and rotations of a row's heads, queries [0] and keys [1].
@@ -103,8 +110,11 @@ constexpr int kAttnSteps = 4;       // steps up to which a sequence is taken one
 hipError_t launch_attn_steps(const AttnArgs& a, int dtype, hipStream_t s);
 // (one definition a type: k_attn_f32.hip, k_attn_f16.hip, k_attn_bf16.hip)
 hipError_t launch_attn_chunks_f32(const AttnArgs& a, bool local, hipStream_t s);
+hipError_t launch_attn_walks_f32(const AttnArgs* w, int n, hipStream_t s);   // (n up to 3)
 hipError_t launch_attn_chunks_f16(const AttnArgs& a, bool local, hipStream_t s);
+hipError_t launch_attn_walks_f16(const AttnArgs* w, int n, hipStream_t s);   // (n up to 3)
 hipError_t launch_attn_chunks_bf16(const AttnArgs& a, bool local, hipStream_t s);
+hipError_t launch_attn_walks_bf16(const AttnArgs* w, int n, hipStream_t s);   // (n up to 3)
 hipError_t launch_attn_join(const AttnJoinArgs& a, hipStream_t s);
 hipError_t launch_attn_decay(const AttnDecayArgs& a, hipStream_t s);
 hipError_t launch_head_sum(const HeadSumArgs& a, int dtype, hipStream_t s);

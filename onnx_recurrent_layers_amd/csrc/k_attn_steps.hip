@@ -194,12 +194,14 @@ template <typename T>
 __global__ __launch_bounds__(256) void head_sum_kernel(HeadSumArgs a) {
   const int groups = a.H / a.per;
   const int64_t cols = int64_t(groups) * a.K;
-  for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < a.rows * cols; i += int64_t(gridDim.x) * 256) {
-    const int64_t row = i / cols, c = i - row * cols, g = c / a.K, k = c - g * a.K;
-    const float* p = a.part + (row * a.H + g * a.per) * a.K + k;
+  for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < a.n * a.rows * cols; i += int64_t(gridDim.x) * 256) {
+    const bool second = i >= a.rows * cols;
+    const int64_t row = i / cols - (second ? a.rows : 0), c = i % cols, g = c / a.K, k = c - g * a.K;
+    const float* p = (second ? a.part[1] : a.part[0]) + (row * a.H + g * a.per) * a.K + k;
+    const Rows& out = second ? a.out[1] : a.out[0];
     float v = 0.f;
     for (int j = 0; j < a.per; ++j) v += p[int64_t(j) * a.K];
-    reinterpret_cast<T*>(a.out.p)[row * a.out.rs + c] = T(v);
+    reinterpret_cast<T*>(out.p)[row * out.rs + c] = T(v);
   }
 }
 
@@ -234,7 +236,7 @@ hipError_t launch_attn_decay(const AttnDecayArgs& a, hipStream_t s) {
 }
 
 hipError_t launch_head_sum(const HeadSumArgs& a, int dtype, hipStream_t s) {
-  const int64_t all = (a.rows * (a.H / a.per) * a.K + 255) / 256, blocks = all < 1 << 20 ? all : 1 << 20;
+  const int64_t all = (a.n * a.rows * (a.H / a.per) * a.K + 255) / 256, blocks = all < 1 << 20 ? all : 1 << 20;
   return dtype == RNN_DTYPE_F32   ? go(head_sum_kernel<float>, blocks, 256, a, s)
          : dtype == RNN_DTYPE_F16 ? go(head_sum_kernel<f16_t>, blocks, 256, a, s)
                                   : go(head_sum_kernel<bf16_t>, blocks, 256, a, s);
