@@ -64,6 +64,13 @@ int attn_sub(const AttnPlan& f, int64_t blocks) {
   return sub;
 }
 
+// Whether a gradient's walks go side by side in one launch: those that do not fill
+// the chip.  A rule on the sizes alone: an output is the same whichever others are
+// asked for.  (5 x 80 steps, 4 heads of 24 x 30, f32: 22 us, one after another 51.)
+bool attn_side_by_side(const rnn_attn& p, const AttnPlan& plan) {
+  return !p.tokens && p.d.batch * p.d.heads * (2 * p.key_cols + p.value_cols) * plan.pieces <= 256;
+}
+
 // The scratch regions of the two directions, in the order that they are taken.
 struct AttnScratch {
   size_t starts, totals, back_starts, back_totals, rows, cols, ends, decay, part[2];
@@ -86,8 +93,8 @@ bool attn_scratch(const rnn_attn& p, bool backward, AttnScratch* at, size_t* tot
     at->cols = r.take({p.key_cols, d.batch, d.heads, d.seq, 4});
     at->ends = r.take({p.key_cols, d.batch, d.heads, p.bd.pieces, 4});
     at->decay = r.take({d.batch, d.heads, p.bd.pieces, 4});
-    if (p.per > 1)
-      for (size_t& part : at->part) part = r.take({d.seq, d.batch, d.heads, d.key, 4});
+    const bool two = attn_side_by_side(p, p.b) || attn_side_by_side(p, p.bd);
+    for (int k = 0; p.per > 1 && k < (two ? 2 : 1); ++k) at->part[k] = r.take({d.seq, d.batch, d.heads, d.key, 4});
   }
   *total = r.off;
   return r.ok;
@@ -290,15 +297,22 @@ extern "C" int rnn_attn_encode_backward(const rnn_attn* attn, const rnn_attn_ope
 
   // dQ and dK: of each head by itself, summed over a group's heads
   AttnArgs walks[3];
-  const char* names[3];
   HeadSumArgs sums{};
   sums.rows = rows, sums.H = int(d.heads), sums.per = p.per, sums.K = int(d.key);
   int n = 0;
-  auto add = [&](const char* name, const AttnArgs& w) {
-    names[n] = name;
-    walks[n++] = w;
+  const bool side = attn_side_by_side(p, plan);
+  auto sum = [&] {
+    const HeadSumArgs now = sums;
+    sums.n = 0;
+    return now.n ? attn_launch("sum", launch_head_sum(now, d.dtype, s)) : RNN_OK;
   };
-  auto shared = [&](const char* name, AttnArgs w, const Rows& out, const HeadRows& dot, float* dots) {
+  auto add = [&](const char* name, const AttnArgs& w) -> int {
+    walks[n++] = w;
+    if (side) return RNN_OK;
+    if (int rc = attn_launch(name, attn_walk(p, w, false, s))) return rc;
+    return sum();
+  };
+  auto shared = [&](const char* name, AttnArgs w, const Rows& out, const HeadRows& dot, float* dots) -> int {
     w.K = int(d.value), w.V = int(d.key);
     w.sk = 1, w.sv = int(d.value);
     w.out = head_rows(out, 1);
@@ -310,7 +324,7 @@ extern "C" int rnn_attn_encode_backward(const rnn_attn* attn, const rnn_attn_ope
       w.out_f32 = 1;
       sums.out[sums.n++] = out;
     }
-    add(name, w);
+    return add(name, w);
   };
   const bool ends = decays && (dfin || a.pieces > 1);
   if (dQ.p || decays) {
@@ -321,12 +335,12 @@ extern "C" int rnn_attn_encode_backward(const rnn_attn* attn, const rnn_attn_ope
       w.others = a.pieces > 1 ? back.starts : nullptr;
       w.ends = f(at.ends);
     }
-    shared("dQ", w, dQ, in.Q, f(at.rows));
+    if (int rc = shared("dQ", w, dQ, in.Q, f(at.rows))) return rc;
   }
   if (dK.p || decays) {
     AttnArgs w = back;
     w.a = in.V, w.b = dY, w.v = in.Q;
-    shared("dK", w, dK, in.K, f(at.cols));
+    if (int rc = shared("dK", w, dK, in.K, f(at.cols))) return rc;
   }
   if (dV.p || dinit) {
     AttnArgs w = back;
@@ -335,17 +349,12 @@ extern "C" int rnn_attn_encode_backward(const rnn_attn* attn, const rnn_attn_ope
     w.sk = int(d.value), w.sv = 1;
     w.out = head_rows(dV, 1);
     w.fin = dinit;
-    add("dV", w);
+    if (int rc = add("dV", w)) return rc;
   }
-  // (a rule on the sizes alone: an output is the same whichever others are asked for)
-  if (!p.tokens && d.batch * d.heads * (2 * p.key_cols + p.value_cols) * a.pieces <= 256) {
+  if (side) {
     if (int rc = attn_launch("gradient", attn_walks(p, walks, n, s))) return rc;
-  } else {
-    for (int k = 0; k < n; ++k)
-      if (int rc = attn_launch(names[k], attn_walk(p, walks[k], false, s))) return rc;
+    if (int rc = sum()) return rc;
   }
-  if (sums.n)
-    if (int rc = attn_launch("sum", launch_head_sum(sums, d.dtype, s))) return rc;
   if (!decays) return RNN_OK;
   const AttnDecayArgs da{a.geo, a.H, p.key_cols, a.piece, a.pieces, f(at.rows), f(at.cols), ends ? f(at.ends) : nullptr, a.G, a.decay, dG,
                          ddecay ? f(at.decay) : nullptr};
