@@ -36,14 +36,17 @@ namespace {
 
 const char kAttn[] = "linear attention", kRotary[] = "rotary norm";
 
-// The pieces of a call whose walks have `blocks` workgroups a piece.  Where these
-// fill the chip by themselves one piece does; more cost a launch for the states
-// that they leave and one that joins them.  `most`: steps of a piece at most.
+// The pieces of a call whose walks have `blocks` workgroups a piece: as many as
+// have 256 in all (one a CU; more take turns), of 128 steps at least, two chunks.
+// (Time axes in one piece and in the rule's, forward, us: 1 x 512 steps, 16 heads of
+// 128 x 128, bf16, 25 and 19; 1 x 2048 79 and 33; 4 x 1024 44 and 41; 5 x 1024 of 8
+// heads 44 and 34; 8 x 1024, 256 workgroups, 48, and in two pieces 72.)  `most`:
+// steps of a piece at most.
 AttnPlan attn_plan(const rnn_attn_desc& d, bool tokens, int64_t blocks, int64_t most) {
   if (tokens) return {int(std::max<int64_t>(d.seq, 1)), 1, 0};
   const int64_t whole = ceil_div(d.seq, 64) * 64;
   int64_t piece = whole;
-  if (blocks <= 128) piece = std::max<int64_t>(ceil_div(ceil_div(whole, ceil_div(256, std::max<int64_t>(blocks, 1))), 64) * 64, 128);
+  if (blocks <= 128) piece = std::max<int64_t>(ceil_div(ceil_div(whole, 256 / std::max<int64_t>(blocks, 1)), 64) * 64, 128);
   piece = std::min(std::min(piece, most), whole);
   if (const char* e = std::getenv("RNN_ATTN_PIECE")) {
     const int64_t c = std::atoll(e);
@@ -175,13 +178,17 @@ extern "C" int rnn_attn_create(const rnn_attn_desc* desc, rnn_attn** out) {
   p.d = d;
   p.es = elem_size(d.dtype);
   p.per = int(d.heads / d.groups);
-  p.tokens = d.seq <= kAttnSteps;
   p.key_cols = int(ceil_div(d.key, kAttnCols));
   p.value_cols = int(ceil_div(d.value, kAttnCols));
   if (bytes_of({d.seq, d.batch, d.heads, d.key, p.es}) < 0) return fail(RNN_ERR_SHAPE, kAttn, "Q: size overflows");
   if (bytes_of({d.seq, d.batch, d.heads, d.value, p.es}) < 0) return fail(RNN_ERR_SHAPE, kAttn, "V: size overflows");
   if (bytes_of({d.batch, d.heads, d.key, d.value, 4}) < 0) return fail(RNN_ERR_SHAPE, kAttn, "initial_state: size overflows");
   const int64_t heads = d.batch * d.heads, blocks = heads * std::max(p.key_cols, p.value_cols);   // (below 2^57)
+  // (Step after step or a chunk, us, bf16: 8 x 16 heads of 128 x 128, 4 steps 10.9
+  // and 10.0, 8 steps 16.5 and 9.9; f32, 8 x 8 of 64 x 64, 7.6 and 10.3, 11.9 and 10.3;
+  // bf16, 64 x 16 of 128 x 128, where the state's bytes count and a chunk's workgroups
+  // take turns, 8 steps 48.8 and 60.6, 12 steps 62.4 and 61.4.)
+  p.tokens = d.seq <= (blocks < 1024 ? kAttnSteps : kAttnManySteps);
   p.f = attn_plan(d, p.tokens, heads * p.value_cols, d.seq + 64);
   p.f.sub = attn_sub(p.f, heads * p.value_cols);
   p.b = attn_plan(d, p.tokens, heads * std::min(p.key_cols, p.value_cols), d.seq + 64);
@@ -190,6 +197,13 @@ extern "C" int rnn_attn_create(const rnn_attn_desc* desc, rnn_attn** out) {
   // norm with pieces of 256, 8.1e-7 of 1024, 1.3e-6 of 2048; f32, d_decay 6.2e-7,
   // 1.3e-6, 3.1e-6)
   p.bd = attn_plan(d, p.tokens, heads * std::min(p.key_cols, p.value_cols), 1024);
+  // (Few walks of not too many steps go side by side in one piece, one launch for
+  // four: 1 x 512 steps, 16 heads of 128 x 128, bf16, 44 us and in pieces 74; 1 x 1024
+  // 75 and 82; 5 x 1024 of 8 heads 79 and 143.  f32, 1 x 512, 8 heads of 64 x 64: 51
+  // and 43.)
+  if (!p.tokens && heads * (2 * p.key_cols + p.value_cols) <= 256 && d.seq <= (d.dtype == RNN_DTYPE_F32 ? 256 : 1024) &&
+      !std::getenv("RNN_ATTN_PIECE"))
+    p.b = p.bd = {int(ceil_div(d.seq, 64) * 64), 1, 0};
   const int64_t pieces = std::max(std::max(p.f.pieces, p.b.pieces), p.bd.pieces);
   if (bytes_of({blocks, pieces, 512}) < 0 || blocks * pieces * 512 > kMaxThreads || heads * ceil_div(d.key * d.value, 256) * 256 > kMaxThreads)
     return fail(RNN_ERR_UNSUPPORTED, kAttn, "batch x heads: too large for one launch");

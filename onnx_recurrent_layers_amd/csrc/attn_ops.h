@@ -105,7 +105,7 @@ constexpr int64_t kRotaryBlocks = 512;   // workgroups of a launch at most
 constexpr int kAttnMaxSize = 256;   // of a head's keys and values
 constexpr int kAttnCols = 64;       // columns of v and out that a workgroup takes
 constexpr int kAttnParts = 8;      // parts before a piece that a walk joins by itself
-constexpr int kAttnSteps = 4;       // steps up to which a sequence is taken one by one
+constexpr int kAttnSteps = 4, kAttnManySteps = 8;   // steps up to which a sequence is taken one by one, few or many
 
 hipError_t launch_attn_steps(const AttnArgs& a, int dtype, hipStream_t s);
 // (one definition a type: k_attn_f32.hip, k_attn_f16.hip, k_attn_bf16.hip)
