@@ -1,5 +1,6 @@
 """ONNX recurrent layers (RNN, GRU, LSTM) on MI355X (gfx950), and the operators
-of a selective state space block with layer normalization.
+of a selective state space block with layer normalization and of a linear
+attention block.
 
 A thin ctypes binding over the C ABI of ``include/rnn.h`` (library
 ``librnn_mi355x.so``, built in-tree by ``onnx_recurrent_layers_amd.build``).

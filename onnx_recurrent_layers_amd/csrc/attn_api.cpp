@@ -1,6 +1,7 @@
 // attn_api.cpp -- the C ABI of linear attention and of the norms and rotations
-// of its queries and keys: validation, scratch sizing, the launches of a call.  Every check runs in 64-bit checked arithmetic before
-// anything is enqueued; messages name operator and argument.
+// of its queries and keys: validation, scratch sizing, the launches of a call.
+// Every check runs in 64-bit checked arithmetic before anything is enqueued;
+// messages name operator and argument.
 #include <cmath>
 #include <cstdlib>
 #include <new>

