@@ -247,7 +247,7 @@ extern "C" int rnn_attn_encode(const rnn_attn* attn, const rnn_attn_operands* op
   a.sk = int(d.value), a.sv = 1;
   a.in_scale = 1.f, a.out_scale = d.scale;
   a.piece = p.f.piece, a.pieces = p.f.pieces;
-  a.sub = a.init == a.fin ? 0 : p.f.sub;   // (the last piece's final state may be written before another walk begins)
+  a.sub = a.init && a.init == a.fin ? 0 : p.f.sub;   // (the last piece's final state may be written before another walk begins)
   if (int rc = check_scratch(kAttn, scratch, p.forward_bytes)) return rc;
   AttnScratch at;
   size_t total;

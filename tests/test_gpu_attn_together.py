@@ -323,3 +323,30 @@ def test_many_rows(b, s):
 def test_gradients_side_by_side_and_one_after_another(dtype, b, s, groups):
     """One head's walks up to a chip of them, and shared heads' sums."""
     attn_case(dtype, b, s, 4, groups, 40, 24, lens=[s - i % 7 for i in range(b)], forward=False, device="cuda")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ref.TYPES)
+@pytest.mark.parametrize("k,v,pad", [(24, 20, 0), (24, 16, 3), (64, 64, 0), (128, 128, 8), (100, 70, 1), (200, 136, 0), (16, 256, 0)])
+def test_walks_of_many_rows(dtype, k, v, pad):
+    """More workgroups than the chip has units: each walk by itself."""
+    attn_case(dtype, 90, 70, 1, 1, k, v, lens=[70 - i % 71 for i in range(90)], pad=pad, device="cuda", seed=k)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ref.TYPES)
+@pytest.mark.parametrize("carried", [False, True])
+def test_many_pieces(dtype, carried, monkeypatch):
+    """Pieces' states joined by the walks (up to eight before them) and by a launch, walks side by side and one after another."""
+    monkeypatch.setenv("RNN_ATTN_PIECE", "64")
+    for b, s, lens, reverse in ((1, 576, None, False), (1, 640, None, True), (2, 640, [640, 577], False), (24, 200, [i * 9 for i in range(24)], True)):
+        attn_case(dtype, b, s, 2, 1, 32, 48, lens=lens, reverse=reverse, device="cuda", carried=carried, seed=s, gate=0.02, fixed=0.002)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ref.TYPES)
+@pytest.mark.parametrize("s,h,k,v", [(2048, 32, 64, 64), (1200, 20, 40, 130)])
+def test_parts_of_pieces(dtype, s, h, k, v):
+    """Two pieces and more, walked for their states in parts."""
+    attn_case(dtype, 2, s, h, 1, k, v, lens=[s, s - 300], back=False, device="cuda", gate=0.02, fixed=0.002)
+    attn_case(dtype, 1, s, h, h, k, v, reverse=True, back=False, device="cuda", gate=0.02, fixed=0.002, carried=False)
