@@ -350,3 +350,31 @@ def test_parts_of_pieces(dtype, s, h, k, v):
     """Two pieces and more, walked for their states in parts."""
     attn_case(dtype, 2, s, h, 1, k, v, lens=[s, s - 300], back=False, device="cuda", gate=0.02, fixed=0.002)
     attn_case(dtype, 1, s, h, h, k, v, reverse=True, back=False, device="cuda", gate=0.02, fixed=0.002, carried=False)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ref.TYPES)
+@pytest.mark.parametrize("name", ["Q", "K", "V", "dY"])
+@pytest.mark.parametrize("b", [2, 70])
+def test_gradients_of_values_that_are_not_finite(dtype, name, b):
+    """They spoil the gradients that depend on them and no other (but of K and V the decays' of the whole row and head)."""
+    s, h, k, v, at = 200, 2, 32, 40, 70
+    t = values(dtype, b, s, h, h, k, v)
+    clean = reference(t, dtype, h, h, 1.0, None, False, True, "cuda")
+    t[name][0, at, 1] = float("inf")     # of head 0
+    to = types(dtype)
+    d = {n: x.to(to[n]).cuda() for n, x in t.items()}
+    op = rl.LinearAttention(dtype=dtype, seq=s, batch=b, heads=h, key=k, value=v)
+    out = {n: torch.full(x[0].shape, float("nan"), dtype=to[n], device="cuda") for n, x in clean.items()}
+    op.backward({**d, **out})
+    torch.cuda.synchronize()
+    want = reference(t, dtype, h, h, 1.0, None, False, True, "cuda")
+    for n, (value, _) in want.items():
+        if n == "d_decay":
+            assert not out[n][0].isfinite() and out[n][1].isfinite()
+            continue
+        ok = value.isfinite()
+        assert torch.equal(out[n].isfinite(), ok), n
+        zero = torch.zeros_like(value)
+        att.close(torch.where(ok, out[n].double(), zero), torch.where(ok, value, zero), torch.where(ok, clean[n][1], zero),
+                  dtype if to[n] != torch.float32 else "f32", n)
