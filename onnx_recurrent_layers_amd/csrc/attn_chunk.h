@@ -429,24 +429,30 @@ __device__ __forceinline__ void attn_walk(const AttnArgs& a, int id, int blocks)
     const float scale = a.in_scale * a.out_scale;
     auto scores = [&](int at, int it, int half) {
       const int i = 16 * it + q, j0 = 32 * half, block = it + (half ? 2 : 0);
-      Op fa[KT], fb[2][KT];
-      f32x4 hj[2], lj[2];
-#pragma unroll
-      for (int k = 0; k < KT; ++k) fa[k] = op_runs<T>(&sa[at][i][32 * k + 8 * g], &sa[at][i][32 * k + 8 * g + 4]);
+      constexpr int KG = KT * int(sizeof(T)) > 16 ? 16 / int(sizeof(T)) : KT;   // (more fill the registers)
+      f32x4 hj[2], lj[2], c[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-#pragma unroll
-        for (int k = 0; k < KT; ++k) fb[j][k] = op_run<T>(&sb[at][j0 + 16 * j + q][32 * k + 8 * g]);
         hj[j] = *reinterpret_cast<const f32x4*>(&shi[at][j0 + 16 * j + 4 * g]);
         lj[j] = *reinterpret_cast<const f32x4*>(&slo[at][j0 + 16 * j + 4 * g]);
       }
       const float hi_i = shi[at][i], lo_i = slo[at][i];
-      asked();
-      f32x4 c[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
-      for (int k = 0; k < KT; ++k)
+      for (int k0 = 0; k0 < KT; k0 += KG) {
+        Op fa[KG], fb[2][KG];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) c[j] = M::mul(fb[j][k], fa[k], c[j]);
+        for (int k = 0; k < KG; ++k) fa[k] = op_runs<T>(&sa[at][i][32 * (k0 + k) + 8 * g], &sa[at][i][32 * (k0 + k) + 8 * g + 4]);
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int k = 0; k < KG; ++k) fb[j][k] = op_run<T>(&sb[at][j0 + 16 * j + q][32 * (k0 + k) + 8 * g]);
+        asked();
+#pragma unroll
+        for (int k = 0; k < KG; ++k)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) c[j] = M::mul(fb[j][k], fa[k], c[j]);
+        asked();
+      }
       float p[2][4], most = 0.f, own = 0.f;
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
