@@ -322,6 +322,12 @@ __device__ __forceinline__ void attn_walk(const AttnArgs& a, int id, int blocks)
       if constexpr (VEC) {
         const uint32_t stride = uint32_t(down ? -from.rs : from.rs) * sizeof(T);
         p = *reinterpret_cast<const Piece*>(reinterpret_cast<const char*>(from.p) + (uint32_t(place(u)) * stride + uint32_t(c < size ? c : 0) * uint32_t(sizeof(T))));
+      } else if (size >= M::Vec) {   // (past the row's last whole piece: the one that ends it, moved down)
+        __builtin_memcpy(&p, from.p + u * from.rs + min(c, size - M::Vec), sizeof(p));
+        if (c + M::Vec > size) {
+          const unsigned __int128 x = __builtin_bit_cast(unsigned __int128, p);
+          p = __builtin_bit_cast(Piece, x >> ((M::Vec - size % M::Vec) % M::Vec * 8 * int(sizeof(T))));
+        }
       } else {
 #pragma unroll
         for (int k = 0; k < M::Vec; ++k)
@@ -728,10 +734,18 @@ __device__ __forceinline__ void attn_walk(const AttnArgs& a, int id, int blocks)
           const float by = sdiag[at][u];
           float d[4] = {};
           if (dots && u < steps) {
+            if (VEC) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              if (VEC) d[k] = float(dx[i].v[k]);
-              else if (c + k < a.V) d[k] = float(pd[u * drs + c + k]);
+              for (int k = 0; k < 4; ++k) d[k] = float(dx[i].v[k]);
+            } else if (c + 4 <= a.V) {
+              T x[4];
+              __builtin_memcpy(x, pd + u * drs + c, sizeof(x));
+#pragma unroll
+              for (int k = 0; k < 4; ++k) d[k] = float(x[k]);
+            } else {
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                if (c + k < a.V) d[k] = float(pd[u * drs + c + k]);
             }
           }
           const Pack<T, 4> own = *reinterpret_cast<const Pack<T, 4>*>(&sv[at][u][cw + 4 * g]);
@@ -785,6 +799,16 @@ __device__ __forceinline__ void attn_walk(const AttnArgs& a, int id, int blocks)
 #pragma unroll
                 for (int k = 0; k < 4; ++k) x.v[k] = T(y[i][k]);
                 *reinterpret_cast<Pack<T, 4>*>(to) = x;
+              }
+            } else if (c + 4 <= a.V) {
+              char* to = po + (u * ors + c) * oes;
+              if (a.out_f32) {
+                __builtin_memcpy(to, &y[i], 16);
+              } else {
+                T x[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) x[k] = T(y[i][k]);
+                __builtin_memcpy(to, x, sizeof(x));
               }
             } else {
 #pragma unroll
