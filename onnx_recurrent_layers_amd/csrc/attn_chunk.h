@@ -40,6 +40,8 @@
 // is not finite goes back to the steps one by one.
 #pragma once
 
+#include <type_traits>
+
 #include "attn_device.h"
 
 namespace rnnhip {
@@ -322,16 +324,15 @@ __device__ __forceinline__ void attn_walk(const AttnArgs& a, int id, int blocks)
       if constexpr (VEC) {
         const uint32_t stride = uint32_t(down ? -from.rs : from.rs) * sizeof(T);
         p = *reinterpret_cast<const Piece*>(reinterpret_cast<const char*>(from.p) + (uint32_t(place(u)) * stride + uint32_t(c < size ? c : 0) * uint32_t(sizeof(T))));
-      } else if (size >= M::Vec) {   // (past the row's last whole piece: the one that ends it, moved down)
+      } else if (size >= M::Vec) {   // (past the row's last whole piece: the one that ends it, moved down later)
         __builtin_memcpy(&p, from.p + u * from.rs + min(c, size - M::Vec), sizeof(p));
-        if (c + M::Vec > size) {
-          const unsigned __int128 x = __builtin_bit_cast(unsigned __int128, p);
-          p = __builtin_bit_cast(Piece, x >> ((M::Vec - size % M::Vec) % M::Vec * 8 * int(sizeof(T))));
-        }
-      } else {
-#pragma unroll
-        for (int k = 0; k < M::Vec; ++k)
-          if (c + k < size) p.v[k] = from.p[u * from.rs + c + k];
+      } else {   // (heads of a few elements, all in the first piece: one by one, in few registers)
+        typedef std::conditional_t<sizeof(T) == 4, uint32_t, uint16_t> Bits;
+        unsigned __int128 x = 0;
+        const Bits* row = reinterpret_cast<const Bits*>(from.p + u * from.rs);
+#pragma unroll 1
+        for (int k = size - 1; k >= c; --k) x = x << (8 * int(sizeof(T))) | row[k];
+        p = __builtin_bit_cast(Piece, x);
       }
       return p;
     };
@@ -352,6 +353,11 @@ __device__ __forceinline__ void attn_walk(const AttnArgs& a, int id, int blocks)
         for (int i = 0; i < NK; ++i) x.a[i] = load(wa, tk + i * RK, left, a.K, ck);
         wa.p += TC * wa.rs;
       }
+    };
+    // a row's last elements to the piece's begin, and zeros after them
+    auto settle = [&](Piece& p, int size, int c) {
+      if (size < M::Vec || size % M::Vec == 0 || c + M::Vec <= size) return;
+      p = __builtin_bit_cast(Piece, __builtin_bit_cast(unsigned __int128, p) >> ((M::Vec - size % M::Vec) * 8 * int(sizeof(T))));
     };
     auto keep = [&](Piece& p, bool is) {
       if (!is) p = Piece{};
@@ -390,6 +396,15 @@ __device__ __forceinline__ void attn_walk(const AttnArgs& a, int id, int blocks)
     };
     // what was fetched, of the steps from u0 on, and b and v of AHEAD chunks later asked for
     auto put_rows = [&](int u0, int at, Rows& x) {
+      if constexpr (!VEC) {
+#pragma unroll
+        for (int i = 0; i < NK; ++i) {
+          if constexpr (WALK) settle(x.a[i], a.K, ck);
+          settle(x.b[i], a.K, ck);
+        }
+#pragma unroll
+        for (int i = 0; i < NV; ++i) settle(x.v[i], a.V, c0 + cv);
+      }
       if (u0 + TC > n || a.K < 32 * KT || c0 + COLS > a.V) {
 #pragma unroll
         for (int i = 0; i < NK; ++i) {
