@@ -292,6 +292,11 @@ extern "C" int rnn_attn_encode_backward(const rnn_attn* attn, const rnn_attn_ope
   auto f = [&](size_t off) { return reinterpret_cast<float*>(static_cast<char*>(scratch) + off); };
   hipStream_t s = static_cast<hipStream_t>(stream);
   OnDevice on(s);
+  auto sum_decay = [&](int parts) {
+    const ColSumArgs cs{f(at.decay), parts, d.heads, ddecay, nullptr, int(d.heads), 1};
+    return attn_launch("sums", launch_colsum(cs, s));
+  };
+  if (d.batch == 0) return ddecay ? sum_decay(0) : int(RNN_OK);   // (no walk, only a sum of nothing)
   const AttnPlan& plan = decays ? p.bd : p.b;
   a.piece = plan.piece, a.pieces = plan.pieces;
   // forward in time from the initial state, back from the final one's gradient
@@ -374,9 +379,7 @@ extern "C" int rnn_attn_encode_backward(const rnn_attn* attn, const rnn_attn_ope
   const AttnDecayArgs da{a.geo, a.H, p.key_cols, a.piece, a.pieces, f(at.rows), f(at.cols), ends ? f(at.ends) : nullptr, a.G, a.decay, dG,
                          ddecay ? f(at.decay) : nullptr};
   if (int rc = attn_launch("decay", launch_attn_decay(da, s))) return rc;
-  if (!ddecay) return RNN_OK;
-  const ColSumArgs cs{f(at.decay), int(d.batch) * a.pieces, d.heads, ddecay, nullptr, int(d.heads), 1};
-  return attn_launch("sums", launch_colsum(cs, s));
+  return ddecay ? sum_decay(int(d.batch) * a.pieces) : int(RNN_OK);
 }
 
 // ---------------------------------------------------------------- rotary norm
