@@ -32,8 +32,10 @@
 // Values of 32 bits (scores, state, decayed v) enter a product of 16-bit operands
 // in parts: bf16 two for the scores and the state (2^-16 of each), three (2^-24)
 // for what is summed into the state or into the decays' gradient; f16 two (2^-22),
-// scaled by a power of two to the largest of the wave's, since f16 has neither
-// the state's range nor the scores'.  f32 uses the f32 matrix cores.
+// scaled by a power of two, since f16 has neither the state's range nor the
+// scores': each step's scores to their largest (one scale for a block of steps took
+// the digits of those beside a large one), the state and decayed v to a wave's.
+// f32 uses the f32 matrix cores.
 //
 // A masked score is a zero, but a zero times a later step's infinity or NaN is
 // not; and an infinite value has no parts.  A wave whose chunk has an output that
@@ -200,6 +202,19 @@ __device__ __forceinline__ Scale wave_scale(float m) {
   return {__builtin_bit_cast(float, (267 - e) << 23), __builtin_bit_cast(float, (e - 13) << 23)};
 }
 
+// The same for the values of the four lanes that share a place among sixteen.
+__device__ __forceinline__ Scale lane_scale(float m) {
+  auto of = [&](auto p) {
+    const float x = __builtin_bit_cast(float, uint32_t(p[0])), y = __builtin_bit_cast(float, uint32_t(p[1]));
+    m = x > y ? x : y;
+  };
+  of(__builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, m), __builtin_bit_cast(uint32_t, m), false, false));
+  of(__builtin_amdgcn_permlane16_swap(__builtin_bit_cast(uint32_t, m), __builtin_bit_cast(uint32_t, m), false, false));
+  int e = __builtin_bit_cast(int, m) >> 23;
+  e = e == 0 || e >= 255 ? 140 : max(e, 14);
+  return {__builtin_bit_cast(float, (267 - e) << 23), __builtin_bit_cast(float, (e - 13) << 23)};
+}
+
 // A sum over the lanes up to each one, without shared memory.
 template <int CTRL, int ROWS>
 __device__ __forceinline__ double lanes_before(double x) {
@@ -271,7 +286,8 @@ __device__ __forceinline__ void attn_walk(const AttnArgs& a, int id, int blocks)
   __shared__ alignas(16) T sv[2][TC][VP];
   // scores, 16 steps by 32: those of the first 32 steps for all, those of the next for the last 32
   __shared__ alignas(16) T sp[2][WALK ? NP : 1][WALK ? PB : 1][16][PP];
-  __shared__ alignas(16) float shi[2][TC], slo[2][TC], ssince[2][TC], sleft[2][TC], slog[2][TC], sdiag[2][TC], sback[2][8], stotal[2], red[4][TC];
+  __shared__ alignas(16) float shi[2][TC], slo[2][TC], ssince[2][TC], sleft[2][TC], slog[2][TC], sdiag[2][TC], stotal[2], red[4][TC];
+  __shared__ float sback[2][WALK && M::Scaled ? PB : 1][16];   // what the scores of a block's steps were scaled by, back
   const int w = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
   const int t = int(threadIdx.x) & 255, lane = t & 63, q = lane & 15, g = lane >> 4;
   const int sub = a.sub ? a.sub : 1, parts = a.pieces * sub;   // (of a head; what is walked for its state)
@@ -497,8 +513,8 @@ __device__ __forceinline__ void attn_walk(const AttnArgs& a, int id, int blocks)
       }
       Scale sc{1.f, 1.f};
       if constexpr (M::Scaled) {
-        sc = wave_scale(most);
-        if (lane == 0) sback[at][block] = sc.back;
+        sc = lane_scale(most);
+        if (g == 0) sback[at][block][q] = sc.back;
       }
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
@@ -734,7 +750,7 @@ __device__ __forceinline__ void attn_walk(const AttnArgs& a, int id, int blocks)
         if (s == 0) y[i] *= since[i] * ss.back;
         if constexpr (M::Scaled) {
           const f32x4 c = mul_parts<T, NP>(fv[s], fp[m % 3], f32x4{0.f, 0.f, 0.f, 0.f});
-          const float back = sback[at][s ? i + 2 : i];
+          const float back = sback[at][s ? i + 2 : i][q];
 #pragma unroll
           for (int k = 0; k < 4; ++k) y[i][k] = __builtin_fmaf(c[k], back, y[i][k]);
         } else {

@@ -1,0 +1,36 @@
+"""Linear attention on the GPU with values of very unlike size side by side:
+steps, columns and entries of a state that do not depend on each other do not
+take each other's digits.  Bounds: attn_reference.walk, of each output's own
+terms; sizes are chosen so that no 16-bit output leaves its type."""
+import pytest
+import torch
+
+from tests import ssm_reference as ref
+from tests import test_gpu_ssm
+from tests.test_gpu_attn import attn_case, rounded, values
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def sentinel(monkeypatch):
+    """Outputs reach the thousands, where bf16 has every fourth number only and meets the usual -777 (-776) now and then:
+    a sentinel above them all, a number of every type."""
+    monkeypatch.setattr(test_gpu_ssm, "SENTINEL", -59904.0)
+
+
+def stored(t, dtype):
+    return {n: rounded(x, dtype if n in ("Q", "K", "V", "dY") else "f32") for n, x in t.items()}
+
+
+@pytest.mark.parametrize("dtype", ref.TYPES)
+@pytest.mark.parametrize("k,reverse", [(64, False), (64, True), (200, False)])
+def test_a_large_step(dtype, k, reverse):
+    """Scores of 64 * 9e8 * scale beside those of 8 * scale: of steps whose value is zero, and that no gradient enters by."""
+    b, s, h, v = 2, 130, 2, 40
+    t = values(dtype, b, s, h, 1, k, v)
+    for at in (12, 77, 125):
+        t["Q"][:, at] = t["K"][:, at] = 3e4
+        t["V"][:, at] = t["dY"][:, at] = 0
+    t["d_final_state"] *= 0.003
+    attn_case(dtype, b, s, h, 1, k, v, t=stored(t, dtype), scale=0.003, reverse=reverse)
