@@ -33,9 +33,9 @@
 // in parts: bf16 two for the scores and the state (2^-16 of each), three (2^-24)
 // for what is summed into the state or into the decays' gradient; f16 two (2^-22),
 // scaled by a power of two, since f16 has neither the state's range nor the
-// scores': each step's scores to their largest (one scale for a block of steps took
-// the digits of those beside a large one), the state and decayed v to a wave's.
-// f32 uses the f32 matrix cores.
+// scores': each step's scores to their largest, each column of the state and of the
+// decayed v to its own (one scale for a block of steps or for sixteen columns took
+// the digits of those beside a large one).  f32 uses the f32 matrix cores.
 //
 // A masked score is a zero, but a zero times a later step's infinity or NaN is
 // not; and an infinite value has no parts.  A wave whose chunk has an output that
@@ -180,29 +180,12 @@ __device__ __forceinline__ f32x4 mul_parts(const typename Mma<T>::Op& a, const P
   return c;
 }
 
-// The power of two that takes the largest magnitude of a wave's values, m, to
-// 2^13 to 2^14, and its inverse (1 for a zero, and for what is not finite).
+// The power of two that takes the largest magnitude, m, of the values of the four
+// lanes that share a place among sixteen to 2^13 to 2^14, and its inverse (1 for a
+// zero, and for what is not finite).
 struct Scale {
   float by, back;
 };
-__device__ __forceinline__ Scale wave_scale(float m) {
-  auto of = [&](auto CTRL) {
-    const float o = __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, m), decltype(CTRL)::value, 0xf, 0xf, true));
-    m = m > o ? m : o;
-  };
-  of(std::integral_constant<int, 0xb1>{});    // lane ^ 1
-  of(std::integral_constant<int, 0x4e>{});    // lane ^ 2
-  of(std::integral_constant<int, 0x141>{});   // the other half of eight lanes
-  of(std::integral_constant<int, 0x140>{});   // the other half of sixteen
-  int e = 0;
-#pragma unroll
-  for (int l = 0; l < 64; l += 16) e = max(e, __builtin_amdgcn_readlane(__builtin_bit_cast(int, m), l));
-  e >>= 23;
-  e = e == 0 || e >= 255 ? 140 : max(e, 14);
-  return {__builtin_bit_cast(float, (267 - e) << 23), __builtin_bit_cast(float, (e - 13) << 23)};
-}
-
-// The same for the values of the four lanes that share a place among sixteen.
 __device__ __forceinline__ Scale lane_scale(float m) {
   auto of = [&](auto p) {
     const float x = __builtin_bit_cast(float, uint32_t(p[0])), y = __builtin_bit_cast(float, uint32_t(p[1]));
@@ -693,14 +676,17 @@ __device__ __forceinline__ void attn_walk(const AttnArgs& a, int id, int blocks)
     if constexpr (WALK) {
 #pragma unroll
       for (int i = 0; i < IT; ++i) y[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-      Scale ss{1.f, 1.f};
+      Scale ss{1.f, 1.f};   // of this lane's column
+      float back[4];        // of the outputs' columns
       if constexpr (M::Scaled) {
         float most = 0.f;
 #pragma unroll
         for (int k = 0; k < 2 * KT; ++k)
 #pragma unroll
           for (int i = 0; i < 4; ++i) most = fmaxf(most, __builtin_fabsf(S[k][i]));
-        ss = wave_scale(most);
+        ss = lane_scale(most);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) back[i] = __shfl(ss.back, 4 * g + i, 16);
       }
       Op fa[2][IT];
       auto read_a = [&](int k) {
@@ -747,13 +733,13 @@ __device__ __forceinline__ void attn_walk(const AttnArgs& a, int id, int blocks)
         const int i = m < 2 ? m : (m - 2) / 2 + 2, s = m < 2 ? 0 : m & 1;
         if (m + 2 < BL) read_p(m + 2);
         asked();
-        if (s == 0) y[i] *= since[i] * ss.back;
         if constexpr (M::Scaled) {
           const f32x4 c = mul_parts<T, NP>(fv[s], fp[m % 3], f32x4{0.f, 0.f, 0.f, 0.f});
-          const float back = sback[at][s ? i + 2 : i][q];
+          const float by = sback[at][s ? i + 2 : i][q];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) y[i][k] = __builtin_fmaf(c[k], back, y[i][k]);
+          for (int k = 0; k < 4; ++k) y[i][k] = __builtin_fmaf(c[k], by, s == 0 ? y[i][k] * (since[i] * back[k]) : y[i][k]);
         } else {
+          if (s == 0) y[i] *= since[i];
           y[i] = mul_parts<T, NP>(fv[s], fp[m % 3], y[i]);
         }
       }
@@ -861,7 +847,7 @@ __device__ __forceinline__ void attn_walk(const AttnArgs& a, int id, int blocks)
         for (int s = 0; s < ST; ++s)
 #pragma unroll
           for (int i = 0; i < 8; ++i) most = fmaxf(most, __builtin_fabsf(value(s, i)));
-        sc = wave_scale(most);
+        sc = lane_scale(most);
       }
       auto value_parts = [&](int s) {
         float x[8];

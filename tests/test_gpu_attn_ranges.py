@@ -34,3 +34,21 @@ def test_a_large_step(dtype, k, reverse):
         t["V"][:, at] = t["dY"][:, at] = 0
     t["d_final_state"] *= 0.003
     attn_case(dtype, b, s, h, 1, k, v, t=stored(t, dtype), scale=0.003, reverse=reverse)
+
+
+@pytest.mark.parametrize("dtype", ref.TYPES)
+@pytest.mark.parametrize("which", ["values", "keys"])
+@pytest.mark.parametrize("k,v", [(32, 48), (48, 200)])
+def test_columns_of_unlike_size(dtype, which, k, v):
+    """Columns of the values, and keys: columns of the gradients' states."""
+    b, s, h = 2, 100, 2
+    t = values(dtype, b, s, h, 1, k, v)
+    size = torch.tensor([1e4, 1.0, 1e-2, 1e-3], dtype=torch.float64)
+    if which == "values":
+        t["V"] *= size.repeat(h * v // 4)
+        t["initial_state"] *= size.repeat(v // 4)
+    else:
+        t["K"] *= size.repeat(k // 4)
+        t["Q"] *= torch.tensor([1e-3, 1.0, 1e-2, 1.0], dtype=torch.float64).repeat(k // 4)
+    t["d_final_state"] *= 0.01
+    attn_case(dtype, b, s, h, 1, k, v, t=stored(t, dtype), scale=0.01)
