@@ -35,7 +35,10 @@
 // scaled by a power of two, since f16 has neither the state's range nor the
 // scores': each step's scores to their largest, each column of the state and of the
 // decayed v to its own (one scale for a block of steps or for sixteen columns took
-// the digits of those beside a large one).  f32 uses the f32 matrix cores.
+// the digits of those beside a large one), and what the first part leaves once more
+// by itself, so that the smaller values of a column keep theirs, too: 2^-22 of
+// each value down to 2^-28 of the largest, and 2^-50 of that below.  f32 uses the
+// f32 matrix cores.
 //
 // A masked score is a zero, but a zero times a later step's infinity or NaN is
 // not; and an infinite value has no parts.  A wave whose chunk has an output that
@@ -136,6 +139,7 @@ __device__ __forceinline__ typename Mma<T>::Op op_column(const T* base, int stri
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+constexpr float kLeft = 8192.f;   // f16: what is left of 2^14, 4 at most, fills the type's range, too
 __device__ __forceinline__ uint32_t take_pair(f32x2& x, bf16_t) {
   const uint32_t k = __builtin_bit_cast(uint32_t, __builtin_convertvector(x, bf16x2));
   x[0] -= __builtin_bit_cast(float, k << 16);
@@ -144,12 +148,13 @@ __device__ __forceinline__ uint32_t take_pair(f32x2& x, bf16_t) {
 }
 __device__ __forceinline__ uint32_t take_pair(f32x2& x, f16_t) {
   const f16x2 k = __builtin_convertvector(x, f16x2);
-  x[0] = __builtin_fmaf(float(k[0]), -1.f, x[0]);
-  x[1] = __builtin_fmaf(float(k[1]), -1.f, x[1]);
+  x[0] = __builtin_fmaf(float(k[0]), -1.f, x[0]) * kLeft;
+  x[1] = __builtin_fmaf(float(k[1]), -1.f, x[1]) * kLeft;
   return __builtin_bit_cast(uint32_t, k);
 }
 
-// N parts of eight values of 32 bits.
+// N parts of eight values of 32 bits (f16: the second times kLeft, which its
+// products are summed with apart).
 template <typename T, int N>
 struct Parts {
   typename Mma<T>::Op p[N];
@@ -177,6 +182,12 @@ template <typename T, int N>
 __device__ __forceinline__ f32x4 mul_parts(const typename Mma<T>::Op& a, const Parts<T, N>& b, f32x4 c) {
 #pragma unroll
   for (int n = N - 1; n >= 0; --n) c = Mma<T>::mul(a, b.p[n], c);
+  return c;
+}
+// The sum of products by first parts and that by second ones.
+__device__ __forceinline__ f32x4 with_left(f32x4 c, const f32x4& left) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) c[i] = __builtin_fmaf(left[i], 1.f / kLeft, c[i]);
   return c;
 }
 
@@ -676,6 +687,9 @@ __device__ __forceinline__ void attn_walk(const AttnArgs& a, int id, int blocks)
     if constexpr (WALK) {
 #pragma unroll
       for (int i = 0; i < IT; ++i) y[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+      f32x4 z[M::Scaled ? IT : 1];   // of second parts
+#pragma unroll
+      for (int i = 0; i < (M::Scaled ? IT : 1); ++i) z[i] = f32x4{0.f, 0.f, 0.f, 0.f};
       Scale ss{1.f, 1.f};   // of this lane's column
       float back[4];        // of the outputs' columns
       if constexpr (M::Scaled) {
@@ -723,7 +737,10 @@ __device__ __forceinline__ void attn_walk(const AttnArgs& a, int id, int blocks)
 #pragma unroll
         for (int m = NP - 1; m >= 0; --m)
 #pragma unroll
-          for (int i = 0; i < IT; ++i) y[i] = M::mul(fs.p[m], fa[k & 1][i], y[i]);
+          for (int i = 0; i < IT; ++i) {
+            f32x4& to = M::Scaled && m == 1 ? z[M::Scaled ? i : 0] : y[i];
+            to = M::mul(fs.p[m], fa[k & 1][i], to);
+          }
         if (k + 1 < KT) fs = state_parts(k + 1);
         if constexpr (sizeof(T) == 2) between_products<NP * IT, 3>();
         asked();
@@ -734,8 +751,10 @@ __device__ __forceinline__ void attn_walk(const AttnArgs& a, int id, int blocks)
         if (m + 2 < BL) read_p(m + 2);
         asked();
         if constexpr (M::Scaled) {
-          const f32x4 c = mul_parts<T, NP>(fv[s], fp[m % 3], f32x4{0.f, 0.f, 0.f, 0.f});
+          const f32x4 left = M::mul(fv[s], fp[m % 3].p[1], f32x4{0.f, 0.f, 0.f, 0.f});
+          const f32x4 c = with_left(M::mul(fv[s], fp[m % 3].p[0], f32x4{0.f, 0.f, 0.f, 0.f}), left);
           const float by = sback[at][s ? i + 2 : i][q];
+          if (s == 0) y[i] = with_left(y[i], z[i]);
 #pragma unroll
           for (int k = 0; k < 4; ++k) y[i][k] = __builtin_fmaf(c[k], by, s == 0 ? y[i][k] * (since[i] * back[k]) : y[i][k]);
         } else {
@@ -861,15 +880,20 @@ __device__ __forceinline__ void attn_walk(const AttnArgs& a, int id, int blocks)
       for (int k = 0; k < 2 * KT / J; ++k) {
         if (k + 1 < 2 * KT / J) read_b(k + 1);
         asked();
-        f32x4 c[J];
+        f32x4 c[J], z[M::Scaled ? J : 1];   // (second parts' apart)
 #pragma unroll
         for (int j = 0; j < J; ++j) c[j] = M::Scaled ? f32x4{0.f, 0.f, 0.f, 0.f} : S[J * k + j] * total;
+#pragma unroll
+        for (int j = 0; j < (M::Scaled ? J : 1); ++j) z[j] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int s = 0; s < ST; ++s) {
 #pragma unroll
           for (int m = NU - 1; m >= 0; --m)
 #pragma unroll
-            for (int j = 0; j < J; ++j) c[j] = M::mul(fb[k & 1][j][s], fx[s].p[m], c[j]);
+            for (int j = 0; j < J; ++j) {
+              f32x4& to = M::Scaled && m == 1 ? z[M::Scaled ? j : 0] : c[j];
+              to = M::mul(fb[k & 1][j][s], fx[s].p[m], to);
+            }
           if (ST == 2 && s == 0 && k == 0) {
             fx[ST - 1] = value_parts(ST - 1);
             if constexpr (sizeof(T) == 2) between_products<NU * J, 4>();
@@ -879,6 +903,7 @@ __device__ __forceinline__ void attn_walk(const AttnArgs& a, int id, int blocks)
 #pragma unroll
         for (int j = 0; j < J; ++j) {
           if constexpr (M::Scaled) {
+            c[j] = with_left(c[j], z[j]);
 #pragma unroll
             for (int i = 0; i < 4; ++i) S[J * k + j][i] = __builtin_fmaf(S[J * k + j][i], total, c[j][i] * sc.back);
           } else {

@@ -52,3 +52,30 @@ def test_columns_of_unlike_size(dtype, which, k, v):
         t["Q"] *= torch.tensor([1e-3, 1.0, 1e-2, 1.0], dtype=torch.float64).repeat(k // 4)
     t["d_final_state"] *= 0.01
     attn_case(dtype, b, s, h, 1, k, v, t=stored(t, dtype), scale=0.01)
+
+
+@pytest.mark.parametrize("dtype", ref.TYPES)
+def test_a_large_state_that_is_not_asked_for(dtype):
+    """One key's 1e10 in two columns, which no query and no gradient meets, beside the ones of the other keys there."""
+    b, s, h, k, v = 2, 100, 2, 32, 48
+    t = values(dtype, b, s, h, 1, k, v)
+    t["initial_state"][..., 3, 5] = t["initial_state"][..., 4, 6] = 1e10
+    t["Q"][..., 3:5] = 0
+    t["dY"].view(b, s, h, v)[..., 5:7] = 0
+    attn_case(dtype, b, s, h, 1, k, v, t=stored(t, dtype))
+
+
+@pytest.mark.parametrize("dtype", ref.TYPES)
+@pytest.mark.parametrize("reverse", [False, True])
+def test_values_of_unlike_size_under_keys_of_their_own(dtype, reverse):
+    """Steps of 1e4, 1e-3 and 1, each under a key that no step of another size has (33 keys, sizes three by three)."""
+    b, s, h, k, v = 2, 130, 2, 33, 24
+    t = values(dtype, b, s, h, h, k, v)
+    at = torch.arange(s)
+    t["K"] = torch.nn.functional.one_hot(at % k, k).double().repeat(b, 1, h)
+    t["Q"] = torch.nn.functional.one_hot(7 * at % k, k).double().repeat(b, 1, h)
+    t["V"] *= torch.tensor([1e4, 1e-3, 1.0], dtype=torch.float64)[at % 3][:, None]
+    t["dY"] *= 0.05
+    t["initial_state"] *= 1e-3
+    t["d_final_state"] *= 0.05
+    attn_case(dtype, b, s, h, h, k, v, t=stored(t, dtype), scale=0.25, reverse=reverse)
