@@ -70,7 +70,8 @@ int attn_sub(const AttnPlan& f, int64_t blocks) {
 
 // Whether a gradient's walks go side by side in one launch: those that do not fill
 // the chip.  A rule on the sizes alone: an output is the same whichever others are
-// asked for.  (5 x 80 steps, 4 heads of 24 x 30, f32: 22 us, one after another 51.)
+// asked for, but for the decays' gradient, which has its own pieces and its own way
+// with a step's own part.  (5 x 80 steps, 4 heads of 24 x 30, f32: 22 us, one after another 51.)
 bool attn_side_by_side(const rnn_attn& p, const AttnPlan& plan) {
   return !p.tokens && p.d.batch * p.d.heads * (2 * p.key_cols + p.value_cols) * plan.pieces <= 256;
 }
@@ -135,11 +136,13 @@ hipError_t attn_walk(const rnn_attn& p, const AttnArgs& a, bool local, hipStream
                                       : launch_attn_chunks_bf16(a, local, s);
 }
 
-// A few walks in one launch.
+// A few walks in one launch, as wide as any of the problem's: width decides the
+// chunks, and so the bits of an output, whichever others go along.
 hipError_t attn_walks(const rnn_attn& p, const AttnArgs* w, int n, hipStream_t s) {
-  return p.d.dtype == RNN_DTYPE_F32   ? launch_attn_walks_f32(w, n, s)
-         : p.d.dtype == RNN_DTYPE_F16 ? launch_attn_walks_f16(w, n, s)
-                                      : launch_attn_walks_bf16(w, n, s);
+  const int K = int(std::max(p.d.key, p.d.value));
+  return p.d.dtype == RNN_DTYPE_F32   ? launch_attn_walks_f32(w, n, K, s)
+         : p.d.dtype == RNN_DTYPE_F16 ? launch_attn_walks_f16(w, n, K, s)
+                                      : launch_attn_walks_bf16(w, n, K, s);
 }
 
 int attn_launch(const char* what, hipError_t e) {

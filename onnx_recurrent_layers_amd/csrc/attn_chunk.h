@@ -1035,15 +1035,13 @@ hipError_t attn_walks_of(const AttnWalks& w, int K, hipStream_t s) {
 }
 
 template <typename T>
-hipError_t attn_walks(const AttnArgs* w, int n, hipStream_t s) {
+hipError_t attn_walks(const AttnArgs* w, int n, int K, hipStream_t s) {
   AttnWalks all{};
   bool vec = true;
-  int K = 0;
   for (int k = 0; k < n; ++k) {
     const AttnArgs& a = all.w[k] = w[k];
     all.first[k + 1] = all.first[k] + a.geo.B * a.H * ((a.V + kAttnCols - 1) / kAttnCols) * a.pieces;
     vec = vec && attn_whole<T>(a, false);
-    K = std::max(K, a.K);
   }
   for (int k = n; k < 3; ++k) all.first[k + 1] = all.first[k];
   return vec ? attn_walks_of<T, true>(all, K, s) : attn_walks_of<T, false>(all, K, s);

@@ -110,11 +110,11 @@ constexpr int kAttnSteps = 4, kAttnManySteps = 8;   // steps up to which a seque
 hipError_t launch_attn_steps(const AttnArgs& a, int dtype, hipStream_t s);
 // (one definition a type: k_attn_f32.hip, k_attn_f16.hip, k_attn_bf16.hip)
 hipError_t launch_attn_chunks_f32(const AttnArgs& a, bool local, hipStream_t s);
-hipError_t launch_attn_walks_f32(const AttnArgs* w, int n, hipStream_t s);   // (n up to 3)
+hipError_t launch_attn_walks_f32(const AttnArgs* w, int n, int K, hipStream_t s);   // (n up to 3, K the most of any)
 hipError_t launch_attn_chunks_f16(const AttnArgs& a, bool local, hipStream_t s);
-hipError_t launch_attn_walks_f16(const AttnArgs* w, int n, hipStream_t s);   // (n up to 3)
+hipError_t launch_attn_walks_f16(const AttnArgs* w, int n, int K, hipStream_t s);   // (n up to 3, K the most of any)
 hipError_t launch_attn_chunks_bf16(const AttnArgs& a, bool local, hipStream_t s);
-hipError_t launch_attn_walks_bf16(const AttnArgs* w, int n, hipStream_t s);   // (n up to 3)
+hipError_t launch_attn_walks_bf16(const AttnArgs* w, int n, int K, hipStream_t s);   // (n up to 3, K the most of any)
 hipError_t launch_attn_join(const AttnJoinArgs& a, hipStream_t s);
 hipError_t launch_attn_decay(const AttnDecayArgs& a, hipStream_t s);
 hipError_t launch_head_sum(const HeadSumArgs& a, int dtype, hipStream_t s);

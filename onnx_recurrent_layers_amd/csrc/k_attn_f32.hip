@@ -4,6 +4,6 @@
 namespace rnnhip {
 
 hipError_t launch_attn_chunks_f32(const AttnArgs& a, bool local, hipStream_t s) { return attn_chunks<float>(a, local, s); }
-hipError_t launch_attn_walks_f32(const AttnArgs* w, int n, hipStream_t s) { return attn_walks<float>(w, n, s); }
+hipError_t launch_attn_walks_f32(const AttnArgs* w, int n, int K, hipStream_t s) { return attn_walks<float>(w, n, K, s); }
 
 }  // namespace rnnhip

@@ -6,6 +6,7 @@ import torch
 import onnx_recurrent_layers_amd as rl
 from tests import ssm_reference as ref
 from tests.gpu_harness import SENTINEL
+from tests.test_gpu_attn import types, values
 
 pytestmark = pytest.mark.gpu
 
@@ -26,3 +27,30 @@ def test_empty_batch(dtype, layout, seq):
     op.backward({**e, "dQ": torch.empty_like(e["Q"]), "dV": torch.empty_like(e["V"]), "d_decay": dd.fill_(SENTINEL)})
     torch.cuda.synchronize()
     assert (dd == 0).all()
+
+
+@pytest.mark.parametrize("dtype,k,v", [("f32", 32, 128), ("f32", 128, 32), ("f32", 64, 128), ("f32", 200, 128), ("f16", 64, 200), ("f16", 200, 64),
+                                       ("bf16", 64, 200), ("bf16", 200, 128)])
+@pytest.mark.parametrize("s", [100, 600])
+def test_each_gradient_alone(dtype, k, v, s):
+    """Walks side by side of keys and values so unlike that each by itself would have chunks of its own length: each
+    output alone is bit for bit that of all together, and of all with one that lies off any alignment."""
+    b, h = 2, 4
+    to = types(dtype)
+    d = {n: x.to(to[n]).cuda() for n, x in values(dtype, b, s, h, 2, k, v).items()}
+    op = rl.LinearAttention(dtype=dtype, seq=s, batch=b, heads=h, groups=2, key=k, value=v)
+    shapes = {"dV": (b, s, h * v), "dQ": (b, s, 2 * k), "dK": (b, s, 2 * k), "dG": (b, s, h), "d_decay": (h,), "d_initial_state": (b, h, k, v)}
+    for names in (("dQ", "dK", "dV", "d_initial_state"), ("dV", "dG", "d_decay", "d_initial_state")):
+        full = {n: torch.empty(shapes[n], dtype=to[n], device="cuda") for n in names}
+        op.backward({**d, **full})
+        odd = {n: torch.empty_like(x) for n, x in full.items()}
+        last = "dQ" if "dQ" in full else "dV"
+        flat = torch.empty(odd[last].numel() + 1, dtype=to[last], device="cuda")
+        odd[last] = flat[1:].view(shapes[last])
+        op.backward({**d, **odd})
+        for n in names:
+            one = torch.empty_like(full[n])
+            op.backward({**d, n: one})
+            torch.cuda.synchronize()
+            assert torch.equal(one, full[n]), n
+            assert torch.equal(odd[n], full[n]), n
