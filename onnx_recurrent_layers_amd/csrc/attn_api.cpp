@@ -76,6 +76,15 @@ bool attn_side_by_side(const rnn_attn& p, const AttnPlan& plan) {
   return !p.tokens && p.d.batch * p.d.heads * (2 * p.key_cols + p.value_cols) * plan.pieces <= 256;
 }
 
+// Whether the launches of walks of `cols` workgroups a head and piece fit: the walks
+// themselves (256 threads a workgroup step after step, 512 over chunks) and, of more
+// pieces than one, their join.
+bool attn_fits(const rnn_attn& p, const AttnPlan& plan, int cols) {
+  const int64_t heads = p.d.batch * p.d.heads;   // (at most 2^54)
+  return heads * cols <= kMaxThreads / (p.tokens ? 256 : 512) / plan.pieces &&
+         (plan.pieces == 1 || heads <= kMaxThreads / 256 / ceil_div(p.d.key * p.d.value, 256));
+}
+
 // The scratch regions of the two directions, in the order that they are taken.
 struct AttnScratch {
   size_t starts, totals, back_starts, back_totals, rows, cols, ends, decay, part[2];
@@ -208,8 +217,7 @@ extern "C" int rnn_attn_create(const rnn_attn_desc* desc, rnn_attn** out) {
   if (!p.tokens && heads * (2 * p.key_cols + p.value_cols) <= 256 && d.seq <= (d.dtype == RNN_DTYPE_F32 ? 256 : 1024) &&
       !std::getenv("RNN_ATTN_PIECE"))
     p.b = p.bd = {int(ceil_div(d.seq, 64) * 64), 1, 0};
-  const int64_t pieces = std::max(std::max(p.f.pieces, p.b.pieces), p.bd.pieces);
-  if (bytes_of({blocks, pieces, 512}) < 0 || blocks * pieces * 512 > kMaxThreads || heads * ceil_div(d.key * d.value, 256) * 256 > kMaxThreads)
+  if (!attn_fits(p, p.f, p.value_cols))   // (the gradient's launches are seen to by its call)
     return fail(RNN_ERR_UNSUPPORTED, kAttn, "batch x heads: too large for one launch");
   AttnScratch at;
   if (!attn_scratch(p, false, &at, &p.forward_bytes) || !attn_scratch(p, true, &at, &p.backward_bytes))
@@ -288,6 +296,9 @@ extern "C" int rnn_attn_encode_backward(const rnn_attn* attn, const rnn_attn_ope
   if (t.status != RNN_OK) return t.status;
   const bool decays = dG.p || ddecay;
   if (!dQ.p && !dK.p && !dV.p && !decays && !dinit) return RNN_OK;
+  const AttnPlan& plan = decays ? p.bd : p.b;
+  if (!attn_fits(p, plan, std::max(p.key_cols, p.value_cols)))
+    return fail(RNN_ERR_UNSUPPORTED, kAttn, "batch x heads: too large for one launch of the gradient");
   if (int rc = check_scratch(kAttn, scratch, p.backward_bytes)) return rc;
   AttnScratch at;
   size_t total;
@@ -300,7 +311,6 @@ extern "C" int rnn_attn_encode_backward(const rnn_attn* attn, const rnn_attn_ope
     return attn_launch("sums", launch_colsum(cs, s));
   };
   if (d.batch == 0) return ddecay ? sum_decay(0) : int(RNN_OK);   // (no walk, only a sum of nothing)
-  const AttnPlan& plan = decays ? p.bd : p.b;
   a.piece = plan.piece, a.pieces = plan.pieces;
   // forward in time from the initial state, back from the final one's gradient
   AttnArgs fore = a, back = a;

@@ -54,3 +54,31 @@ def test_each_gradient_alone(dtype, k, v, s):
             torch.cuda.synchronize()
             assert torch.equal(one, full[n]), n
             assert torch.equal(odd[n], full[n]), n
+
+
+def test_tokens_of_many_rows():
+    """A token of each of 16384 rows, 16 heads of 128 x 128: 2^32 elements of state, 16 GiB, updated in place; rows here and there."""
+    b, h, k, v = 16384, 16, 128, 128
+    gen = torch.Generator("cuda").manual_seed(3)
+
+    def new(*shape):
+        return torch.randn(*shape, generator=gen, device="cuda").to(torch.bfloat16)
+
+    q, key, val = new(b, 1, h * k), new(b, 1, h * k), new(b, 1, h * v)
+    decay = -torch.rand(h, generator=gen, device="cuda")
+    state = torch.empty(b, h, k, v, device="cuda")
+    state.normal_(generator=gen)
+    at = [0, 1, 8191, 8192, 12345, b - 1]
+    before = state[at].double()
+    y = torch.empty_like(val)
+    op = rl.LinearAttention(dtype="bf16", seq=1, batch=b, heads=h, key=k, value=v, scale=0.1)
+    op.encode({"Q": q, "K": key, "V": val, "decay": decay, "initial_state": state, "final_state": state, "Y": y})
+    torch.cuda.synchronize()
+    qs, ks, vs = (t[at].double().view(len(at), h, -1) for t in (q, key, val))
+    new_state = before * decay.double().exp()[:, None, None] + ks[..., None] * vs[..., None, :]
+    out = 0.1 * (qs[..., None] * new_state).sum(-2)
+    # (a product by a decay, its two roundings and its argument's, one by a value and a sum; sums of 128 and a scale)
+    terms = before.abs() + ks.abs()[..., None] * vs.abs()[..., None, :]
+    assert ((state[at].double() - new_state).abs() <= 6 * 2.0 ** -24 * terms).all()
+    room = 2.0 ** -8 * out.abs() + 140 * 2.0 ** -24 * 0.1 * (qs.abs()[..., None] * terms).sum(-2)
+    assert ((y[at].double().view(len(at), h, v) - out).abs() <= room).all()
