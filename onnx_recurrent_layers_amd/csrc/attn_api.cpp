@@ -531,7 +531,7 @@ extern "C" int rnn_rotary_encode_backward(const rnn_rotary* rotary, const rnn_ro
   const rnn_rotary_gradients& g = *gradients;
   Tensors t(kRotary);
   RotaryArgs a{};
-  const bool keys = d.k_heads > 0 && (g.dK_out.ptr || g.dK.ptr || g.dk_scale.ptr);
+  const bool keys = d.k_heads > 0 && (g.dK.ptr || g.dk_scale.ptr);
   const bool any = d.rows > 0;
   rotary_inputs(p, *operands, keys, t, a);
   a.dy[0] = t.rows(g.dQ_out, p.es, d.q_heads * d.size, d.rows, "dQ_out", any);
