@@ -516,7 +516,8 @@ int rnn_norm_encode_backward(const rnn_norm* norm, const rnn_norm_operands* oper
  *   Y_s[h]      = scale * Q_s[g]^T S_s[h]
  * for head h in group g = h / (heads / groups).  G + decay is a step's log
  * decay: above 0 it acts as 0 (and has no gradient there), at -infinity a step
- * forgets all before it.  Rows, steps, lengths and carried states are those of
+ * forgets all before it (but a state that is infinite or NaN: zero times it is
+ * NaN).  Rows, steps, lengths and carried states are those of
  * the operators above; S_{-1} is initial_state. */
 typedef struct {
   int32_t dtype;      /* rnn_dtype of Q, K, V, Y and their gradients (G, the states and the rest are f32) */
@@ -546,7 +547,8 @@ typedef struct {
 } rnn_attn_operands;
 
 /* Gradients; states are computed again from the inputs.  dG and d_decay may be
- * asked for without G and decay. */
+ * asked for without G and decay; an infinity or NaN in K or V spoils them for the
+ * whole row and head, earlier steps too. */
 typedef struct {
   rnn_rows dY;                 /* [heads * value] a row            required */
   rnn_tensor d_final_state;    /* as initial_state                 optional (zeros) */

@@ -23,11 +23,12 @@
 // product and the fourth) are read from shared memory by the transposing reads.
 //
 // The state is in f32 and never leaves the registers inside a piece of the time
-// axis; what bounds a chunk (64 steps, heads of 128 x 128, bf16: 3.1 us, 8 x 1024
-// steps of 16 heads 51 us) is the four waves' own instructions, most of them the
-// splitting of 32-bit values below, with the reads of shared memory between (busy 42
-// clocks of 100, the matrix units 26).  All eight waves doing both with one chunk of
-// rows ahead took 97 us.
+// axis.  No unit is busy for the whole of a chunk's time (64 steps, heads of 128 x
+// 128, bf16: 3.1 us, 8 x 1024 steps of 16 heads 51 us): shared memory 42 clocks of
+// 100, vector instructions, most of them the splitting of 32-bit values below, 40,
+// the matrix units 26.  In the rest the waves, one of each role a SIMD, wait for what
+// they read and for each other at the barriers.  All eight waves doing both with one
+// chunk of rows ahead took 97 us.
 //
 // Values of 32 bits (scores, state, decayed v) enter a product of 16-bit operands
 // in parts: bf16 two for the scores and the state (2^-16 of each), three (2^-24)

@@ -16,12 +16,14 @@
 //
 // The grid is at most 512 workgroups, two a CU, that go on over the rows: scales
 // are read and the scales' gradients summed once a workgroup, and more of them
-// cost more than they hide (8192 rows of 32 heads of 128, f16: forward 31.7 us
-// with 512, 33.1 with 768, 34.9 with 1024, 40.1 with one for every four rows;
-// gradient 50.3, 53.2, 62.1, - ; with 256 46.2 and 60.7).  Heads that lie on all
-// lanes with every element turned take a kernel without conditions in the lanes
-// (ALL; else the same call 35.8 and 72.5).  A copy of the same bytes (134 and 203
-// MB) takes 27 and 43.  Not kept: loads of the next heads under way while a wave
+// cost more than they hide (8192 rows of 32 heads of 128, f16, the same inputs again
+// and again: forward 31.7 us with 512, 33.1 with 768, 34.9 with 1024, 40.1 with one
+// for every four rows; gradient 50.3, 53.2, 62.1, - ; with 256 46.2 and 60.7).  Heads
+// that lie on all lanes with every element turned take a kernel without conditions in
+// the lanes (ALL; else the same call 35.8 and 72.5).  Over inputs that change the
+// forward call takes 32.2 and the gradient's, bf16, 52.9: its kernel 48.5, the scales'
+// sums, a launch of their own, the rest.  A copy of the same bytes (134 and 203 MB)
+// takes 27 and 43.  Not kept: loads of the next heads under way while a wave
 // takes these (33.2), and of the next row (32.1 to 46, the registers of 151).
 #include "attn_ops.h"
 #include "seq_device.h"
